@@ -21,7 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_ep.so")
-SOURCES = [os.path.join(CSRC, "moe_ep.hip"), os.path.join(CSRC, "moe_kernels.hip")]
+SOURCES = [os.path.join(CSRC, name) for name in (
+    "moe_ep.hip", "moe_kernels.hip", "moe_ops.hip", "token_ops.hip", "expert_product.hip",
+    "few_token.hip")]
 ARCH = "gfx950"
 
 

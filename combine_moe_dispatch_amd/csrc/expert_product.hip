@@ -1,0 +1,585 @@
+// Product of e4m3 rows, grouped by expert, with block-scaled e4m3 weights.
+//
+//   y[r][n] = sum over blocks b of 128 of  xs[r][b] * ws[e][n/128][b] * (x_b[r] . w_b[e][n])
+//
+// for row r of expert e (rows offsets[e] .. offsets[e+1]).  The products of a
+// block (or of half a block) start from zero in fp32; the scales join them to
+// the running sums, acc = fma(product, xs*ws, acc).
+//
+// Two kinds of arithmetic for the block sums:
+//  - moe_expert_matmul, whose output is bf16, uses the e4m3 matrix
+//    instruction (16x16x128, one block per instruction).  It aligns a block's
+//    products to the largest before adding them: measured over random codes a
+//    block sum is off by 2^-13.5 of its largest product (rms; 2^-11.2 at
+//    worst), below the bf16 rounding that follows (2^-9 of the result, rms
+//    error against 64 bits 1.7e-3 with either kind).  Across blocks the sums
+//    are fp32.
+//  - moe_expert_gate_up, whose scales are fp32, converts the codes to fp16
+//    (exact, two codes per vector instruction) for the fp16 matrix
+//    instruction, whose sums are off by 2^-23: half the matrix rate, and the
+//    conversions take most of the vector unit's.
+//
+// Weights take the matrix instruction's row operand and the token rows its
+// column operand: a lane then holds outputs of ONE token, so its scale
+// product is one number, and runs of four consecutive n, an 8-byte store.
+//
+// gate_up runs the same loop with 128 gate rows and the matching 128 up rows
+// in one tile; its epilogue forms silu(gate) * up, shares each token's largest
+// magnitude over the block of 128 and writes codes and scale, so the fp32
+// intermediate never leaves the registers.
+#include <algorithm>
+#include <type_traits>
+
+#include "moe_ops.h"
+#include "ops_common.h"
+
+namespace moe {
+namespace ops {
+namespace {
+
+// One tile: BM token rows by BN weight rows, WM x WN waves, S stages of the
+// LDS ring.  EIGHT: the e4m3 matrix instruction, else the codes go through
+// fp16.  SUB x SUB outputs per matrix instruction.
+template <int BM_, int BN_, int WM_, int WN_, int S_, bool EIGHT_, int SUB_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, SUB = SUB_;
+    static constexpr bool EIGHT = EIGHT_;
+    static constexpr int WAVES = WM * WN;
+    static constexpr int THREADS = WAVES * WAVE;
+    static constexpr int TM = BM / WM, TN = BN / WN;     // a wave's share
+    static constexpr int MT = TM / SUB, NT = TN / SUB;
+    static constexpr int GROUPS = WAVE / SUB;            // lanes sharing a row of an operand
+    static constexpr int PIECES = EIGHT ? 2 : 1;         // 16-byte pieces converted at a time
+    static constexpr int STEPS = EIGHT ? 1 : 2;          // matrix instructions they make
+    static constexpr int ROUNDS = 8 / GROUPS / PIECES;   // times that makes a block
+    static constexpr int OUTS = SUB * SUB / WAVE;        // outputs per lane
+    // vector instructions beside each matrix instruction: a round's share of
+    // the joins and the next operand's conversions, spread evenly
+    static constexpr int JOINS = MT * OUTS / ROUNDS;
+    static constexpr int BESIDE = (JOINS + (EIGHT ? 0 : 8)) / (MT * STEPS);
+    static_assert(!EIGHT || SUB == 16, "the e4m3 instruction takes a whole block of 16 rows");
+
+    static constexpr int W_BYTES = BN * SCALE_BLOCK, X_BYTES = BM * SCALE_BLOCK;
+    static constexpr int STAGE = W_BYTES + X_BYTES;
+    // loads of one stage that each wave issues (1 KB each)
+    static constexpr int W_LOADS = W_BYTES / 1024 / WAVES;
+    static constexpr int X_LOADS_ALL = X_BYTES / 1024;
+    static constexpr int X_LOADS = (X_LOADS_ALL + WAVES - 1) / WAVES;
+    static constexpr int LOADS = W_LOADS + X_LOADS;
+    // row scales come SC_STEPS blocks at a time, 8 rows by 8 blocks per load
+    static constexpr int SC_STEPS = 8;
+    static constexpr int SC_BYTES = BM * SC_STEPS * 4;
+    static constexpr int SC_LOADS_ALL = SC_BYTES / 256;
+    static constexpr int SC_LOADS = (SC_LOADS_ALL + WAVES - 1) / WAVES;
+    static constexpr int RING = S * STAGE + 2 * SC_BYTES;
+    static_assert(W_BYTES % (1024 * WAVES) == 0, "weight rows split evenly over the waves");
+    static_assert(S <= SC_STEPS, "a scale buffer is free when its next turn is loaded");
+};
+
+typedef const __attribute__((address_space(1))) void gvoid;
+typedef __attribute__((address_space(3))) void lvoid;
+
+__device__ inline void load_lds16(const uint8_t* g, uint8_t* l)
+{
+    __builtin_amdgcn_global_load_lds((gvoid*)g, (lvoid*)l, 16, 0, 0);
+}
+
+__device__ inline void load_lds4(const float* g, uint8_t* l)
+{
+    __builtin_amdgcn_global_load_lds((gvoid*)g, (lvoid*)l, 4, 0, 0);
+}
+
+// Everything this wave loaded but its last n loads has arrived in LDS, its own
+// LDS reads are done, and so it is with every wave of the workgroup.
+template <int N>
+__device__ inline void wait_loads_and_meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int SUB>
+struct Outs {
+    typedef v4f type;
+};
+template <>
+struct Outs<32> {
+    typedef v16f type;
+};
+
+// PIECES pieces of an operand's row as the matrix instructions take them.
+template <class C, bool EIGHT = C::EIGHT>
+struct Operand {
+    v8h f[C::STEPS];
+    __device__ inline void from(const v4u (&raw)[C::PIECES])
+    {
+        f[0] = e4m3_to_f16(raw[0].x, raw[0].y);
+        f[1] = e4m3_to_f16(raw[0].z, raw[0].w);
+    }
+};
+template <class C>
+struct Operand<C, true> {
+    v8i f[1];
+    __device__ inline void from(const v4u (&r)[C::PIECES])
+    {
+        f[0] = v8i{(int)r[0].x, (int)r[0].y, (int)r[0].z, (int)r[0].w,
+                   (int)r[1].x, (int)r[1].y, (int)r[1].z, (int)r[1].w};
+    }
+};
+
+__device__ inline v4f product_step(v8i a, v8i b, v4f c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+__device__ inline v4f product_step(v8h a, v8h b, v4f c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ inline v16f product_step(v8h a, v8h b, v16f c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// 16-byte piece c of row r lies at place c ^ swizzle(r) of the row's 128
+// bytes, so that the 16 rows a fragment reads at once spread over the banks.
+__device__ inline int swizzle(int r) { return (r >> 1) & 7; }
+
+struct Place {
+    int e, m0, rows;          // expert, first row of the tile, rows of the tile (> 0)
+    int n_tile;
+};
+
+// Tile t of the launch: experts in order, each expert's tiles in groups of up
+// to 8 row tiles, row tiles fastest inside a group.  Every wave finds it for
+// itself: lane l holds experts [l*per, (l+1)*per).
+template <int BM>
+__device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int64_t rows_max, int n_tiles,
+                                 Place& out)
+{
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int per = (E + WAVE - 1) / WAVE;
+    const int rmax = (int)rows_max;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
+        if (e < E) {
+            const int a = min(max(offsets[e], 0), rmax), b = min(max(offsets[e + 1], 0), rmax);
+            mine += b > a ? (b - a + BM - 1) / BM : 0;
+        }
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < WAVE; d <<= 1) {
+        const int o = __shfl_up(incl, d, WAVE);
+        if (lane >= d)
+            incl += o;
+    }
+    const int total = __builtin_amdgcn_readlane(incl, WAVE - 1);
+    const int64_t tiles = (int64_t)total * n_tiles;
+    // consecutive workgroups go to the 8 XCDs in turn: each XCD takes one
+    // contiguous run of tiles, so that the tiles sharing weights share its L2
+    const int64_t per_xcd = (tiles + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t at = id >> 3;
+    const int64_t t = (id & 7) * per_xcd + at;
+    if (at >= per_xcd || t >= tiles)
+        return false;
+    // the lane whose experts hold the tile
+    const uint64_t below = __ballot((int64_t)incl * n_tiles <= t);
+    const int src = __popcll(below);                   // lanes whose experts end before t
+    int first = __builtin_amdgcn_readlane(incl - mine, src);
+    for (int i = 0; i < per; ++i) {
+        const int e = src * per + i;
+        if (e >= E)
+            return false;
+        const int a = min(max(offsets[e], 0), rmax), b = min(max(offsets[e + 1], 0), rmax);
+        const int m_tiles = b > a ? (b - a + BM - 1) / BM : 0;
+        const int64_t u = t - (int64_t)first * n_tiles;
+        if (u < (int64_t)m_tiles * n_tiles) {
+            constexpr int GROUP = 8;
+            const int per_group = GROUP * n_tiles;
+            const int g = (int)(u / per_group);
+            const int in = (int)(u - (int64_t)g * per_group);
+            const int gm = min(GROUP, m_tiles - g * GROUP);
+            const int mt = g * GROUP + in % gm;
+            out.e = e;
+            out.m0 = a + mt * BM;
+            out.rows = min(BM, b - out.m0);
+            out.n_tile = in / gm;
+            return true;
+        }
+        first += m_tiles;
+    }
+    return false;
+}
+
+template <class C, bool GATE_UP>
+__global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const ExpertProduct p, int n_tiles)
+{
+    extern __shared__ __align__(1024) uint8_t lds[];
+    Place at;
+    if (!find_tile<C::BM>(p.offsets, p.E, p.rows, n_tiles, at))
+        return;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    const int KB = p.k / SCALE_BLOCK;
+    const int F = p.n / 2;
+    const int nb = (p.n + SCALE_BLOCK - 1) / SCALE_BLOCK;
+
+    // Weight rows of this tile start at wbase (gate_up: gate rows at wbase, up
+    // rows at wbase_up).  A lane's 16-byte pieces lie at 32-bit offsets from
+    // there, rows clamped to the last valid one (what a clamped row computes
+    // is never stored).
+    const int n0 = at.n_tile * (GATE_UP ? C::BN / 2 : C::BN);
+    const uint8_t* wbase = p.w + ((int64_t)at.e * p.n + n0) * p.k;
+    const uint8_t* wbase_up = wbase + (int64_t)F * p.k;
+    const uint8_t* xbase = p.x + (int64_t)at.m0 * p.k;
+    const float* sbase = p.xs + (int64_t)at.m0 * KB;
+    const int sub = lane >> 3;
+    uint32_t woff[C::W_LOADS], xoff[C::X_LOADS];
+#pragma unroll
+    for (int i = 0; i < C::W_LOADS; ++i) {
+        const int r = (i * C::WAVES + wave) * 8 + sub;
+        const int n = GATE_UP ? r % (C::BN / 2) : min(r, p.n - 1 - n0);
+        woff[i] = (uint32_t)n * p.k + (((lane & 7) ^ swizzle(r)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < C::X_LOADS; ++i) {
+        const int r = ((i * C::WAVES + wave) % C::X_LOADS_ALL) * 8 + sub;
+        xoff[i] = (uint32_t)min(r, at.rows - 1) * p.k + (((lane & 7) ^ swizzle(r)) << 4);
+    }
+    // row scales: lane (k, row) = (lane / 8, lane % 8) of an 8 x 8 load, a line
+    // of eight scales per row (scales of one block for 64 rows, a load per
+    // block, cost a quarter of the whole load path: 64 lines each)
+    uint32_t soff[C::SC_LOADS];
+#pragma unroll
+    for (int i = 0; i < C::SC_LOADS; ++i)
+        soff[i] = (uint32_t)min(((i * C::WAVES + wave) % C::SC_LOADS_ALL) * 8 + (lane & 7), at.rows - 1) * KB;
+    uint8_t* const sc_lds = lds + C::S * C::STAGE;
+
+    // the row scales of blocks kb .. kb+7
+    auto issue_scales = [&](int kb) {
+        const int k = min(kb + (lane >> 3), KB - 1);
+        uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES;
+#pragma unroll
+        for (int i = 0; i < C::SC_LOADS; ++i)
+            load_lds4(sbase + soff[i] + k, sc + ((i * C::WAVES + wave) % C::SC_LOADS_ALL) * 256);
+    };
+    auto issue = [&](int kb, int slot) {
+        uint8_t* st = lds + slot * C::STAGE;
+        const int k0 = kb * SCALE_BLOCK;
+#pragma unroll
+        for (int i = 0; i < C::W_LOADS; ++i) {
+            const bool up = GATE_UP && (i * C::WAVES + wave) * 8 >= C::BN / 2;
+            load_lds16((up ? wbase_up : wbase) + k0 + woff[i], st + (i * C::WAVES + wave) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < C::X_LOADS; ++i)
+            load_lds16(xbase + k0 + xoff[i], st + C::W_BYTES + ((i * C::WAVES + wave) % C::X_LOADS_ALL) * 1024);
+    };
+
+    // The tile's weight scales, [2][KB + 1] (two blocks of 128 columns; gate_up:
+    // the gate block and the up block), wait in LDS behind the ring: a load of
+    // them inside the loop would wait for every stage in flight.
+    float* wsc = (float*)(lds + C::RING);
+    {
+        const int b0 = n0 / SCALE_BLOCK;
+        const int b1 = GATE_UP ? F / SCALE_BLOCK + b0 : min(b0 + 1, nb - 1);
+        const float* s0 = p.ws + ((int64_t)at.e * nb + b0) * KB;
+        const float* s1 = p.ws + ((int64_t)at.e * nb + b1) * KB;
+        for (int i = threadIdx.x; i < KB; i += C::THREADS) {
+            wsc[i] = s0[i];
+            wsc[KB + 1 + i] = s1[i];
+        }
+    }
+    static_assert(C::BN == 2 * SCALE_BLOCK, "two weight scale blocks per tile");
+    const float* wsc_mine = GATE_UP || wn * C::TN < SCALE_BLOCK ? wsc : wsc + KB + 1;
+
+    typedef typename Outs<C::SUB>::type outs;
+    outs acc[C::NT][C::MT];
+    outs zero;
+#pragma unroll
+    for (int c = 0; c < C::OUTS; ++c)
+        zero[c] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            acc[j][i] = zero;
+
+    const int fr = lane % C::SUB, fg = lane / C::SUB;   // operand row, piece of it
+    // LDS row of weight subtile j: gate_up keeps gate rows in the first half
+    auto wrow = [&](int j) {
+        if (GATE_UP) {
+            constexpr int HALF = C::NT / 2;
+            return (j < HALF ? 0 : C::BN / 2) + wn * (C::TN / 2) + (j % HALF) * C::SUB;
+        }
+        return wn * C::TN + j * C::SUB;
+    };
+    // This lane's pieces of its row: fg, fg + GROUPS, ... (the order inside a
+    // block is free as long as both operands share it); the subtiles start at
+    // multiples of 16 rows, so the swizzle is the row's.
+    int piece[8 / C::GROUPS];
+#pragma unroll
+    for (int c = 0; c < 8 / C::GROUPS; ++c)
+        piece[c] = fr * SCALE_BLOCK + (((fg + c * C::GROUPS) ^ swizzle(fr)) << 4);
+    auto load = [&](const uint8_t* rows, int round, v4u(&raw)[C::PIECES]) {
+#pragma unroll
+        for (int c = 0; c < C::PIECES; ++c)
+            raw[c] = *(const v4u*)(rows + piece[round * C::PIECES + c]);
+    };
+
+    // The products of subtile j run while those of the subtile before it join
+    // the accumulators.
+    outs held[C::MT];
+    float held_s[C::MT];
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) {
+        held[i] = zero;
+        held_s[i] = 0.0f;
+    }
+    auto join = [&](int j, int round) {
+#pragma unroll
+        for (int o = round * C::JOINS; o < (round + 1) * C::JOINS; ++o) {
+            const int i = o / C::OUTS, c = o % C::OUTS;
+            acc[j][i][c] = fmaf(held[i][c], held_s[i], acc[j][i][c]);
+        }
+    };
+
+    // What a block starts with is read from LDS ahead of the matrix
+    // instructions that end the block before it.
+    v4u wraw[C::PIECES], xraw[C::MT][C::ROUNDS][C::PIECES];
+    float xsc[C::MT], gs, us;
+    auto read_ahead = [&](const uint8_t* st, int kb) {
+        load(st + wrow(0) * SCALE_BLOCK, 0, wraw);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+            for (int r = 0; r < C::ROUNDS; ++r)
+                load(st + C::W_BYTES + (wm * C::TM + i * C::SUB) * SCALE_BLOCK, r, xraw[i][r]);
+        gs = wsc_mine[kb];
+        us = GATE_UP ? wsc[KB + 1 + kb] : 0.0f;
+        const uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES + (kb % C::SC_STEPS) * 32;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            const int m = wm * C::TM + i * C::SUB + fr;
+            xsc[i] = *(const float*)(sc + (m >> 3) * 256 + (m & 7) * 4);
+        }
+    };
+
+    issue_scales(0);
+#pragma unroll
+    for (int s = 0; s < C::S; ++s)
+        if (s < KB)
+            issue(s, s);
+    if (KB >= C::S)
+        wait_loads_and_meet<(C::S - 1) * C::LOADS>();
+    else
+        wait_loads_and_meet<0>();
+    read_ahead(lds, 0);
+    int slot = 0;
+    // One block.  `steady`: stage kb+S exists and is loaded into the slot that
+    // this block frees; else (the last S blocks) nothing more is loaded.
+    auto step = [&](const int kb, auto steady) {
+        const uint8_t* st = lds + slot * C::STAGE;
+        if (steady && (kb + C::S) % C::SC_STEPS == 0)
+            issue_scales(kb + C::S);
+        float sg[C::MT], su[C::MT];
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            sg[i] = xsc[i] * gs;
+            su[i] = xsc[i] * us;
+        }
+        Operand<C> xf[C::MT][C::ROUNDS], wf;
+        wf.from(wraw);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+            for (int r = 0; r < C::ROUNDS; ++r)
+                xf[i][r].from(xraw[i][r]);
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j) {
+            outs t[C::MT];
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+                t[i] = zero;
+#pragma unroll
+            for (int r = 0; r < C::ROUNDS; ++r) {
+                Operand<C> wnext = wf;
+                if (j + 1 < C::NT || r + 1 < C::ROUNDS) {
+                    const int jn = r + 1 < C::ROUNDS ? j : j + 1;
+                    load(st + wrow(jn) * SCALE_BLOCK, r + 1 < C::ROUNDS ? r + 1 : 0, wraw);
+                    wnext.from(wraw);
+                } else {
+                    // stage kb has been read by this wave: once every wave is
+                    // here its slot is free, and stage kb+1 has arrived (the
+                    // S-2 stages behind it may still be in flight; row scales
+                    // among them only make the wait longer)
+                    wait_loads_and_meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
+                    if constexpr (decltype(steady)::value)
+                        issue(kb + C::S, slot);
+                    slot = slot + 1 == C::S ? 0 : slot + 1;
+                    // (past the last block: a stale stage, never used)
+                    read_ahead(lds + slot * C::STAGE, kb + 1);
+                }
+#pragma unroll
+                for (int s = 0; s < C::STEPS; ++s)
+#pragma unroll
+                    for (int i = 0; i < C::MT; ++i)
+                        t[i] = product_step(wf.f[s], xf[i][r].f[s], t[i]);
+                join(j > 0 ? j - 1 : C::NT - 1, r);
+                wf = wnext;
+#pragma unroll
+                for (int i = 0; i < C::MT * C::STEPS; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // a matrix instruction,
+                    __builtin_amdgcn_sched_group_barrier(0x002, C::BESIDE, 0);  // what goes beside it
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i) {
+                held[i] = t[i];
+                held_s[i] = GATE_UP && j >= C::NT / 2 ? su[i] : sg[i];
+            }
+        }
+    };
+    int kb = 0;
+    for (; kb + C::S < KB; ++kb)
+        step(kb, std::true_type{});
+    for (; kb < KB; ++kb)
+        step(kb, std::false_type{});
+#pragma unroll
+    for (int r = 0; r < C::ROUNDS; ++r)
+        join(C::NT - 1, r);
+
+    // Lane (fr, fg) holds, of subtile (j, i), column fr (token i*SUB + fr) and
+    // in its outputs 4q .. 4q+3 the rows 4*GROUPS*q + 4*fg .. +3.
+    constexpr int QUADS = C::OUTS / 4;
+    auto row_of = [&](int j, int q) { return wrow(j) + 4 * C::GROUPS * q + 4 * fg; };
+    if (!GATE_UP) {
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            const int m = wm * C::TM + i * C::SUB + fr;
+            if (m >= at.rows)
+                continue;
+            uint16_t* yr = p.y + (int64_t)(at.m0 + m) * p.n;
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+                for (int q = 0; q < QUADS; ++q) {
+                    const int n = n0 + row_of(j, q);
+                    if (n < p.n) {
+                        const v2u o{bf16_pack(acc[j][i][4 * q], acc[j][i][4 * q + 1]),
+                                    bf16_pack(acc[j][i][4 * q + 2], acc[j][i][4 * q + 3])};
+                        *(v2u*)(yr + n) = o;
+                    }
+                }
+        }
+        return;
+    }
+
+    // h = silu(gate) * up in fp32, then the block's code and scale per token
+    constexpr int HALF = C::NT / 2 > 0 ? C::NT / 2 : 1;
+    float* tops = (float*)lds;                       // [WN][BM] largest magnitudes
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < HALF; ++j)
+#pragma unroll
+            for (int c = 0; c < C::OUTS; ++c) {
+                const float g = acc[j][i][c], u = acc[(j + HALF) % C::NT][i][c];
+                const float h = g / (1.0f + __expf(-g)) * u;
+                acc[j][i][c] = h;
+                top = fmaxf(top, fabsf(h));
+            }
+#pragma unroll
+        for (int d = C::SUB; d < WAVE; d <<= 1)
+            top = fmaxf(top, __shfl_xor(top, d, WAVE));
+        if (fg == 0)
+            tops[wn * C::BM + wm * C::TM + i * C::SUB + fr] = top;
+    }
+    __syncthreads();
+    uint8_t* codes = lds + C::WN * C::BM * 4;        // [BM][128]
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) {
+        const int m = wm * C::TM + i * C::SUB + fr;
+        float top = 0.0f;
+#pragma unroll
+        for (int q = 0; q < C::WN; ++q)
+            top = fmaxf(top, tops[q * C::BM + m]);
+        float inv, scale;
+        block_scale(top, inv, scale);
+        if (wn == 0 && fg == 0 && m < at.rows)
+            p.hs[(int64_t)(at.m0 + m) * (F / SCALE_BLOCK) + at.n_tile] = scale;
+#pragma unroll
+        for (int j = 0; j < HALF; ++j)
+#pragma unroll
+            for (int q = 0; q < QUADS; ++q)
+                *(uint32_t*)(codes + m * SCALE_BLOCK + row_of(j, q)) =
+                    e4m3_pack4(acc[j][i][4 * q] * inv, acc[j][i][4 * q + 1] * inv, acc[j][i][4 * q + 2] * inv,
+                               acc[j][i][4 * q + 3] * inv);
+    }
+    __syncthreads();
+    for (int v = threadIdx.x; v < at.rows * 8; v += C::THREADS) {
+        const int m = v >> 3, c = v & 7;
+        *(v4u*)(p.h + (int64_t)(at.m0 + m) * F + at.n_tile * SCALE_BLOCK + c * 16) =
+            *(const v4u*)(codes + m * SCALE_BLOCK + c * 16);
+    }
+}
+
+template <class C, bool GATE_UP>
+hipError_t launch(const ExpertProduct& p, hipStream_t stream)
+{
+    const int n_tiles = GATE_UP ? p.n / C::BN : (p.n + C::BN - 1) / C::BN;
+    const int64_t used = p.rows < p.E ? p.rows : p.E;   // experts that can have rows
+    // sum of ceil(rows_e / BM) over the used experts, at most
+    const int64_t m_tiles = (p.rows - used) / C::BM + used;
+    const int64_t grid = (m_tiles * n_tiles + 7) / 8 * 8;
+    constexpr int64_t ROW = 1 << 20;              // a grid dimension times the threads stays below 2^32
+    const dim3 blocks((uint32_t)std::min(grid, ROW), (uint32_t)((grid + ROW - 1) / ROW));
+    constexpr int ring = C::RING;
+    constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
+    const int bytes = std::max(ring + 2 * (p.k / SCALE_BLOCK + 1) * 4, epi);
+    hipError_t e = hipFuncSetAttribute((const void*)expert_product_kernel<C, GATE_UP>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess)
+        return e;
+    expert_product_kernel<C, GATE_UP><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
+    return hipGetLastError();
+}
+
+template <bool GATE_UP>
+hipError_t choose(const ExpertProduct& p, hipStream_t stream)
+{
+    if (p.rows == 0)
+        return hipSuccess;
+    const int64_t mean = p.rows / p.E;
+    constexpr bool EIGHT = !GATE_UP;
+    if (mean <= 12)
+        return launch<Tile<16, 256, 1, 8, 3, EIGHT, 16>, GATE_UP>(p, stream);
+    if (mean <= 48)
+        return launch<Tile<64, 256, 1, 8, 3, EIGHT, 16>, GATE_UP>(p, stream);
+    if constexpr (EIGHT) {
+        if (mean <= 96)
+            return launch<Tile<128, 256, 2, 4, 3, true, 16>, GATE_UP>(p, stream);
+        return launch<Tile<256, 256, 4, 2, 2, true, 16>, GATE_UP>(p, stream);
+    } else {
+        return launch<Tile<128, 256, 2, 4, 3, false, 32>, GATE_UP>(p, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_expert_matmul(const ExpertProduct& p, hipStream_t stream)
+{
+    return choose<false>(p, stream);
+}
+
+hipError_t launch_expert_gate_up(const ExpertProduct& p, hipStream_t stream)
+{
+    return choose<true>(p, stream);
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -1,0 +1,73 @@
+// Device helpers shared by the operators around dispatch and combine (norm,
+// routing, the experts' products, the few-token layer).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+namespace ops {
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr int WAVE = 64;
+constexpr int SCALE_BLOCK = 128;      // elements per scale, rows; also rows per weight scale block
+
+__device__ inline float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ inline float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+
+// Two fp32 values to packed bf16, round to nearest even; NaN stays NaN.
+__device__ inline uint32_t bf16_pack(float lo, float hi)
+{
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    const v2b v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// The dispatch payload's block scale from a block's largest magnitude:
+// scale = amax/448 and inv = 448/amax (correctly rounded divisions), the
+// scale held at the smallest normal number, 1 for a block of zeros.
+__device__ inline void block_scale(float amax, float& inv, float& scale)
+{
+    inv = 0.0f;
+    scale = 1.0f;
+    if (amax >= 0x1.cp-118f) {             // 448 * 2^-126
+        inv = 448.0f / amax;
+        scale = amax / 448.0f;
+    } else if (amax > 0.0f) {
+        inv = 0x1p126f;
+        scale = 0x1p-126f;
+    }
+}
+
+// Four fp32 values to four e4m3 codes (first in the low byte), round to
+// nearest even.  The values are a block's, times its inverse scale: finite
+// ones are at most 448 but for the roundings of the inverse and the product,
+// far below 464 where the conversion would leave the format; NaN codes as NaN.
+__device__ inline uint32_t e4m3_pack4(float a, float b, float c, float d)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    return (uint32_t)r;
+}
+
+// Eight e4m3 codes (two dwords) as fp16, exactly: the format's values
+// (2^-9 .. 448, NaN) are all normal fp16 numbers.  The instruction
+// takes two codes at the rate of an fp32 add.
+__device__ inline v8h e4m3_to_f16(uint32_t lo, uint32_t hi)
+{
+    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, false);
+    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)lo, 1.0f, true);
+    const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, false);
+    const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)hi, 1.0f, true);
+    return v8h{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -1,0 +1,278 @@
+// Per-token operators ahead of dispatch: residual addition with RMS norm (and
+// the dispatch codec's e4m3 rows), and the choice of a token's experts.
+#include "moe_ops.h"
+#include "ops_common.h"
+
+namespace moe {
+namespace ops {
+namespace {
+
+__device__ inline v4u ld_nt(const v4u* p) { return __builtin_nontemporal_load(p); }
+__device__ inline void st_nt(const v4u& v, v4u* p) { __builtin_nontemporal_store(v, p); }
+
+// ---------------------------------------------------------------------------
+// s = x + residual (fp32); y = s / sqrt(mean(s^2) + eps) * weight.
+//
+// One pass: a row is read once, stays in registers as fp32 (V vectors of 8
+// elements per thread) through the sum of squares, and every output is
+// written from there.  A row belongs to W waves; the norm is of the fp32 sum,
+// not of its bf16 rounding, and the codes are of the fp32 result, not of y's
+// bf16 rounding, so each output is rounded once.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+    int64_t rows;
+    int hidden, vecs;         // vecs: 8-element vectors per row
+    const uint16_t* x;
+    const uint16_t* residual;
+    const uint16_t* weight;
+    float eps;
+    uint16_t* residual_out;
+    uint16_t* y;
+    uint8_t* yq;
+    float* ys;
+};
+
+template <int V>
+__global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int waves_per_row)
+{
+    __shared__ float part[16];
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = threadIdx.x / WAVE;
+    const int per_block = blockDim.x / WAVE / waves_per_row;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t row = block * per_block + wave / waves_per_row;
+    const int t = (wave % waves_per_row) * WAVE + lane;      // thread of the row
+    const int nt = waves_per_row * WAVE;
+    const bool live = row < a.rows;
+    const int64_t at = row * a.hidden;
+    float s[V][8];
+    float sum = 0.0f;
+    v4u xv[V], rv[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int v = u * nt + t;
+        xv[u] = rv[u] = v4u{0, 0, 0, 0};
+        if (live && v < a.vecs) {
+            xv[u] = ld_nt((const v4u*)(a.x + at) + v);
+            if (a.residual)
+                rv[u] = ld_nt((const v4u*)(a.residual + at) + v);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s[u][2 * c] = bf16_lo(xv[u][c]) + bf16_lo(rv[u][c]);
+            s[u][2 * c + 1] = bf16_hi(xv[u][c]) + bf16_hi(rv[u][c]);
+            sum = fmaf(s[u][2 * c], s[u][2 * c], sum);
+            sum = fmaf(s[u][2 * c + 1], s[u][2 * c + 1], sum);
+        }
+#pragma unroll
+    for (int d = WAVE / 2; d; d >>= 1)
+        sum += __shfl_xor(sum, d, WAVE);
+    if (waves_per_row > 1) {
+        if (lane == 0)
+            part[wave] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        const int w0 = wave / waves_per_row * waves_per_row;
+        for (int w = 0; w < waves_per_row; ++w)
+            sum += part[w0 + w];
+    }
+    const float r = 1.0f / sqrtf(sum / (float)a.hidden + a.eps);
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int v = u * nt + t;
+        const bool mine = live && v < a.vecs;
+        v4u wv{0, 0, 0, 0};
+        if (mine) {
+            wv = ((const v4u*)a.weight)[v];
+            if (a.residual_out) {
+                v4u o;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    o[c] = bf16_pack(s[u][2 * c], s[u][2 * c + 1]);
+                st_nt(o, (v4u*)(a.residual_out + at) + v);
+            }
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            s[u][2 * c] *= r * bf16_lo(wv[c]);
+            s[u][2 * c + 1] *= r * bf16_hi(wv[c]);
+            top = fmaxf(top, fmaxf(fabsf(s[u][2 * c]), fabsf(s[u][2 * c + 1])));
+        }
+        if (mine && a.y) {
+            v4u o;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                o[c] = bf16_pack(s[u][2 * c], s[u][2 * c + 1]);
+            ((v4u*)(a.y + at))[v] = o;
+        }
+        if (a.yq) {
+            // a block of 128 is 16 consecutive lanes
+#pragma unroll
+            for (int d = 8; d; d >>= 1)
+                top = fmaxf(top, __shfl_xor(top, d, WAVE));
+            float inv, scale;
+            block_scale(top, inv, scale);
+            if (mine) {
+                const v2u q{e4m3_pack4(s[u][0] * inv, s[u][1] * inv, s[u][2] * inv, s[u][3] * inv),
+                            e4m3_pack4(s[u][4] * inv, s[u][5] * inv, s[u][6] * inv, s[u][7] * inv)};
+                ((v2u*)(a.yq + at))[v] = q;
+                if ((v & 15) == 0)
+                    a.ys[row * (a.hidden / SCALE_BLOCK) + (v >> 4)] = scale;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A token's K best experts and their softmax weights.  G lanes share a token,
+// lane l of them holds experts l, l+G, ...; K times: the largest logit left
+// (lowest expert among equals) is taken out.  NaN counts as -infinity.
+// ---------------------------------------------------------------------------
+template <int G, int V, bool BF16>
+__global__ __launch_bounds__(256) void topk_route_kernel(int64_t tokens, int E, int K, const void* logits,
+                                                         int renorm, int32_t* idx, float* w)
+{
+    constexpr int PER = 256 / G;
+    const int l = threadIdx.x % G;
+    const int64_t tok = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * PER + threadIdx.x / G;
+    const int64_t row = (tok < tokens ? tok : tokens - 1) * E;
+    float z[V];
+    bool gone[V];                 // taken, or past the last expert
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * G + l;
+        z[i] = -INFINITY;
+        gone[i] = e >= E;
+        if (e < E) {
+            if (BF16)
+                z[i] = __uint_as_float((uint32_t)((const uint16_t*)logits)[row + e] << 16);
+            else
+                z[i] = ((const float*)logits)[row + e];
+            if (z[i] != z[i])
+                z[i] = -INFINITY;
+        }
+        top = fmaxf(top, z[i]);
+    }
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor(top, d, G));
+    // p(z) = exp(z - top); infinite tops share the whole weight
+    auto p = [&](float v) {
+        if (top == -INFINITY)
+            return 0.0f;
+        return v == top ? 1.0f : __expf(v - top);
+    };
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        sum += i * G + l < E ? p(z[i]) : 0.0f;
+#pragma unroll
+    for (int d = G / 2; d; d >>= 1)
+        sum += __shfl_xor(sum, d, G);
+    float best_sum = 0.0f, mine = 0.0f;
+    int mine_e = 0;
+    for (int k = 0; k < K; ++k) {
+        float bz = -INFINITY;
+        int be = 1 << 30;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (!gone[i] && z[i] >= bz) {
+                bz = z[i];
+                be = i * G + l;
+            }
+#pragma unroll
+        for (int d = G / 2; d; d >>= 1) {
+            const float oz = __shfl_xor(bz, d, G);
+            const int oe = __shfl_xor(be, d, G);
+            if (oz > bz || (oz == bz && oe < be)) {
+                bz = oz;
+                be = oe;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * G + l == be)
+                gone[i] = true;
+        const float v = p(bz);
+        best_sum += v;
+        // lane k % G keeps pick k and writes it when it must
+        if (k % G == l) {
+            mine = v;
+            mine_e = be;
+        }
+        if ((k % G == G - 1 || k == K - 1)) {
+            const int k0 = k / G * G;
+            if (tok < tokens && k0 + l <= k) {
+                idx[tok * K + k0 + l] = mine_e;
+                w[tok * K + k0 + l] = mine;
+            }
+        }
+    }
+    const float total = renorm ? best_sum : sum;
+    const float scale = total > 0.0f ? 1.0f / total : 0.0f;
+    if (tok < tokens)
+        for (int k = l; k < K; k += G)
+            w[tok * K + k] *= scale;
+}
+
+// `blocks` workgroups as a grid whose dimensions times the threads stay below 2^32.
+inline dim3 grid_of(int64_t blocks)
+{
+    constexpr int64_t ROW = 1 << 20;
+    return dim3((uint32_t)(blocks < ROW ? blocks : ROW), (uint32_t)((blocks + ROW - 1) / ROW));
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const uint16_t* residual,
+                              const uint16_t* weight, float eps, uint16_t* residual_out, uint16_t* y,
+                              uint8_t* yq, float* ys, hipStream_t stream)
+{
+    if (rows == 0)
+        return hipSuccess;
+    const NormArgs a{rows, hidden, hidden / 8, x, residual, weight, eps, residual_out, y, yq, ys};
+    const int waves = (a.vecs + 2 * WAVE - 1) / (2 * WAVE);     // at two vectors per thread
+    if (waves <= 16) {
+        // short rows: several to a workgroup of up to four waves
+        const int per = waves < 4 ? 4 / waves : 1;
+        const int64_t grid = (rows + per - 1) / per;
+        add_rmsnorm_kernel<2><<<grid_of(grid), dim3(per * waves * WAVE), 0, stream>>>(a, waves);
+    } else {
+        add_rmsnorm_kernel<8><<<grid_of(rows), dim3(1024), 0, stream>>>(a, 16);
+    }
+    return hipGetLastError();
+}
+
+template <int G, int V>
+static hipError_t route(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm, int32_t* idx,
+                        float* w, hipStream_t stream)
+{
+    const int64_t grid = (tokens + 256 / G - 1) / (256 / G);
+    if (bf16)
+        topk_route_kernel<G, V, true><<<grid_of(grid), dim3(256), 0, stream>>>(tokens, E, K, logits,
+                                                                                     renorm, idx, w);
+    else
+        topk_route_kernel<G, V, false><<<grid_of(grid), dim3(256), 0, stream>>>(tokens, E, K, logits,
+                                                                                      renorm, idx, w);
+    return hipGetLastError();
+}
+
+hipError_t launch_topk_route(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm,
+                             int32_t* idx, float* w, hipStream_t stream)
+{
+    if (tokens == 0)
+        return hipSuccess;
+    if (E <= 64)
+        return route<16, 4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+    if (E <= 256)
+        return route<16, 16>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+    return route<64, 16>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -75,7 +75,8 @@ typedef enum moe_status {
 
 typedef enum moe_dtype {
     MOE_BF16 = 0,           /* dispatch payload: bf16 rows, 2H bytes */
-    MOE_FP8_E4M3 = 1        /* dispatch payload: OCP e4m3 rows (H bytes) + fp32 scale per 128 elements */
+    MOE_FP8_E4M3 = 1,       /* dispatch payload: OCP e4m3 rows (H bytes) + fp32 scale per 128 elements */
+    MOE_FP32 = 2            /* moe_topk_route's logits only */
 } moe_dtype;
 
 /* How rows reach the peer (same four calls and results either way, as the
@@ -369,6 +370,112 @@ typedef enum moe_probe_kind {
 } moe_probe_kind;
 
 int moe_hbm_probe(int kind, void* dst, const void* src, size_t bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around dispatch and combine.
+ *
+ * What a layer runs beside the four calls: the norm that makes its rows, the
+ * choice of experts that dispatch_send reads, the experts themselves (between
+ * dispatch_recv and combine_send), and the whole layer for a batch so small
+ * that moving rows costs more than it saves.  None needs a group.  They
+ * follow the conventions at the top of this file (status codes, dense 16-byte
+ * aligned device tensors of the current device, work enqueued on `stream`,
+ * nothing synchronised, kernels only, so all of them can be captured); each
+ * is a ROCTX range of its name.  They keep no state between calls: two calls
+ * may run at once on two streams unless one's output is the other's input,
+ * output or workspace.  Inputs and outputs must not overlap, except where
+ * said.  Zero rows or tokens is a valid call that does nothing and needs no
+ * pointers.
+ *
+ * Rows in 8 bits are the dispatch payload of MOE_FP8_E4M3 everywhere: e4m3
+ * codes and one fp32 scale per 128 elements, scale = amax/448 (held at 2^-126
+ * or more; 1 for a block of zeros), code = e4m3(value * (448/amax)), value =
+ * code * scale.  Weights in 8 bits are e4m3 codes, row-major, with one fp32
+ * scale per block of 128 rows by 128 columns (the last block of rows may be
+ * short).
+ * ------------------------------------------------------------------------- */
+
+/* Residual addition and root-mean-square norm.
+ *   x             bf16 [rows][hidden]; residual bf16, the same shape, or NULL
+ *   weight        bf16 [hidden]; eps >= 0
+ *   residual_out  bf16 [rows][hidden] or NULL: s = x + residual
+ *   y             bf16 [rows][hidden] or NULL
+ *   y_q, y_scale  e4m3 [rows][hidden] and fp32 [rows][hidden/128], or both NULL
+ * s is the fp32 sum, y = s / sqrt(mean(s^2) + eps) * weight in fp32; every
+ * output is rounded once from there (the norm does not see residual_out's
+ * rounding, nor the codes y's).  At least one output is given.  hidden a
+ * multiple of 8 (of 128 with y_q), <= 65536.  residual_out and y may be x or
+ * residual themselves.  The sum of squares is an fp32 sum: elements above
+ * about 1e19/sqrt(hidden) overflow it. */
+int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, const void* residual,
+                    const void* weight, float eps, void* residual_out, void* y, void* y_q,
+                    float* y_scale, hipStream_t stream);
+
+/* The experts of each token, as dispatch_send reads them.
+ *   logits        [tokens][num_experts], MOE_BF16 or MOE_FP32 (logits_dtype)
+ *   topk_idx      int32 [tokens][top_k]: the largest logits, descending, the
+ *                 lower expert first among equals
+ *   topk_weights  fp32 [tokens][top_k]: softmax over all experts at those
+ *                 ids; with renormalise != 0 divided by their sum
+ * top_k <= num_experts <= 1024, top_k <= 64.  A logit of -infinity (or NaN)
+ * masks its expert: weight 0, chosen only when fewer than top_k others are
+ * left, lower experts first.  A token with every expert masked gets ids
+ * 0..top_k-1 with weight 0.  Logits of +infinity share the whole weight. */
+int moe_topk_route(int32_t tokens, int32_t num_experts, int32_t top_k, const void* logits,
+                   int32_t logits_dtype, int32_t renormalise, int32_t* topk_idx,
+                   float* topk_weights, hipStream_t stream);
+
+/* The experts' product on rows as dispatch_recv leaves them.
+ *   x, x_scale      e4m3 [rows][k], fp32 [rows][k/128]
+ *   expert_offsets  int32 [num_experts+1]: expert e's rows are
+ *                   [expert_offsets[e], expert_offsets[e+1]), ascending from
+ *                   0 to at most rows; rows behind the last expert's are
+ *                   neither read nor written.  (Offsets outside [0, rows]
+ *                   are held to it: the result is then unspecified, but
+ *                   nothing outside the tensors is touched.)
+ *   w, w_scale      e4m3 [num_experts][n][k], fp32 [num_experts][ceil(n/128)][k/128]
+ *   y               bf16 [rows][n]: y[r][j] = sum over k of x[r][k] * w[e][j][k],
+ *                   products of a block of 128 summed first, block sums
+ *                   scaled and summed in fp32, one rounding to bf16
+ * n a multiple of 8, k of 128, both <= 65536; num_experts <= 1024. */
+int moe_expert_matmul(int32_t rows, int32_t num_experts, int32_t n, int32_t k, const void* x,
+                      const float* x_scale, const int32_t* expert_offsets, const void* w,
+                      const float* w_scale, void* y, hipStream_t stream);
+
+/* The experts' gate and up products, their activation and its coding, in one:
+ *   w13, w13_scale  e4m3 [num_experts][2f][k] (f gate rows, then f up rows),
+ *                   fp32 [num_experts][2f/128][k/128]
+ *   h, h_scale      e4m3 [rows][f], fp32 [rows][f/128]: the coded rows of
+ *                   silu(gate) * up, silu(v) = v / (1 + exp(-v)), formed and
+ *                   coded in fp32 -- what moe_expert_matmul reads next
+ * Other arguments as for moe_expert_matmul; f a multiple of 128, <= 65536. */
+int moe_expert_gate_up(int32_t rows, int32_t num_experts, int32_t f, int32_t k, const void* x,
+                       const float* x_scale, const int32_t* expert_offsets, const void* w13,
+                       const float* w13_scale, void* h, float* h_scale, hipStream_t stream);
+
+/* A whole layer for at most MOE_FEW_TOKENS_MAX tokens, with no dispatch:
+ * every token's row is coded (as dispatch codes it), goes through the gate,
+ * up and down products of each expert it names (h coded between, as above),
+ * and out[t] = bf16(sum over k of topk_weights[t][k] * y_k), y_k held in fp32.
+ *   x             bf16 [num_tokens][hidden]
+ *   topk_idx      int32 [num_tokens][top_k]; an id outside [0, num_experts)
+ *                 names no expert (padding): it adds nothing, and a token
+ *                 with no expert gets zeros.  An expert may be named twice.
+ *   topk_weights  fp32 [num_tokens][top_k]
+ *   w13, w13_scale, w2, w2_scale   as above; w2 e4m3 [num_experts][hidden][f]
+ *   out           bf16 [num_tokens][hidden]
+ *   workspace     device, moe_few_token_workspace(...) bytes, this call's own
+ *                 until its work has run (two captured graphs that may run at
+ *                 once need one each); holds nothing between calls
+ * hidden and f multiples of 128, <= 65536; num_experts <= 1024, top_k <= 64. */
+#define MOE_FEW_TOKENS_MAX 64
+/* Bytes of workspace for these sizes; 0 if they are out of range. */
+size_t moe_few_token_workspace(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t f);
+int moe_few_token_layer(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden,
+                        int32_t f, const void* x, const int32_t* topk_idx,
+                        const float* topk_weights, const void* w13, const float* w13_scale,
+                        const void* w2, const float* w2_scale, void* out, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
 
 /* Static description of a status code; never NULL. */
 const char* moe_strerror(int status);
