@@ -30,6 +30,21 @@ __device__ inline uint32_t bf16_pack(float lo, float hi)
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// The largest of 16 consecutive lanes, in each of them (rotations inside the
+// vector unit, no LDS).
+template <int N>
+__device__ inline float rotate16(float v)
+{
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ inline float max16(float v)
+{
+    v = fmaxf(v, rotate16<8>(v));
+    v = fmaxf(v, rotate16<4>(v));
+    v = fmaxf(v, rotate16<2>(v));
+    return fmaxf(v, rotate16<1>(v));
+}
+
 // The dispatch payload's block scale from a block's largest magnitude:
 // scale = amax/448 and inv = 448/amax (correctly rounded divisions), the
 // scale held at the smallest normal number, 1 for a block of zeros.

@@ -111,9 +111,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
         }
         if (a.yq) {
             // a block of 128 is 16 consecutive lanes
-#pragma unroll
-            for (int d = 8; d; d >>= 1)
-                top = fmaxf(top, __shfl_xor(top, d, WAVE));
+            top = max16(top);
             float inv, scale;
             block_scale(top, inv, scale);
             if (mine) {
