@@ -45,6 +45,35 @@ __device__ inline float max16(float v)
     return fmaxf(v, rotate16<1>(v));
 }
 
+// The largest of a wave's unsigned values, and the sum of its floats (in a
+// fixed order), as uniform values: rotations inside rows of 16 lanes, then
+// row 0 into row 1 and row 2 into row 3, then row 1 into row 3.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t move_rows(uint32_t v)      // 0 in the rows that take nothing
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF);
+}
+__device__ inline uint32_t wave_max(uint32_t v)
+{
+    v = max(v, move_rows<0x128, 0xF>(v));
+    v = max(v, move_rows<0x124, 0xF>(v));
+    v = max(v, move_rows<0x122, 0xF>(v));
+    v = max(v, move_rows<0x121, 0xF>(v));
+    v = max(v, move_rows<0x142, 0xA>(v));
+    v = max(v, move_rows<0x143, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, WAVE - 1);
+}
+__device__ inline float wave_sum(float v)
+{
+    v += rotate16<8>(v);
+    v += rotate16<4>(v);
+    v += rotate16<2>(v);
+    v += rotate16<1>(v);
+    v += __uint_as_float(move_rows<0x142, 0xA>(__float_as_uint(v)));
+    v += __uint_as_float(move_rows<0x143, 0xC>(__float_as_uint(v)));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), WAVE - 1));
+}
+
 // The dispatch payload's block scale from a block's largest magnitude:
 // scale = amax/448 and inv = 448/amax (correctly rounded divisions), the
 // scale held at the smallest normal number, 1 for a block of zeros.

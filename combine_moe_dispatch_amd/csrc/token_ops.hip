@@ -218,6 +218,121 @@ __global__ __launch_bounds__(256) void topk_route_kernel(int64_t tokens, int E, 
             w[tok * K + k] *= scale;
 }
 
+// Floats as unsigned numbers in the same order; -0 as +0, NaN as -infinity.
+// 0 is below all of them.
+__device__ inline uint32_t order_of(float v)
+{
+    const uint32_t u = __float_as_uint(v == v ? v + 0.0f : -INFINITY);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ inline float value_of(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// The same with a wave per token, for 64 < E <= 64 V: lane l holds experts
+// l*V .. l*V+V-1, sorted once (largest first, stable).  A pick is then the
+// largest of the lanes' heads, the lowest lane among equals (its experts are
+// the lowest), and one shift of that lane's list; lists end in 0.  The logits
+// are compared as ordered unsigned numbers, whose maximum is one instruction
+// across lanes too.
+template <int V, bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void topk_route_wave_kernel(int64_t tokens, int E, int K, const void* logits,
+                                                              int renorm, int32_t* idx, float* w)
+{
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int64_t tok = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + threadIdx.x / WAVE;
+    if (tok >= tokens)
+        return;
+    float z[V];
+    const int e0 = lane * V;
+    if (VEC) {
+        // E is a multiple of 4: whole groups of 4 are inside or outside
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            v4f v{NAN, NAN, NAN, NAN};
+            if (e0 + i < E) {
+                if (BF16) {
+                    const v2u b = *(const v2u*)((const uint16_t*)logits + tok * E + e0 + i);
+                    v = v4f{bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)};
+                } else {
+                    v = *(const v4f*)((const float*)logits + tok * E + e0 + i);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                z[i + c] = v[c];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = NAN;
+            if (e0 + i < E)
+                z[i] = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[tok * E + e0 + i] << 16)
+                            : ((const float*)logits)[tok * E + e0 + i];
+        }
+    }
+    uint32_t key[V], best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        key[i] = e0 + i < E ? order_of(z[i]) : 0;
+        best = max(best, key[i]);
+    }
+    const float top = value_of(wave_max(best));
+    // p(z) = exp(z - top); infinite tops share the whole weight, and a token
+    // with nothing but -infinity has none
+    auto p = [&](float v) { return __expf(v == top ? 0.0f : v - top); };
+    const bool none = top == -INFINITY;
+    float sum = 0.0f;
+    if (!renorm) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            sum += key[i] ? p(value_of(key[i])) : 0.0f;
+        sum = wave_sum(sum);
+    }
+    int at[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        at[i] = i;
+#pragma unroll
+    for (int n = V - 1; n > 0; --n)
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t a = key[i], b = key[i + 1];
+            const int c = at[i], d = at[i + 1];
+            key[i] = max(a, b);
+            key[i + 1] = min(a, b);
+            at[i] = a < b ? d : c;
+            at[i + 1] = a < b ? c : d;
+        }
+    uint32_t order = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        order |= (uint32_t)at[i] << (4 * i);
+    uint32_t mine = 0;
+    int mine_e = 0;
+    for (int k = 0; k < K; ++k) {
+        const uint32_t pick = wave_max(key[0]);
+        const int src = __builtin_ctzll(__ballot(key[0] == pick));
+        const int e = src * V + (__builtin_amdgcn_readlane((int)order, src) & 15);
+        mine = lane == k ? pick : mine;
+        mine_e = lane == k ? e : mine_e;
+        const uint32_t win = lane == src ? ~0u : 0u;     // a bit select per entry
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i)
+            key[i] = (key[i + 1] & win) | (key[i] & ~win);
+        key[V - 1] &= ~win;
+        order >>= win & 4;
+    }
+    const float v = lane < K ? p(value_of(mine)) : 0.0f;
+    if (renorm)
+        sum = wave_sum(v);
+    if (lane < K) {
+        idx[tok * K + lane] = mine_e;
+        w[tok * K + lane] = none ? 0.0f : v / sum;
+    }
+}
+
 // `blocks` workgroups as a grid whose dimensions times the threads stay below 2^32.
 inline dim3 grid_of(int64_t blocks)
 {
@@ -260,6 +375,25 @@ static hipError_t route(int64_t tokens, int E, int K, const void* logits, int bf
     return hipGetLastError();
 }
 
+template <int V>
+static hipError_t route_wave(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm,
+                             int32_t* idx, float* w, hipStream_t stream)
+{
+    const dim3 grid = grid_of((tokens + 3) / 4), block(256);
+    if (E % 4 == 0) {
+        if (bf16)
+            topk_route_wave_kernel<V, true, true><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+        else
+            topk_route_wave_kernel<V, false, true><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+    } else {
+        if (bf16)
+            topk_route_wave_kernel<V, true, false><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+        else
+            topk_route_wave_kernel<V, false, false><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+    }
+    return hipGetLastError();
+}
+
 hipError_t launch_topk_route(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm,
                              int32_t* idx, float* w, hipStream_t stream)
 {
@@ -268,7 +402,9 @@ hipError_t launch_topk_route(int64_t tokens, int E, int K, const void* logits, i
     if (E <= 64)
         return route<16, 4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
     if (E <= 256)
-        return route<16, 16>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+        return route_wave<4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+    if (E <= 512)
+        return route_wave<8>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
     return route<64, 16>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
 }
 
