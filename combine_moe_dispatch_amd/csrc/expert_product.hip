@@ -40,8 +40,10 @@ namespace {
 // One tile: BM token rows by BN weight rows, WM x WN waves, S stages of the
 // LDS ring.  EIGHT: the e4m3 matrix instruction, else the codes go through
 // fp16.  SUB x SUB outputs per matrix instruction.
-template <int BM_, int BN_, int WM_, int WN_, int S_, bool EIGHT_, int SUB_>
+// STREAM: the weights are read once (few rows per expert).
+template <int BM_, int BN_, int WM_, int WN_, int S_, bool EIGHT_, int SUB_, bool STREAM_>
 struct Tile {
+    static constexpr bool STREAM = STREAM_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, SUB = SUB_;
     static constexpr bool EIGHT = EIGHT_;
     static constexpr int WAVES = WM * WN;
@@ -52,6 +54,8 @@ struct Tile {
     static constexpr int PIECES = EIGHT ? 2 : 1;         // 16-byte pieces converted at a time
     static constexpr int STEPS = EIGHT ? 1 : 2;          // matrix instructions they make
     static constexpr int ROUNDS = 8 / GROUPS / PIECES;   // times that makes a block
+    static constexpr int FRAGS = NT * ROUNDS;            // weight operands of a block
+    static_assert(FRAGS % 2 == 0, "two operands are read ahead in turn");
     static constexpr int OUTS = SUB * SUB / WAVE;        // outputs per lane
     // vector instructions beside each matrix instruction: a round's share of
     // the joins and the next operand's conversions, spread evenly
@@ -79,9 +83,11 @@ struct Tile {
 typedef const __attribute__((address_space(1))) void gvoid;
 typedef __attribute__((address_space(3))) void lvoid;
 
+// STREAM: the nontemporal hint, for bytes that no other workgroup will read.
+template <bool STREAM>
 __device__ inline void load_lds16(const uint8_t* g, uint8_t* l)
 {
-    __builtin_amdgcn_global_load_lds((gvoid*)g, (lvoid*)l, 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((gvoid*)g, (lvoid*)l, 16, 0, STREAM ? 2 : 0);
 }
 
 __device__ inline void load_lds4(const float* g, uint8_t* l)
@@ -235,47 +241,50 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
     const uint8_t* wbase_up = wbase + (int64_t)F * p.k;
     const uint8_t* xbase = p.x + (int64_t)at.m0 * p.k;
     const float* sbase = p.xs + (int64_t)at.m0 * KB;
-    const int sub = lane >> 3;
-    uint32_t woff[C::W_LOADS], xoff[C::X_LOADS];
-#pragma unroll
-    for (int i = 0; i < C::W_LOADS; ++i) {
-        const int r = (i * C::WAVES + wave) * 8 + sub;
-        const int n = GATE_UP ? r % (C::BN / 2) : min(r, p.n - 1 - n0);
-        woff[i] = (uint32_t)n * p.k + (((lane & 7) ^ swizzle(r)) << 4);
-    }
-#pragma unroll
-    for (int i = 0; i < C::X_LOADS; ++i) {
-        const int r = ((i * C::WAVES + wave) % C::X_LOADS_ALL) * 8 + sub;
-        xoff[i] = (uint32_t)min(r, at.rows - 1) * p.k + (((lane & 7) ^ swizzle(r)) << 4);
-    }
-    // row scales: lane (k, row) = (lane / 8, lane % 8) of an 8 x 8 load, a line
-    // of eight scales per row (scales of one block for 64 rows, a load per
-    // block, cost a quarter of the whole load path: 64 lines each)
-    uint32_t soff[C::SC_LOADS];
-#pragma unroll
-    for (int i = 0; i < C::SC_LOADS; ++i)
-        soff[i] = (uint32_t)min(((i * C::WAVES + wave) % C::SC_LOADS_ALL) * 8 + (lane & 7), at.rows - 1) * KB;
+    // Load i of a wave brings rows (i*WAVES + wave)*8 .. +7; WAVES*4 is a
+    // multiple of 8, so a lane's piece of its row is the same in all of them.
+    // The offsets are formed where they are used, three instructions a load:
+    // kept, they would take registers that the products need.
+    static_assert(C::WAVES * 4 % 8 == 0, "one swizzle per lane");
+    const int row0 = wave * 8 + (lane >> 3);
+    const uint32_t place = ((lane & 7) ^ swizzle(row0)) << 4;
+    const int w_last = GATE_UP ? C::BN / 2 - 1 : min(C::BN, p.n - n0) - 1;
     uint8_t* const sc_lds = lds + C::S * C::STAGE;
 
-    // the row scales of blocks kb .. kb+7
+    // the row scales of blocks kb .. kb+7: lane (k, row) = (lane / 8, lane % 8)
+    // of an 8 x 8 load, a line of eight scales per row (scales of one block for
+    // 64 rows, a load per block, cost a quarter of the whole load path: 64
+    // lines each)
     auto issue_scales = [&](int kb) {
         const int k = min(kb + (lane >> 3), KB - 1);
         uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES;
 #pragma unroll
-        for (int i = 0; i < C::SC_LOADS; ++i)
-            load_lds4(sbase + soff[i] + k, sc + ((i * C::WAVES + wave) % C::SC_LOADS_ALL) * 256);
+        for (int i = 0; i < C::SC_LOADS; ++i) {
+            const int part = (i * C::WAVES + wave) % C::SC_LOADS_ALL;
+            load_lds4(sbase + (uint32_t)min(part * 8 + (lane & 7), at.rows - 1) * KB + k, sc + part * 256);
+        }
     };
     auto issue = [&](int kb, int slot) {
         uint8_t* st = lds + slot * C::STAGE;
         const int k0 = kb * SCALE_BLOCK;
+        int r = row0;
+        asm volatile("" : "+v"(r));           // keeps the offsets from being formed ahead
 #pragma unroll
         for (int i = 0; i < C::W_LOADS; ++i) {
-            const bool up = GATE_UP && (i * C::WAVES + wave) * 8 >= C::BN / 2;
-            load_lds16((up ? wbase_up : wbase) + k0 + woff[i], st + (i * C::WAVES + wave) * 1024);
+            constexpr int HALF = GATE_UP ? C::BN / 2 : C::BN;
+            const int first = i * C::WAVES * 8;
+            const bool up = first >= HALF;
+            const uint32_t n = min(r + first % HALF, w_last);
+            load_lds16<C::STREAM>((up ? wbase_up : wbase) + k0 + (__umul24(n, p.k) + place),
+                             st + (i * C::WAVES + wave) * 1024);
         }
 #pragma unroll
-        for (int i = 0; i < C::X_LOADS; ++i)
-            load_lds16(xbase + k0 + xoff[i], st + C::W_BYTES + ((i * C::WAVES + wave) % C::X_LOADS_ALL) * 1024);
+        for (int i = 0; i < C::X_LOADS; ++i) {
+            const int part = (i * C::WAVES + wave) % C::X_LOADS_ALL;
+            const uint32_t m = min(C::X_LOADS_ALL >= C::WAVES ? r + i * C::WAVES * 8 : part * 8 + (lane >> 3),
+                                   at.rows - 1);
+            load_lds16<false>(xbase + k0 + (__umul24(m, p.k) + place), st + C::W_BYTES + part * 1024);
+        }
     };
 
     // The tile's weight scales, [2][KB + 1] (two blocks of 128 columns; gate_up:
@@ -348,10 +357,12 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
 
     // What a block starts with is read from LDS ahead of the matrix
     // instructions that end the block before it.
-    v4u wraw[C::PIECES], xraw[C::MT][C::ROUNDS][C::PIECES];
+    v4u wraw[2][C::PIECES], xraw[C::MT][C::ROUNDS][C::PIECES];
     float xsc[C::MT], gs, us;
-    auto read_ahead = [&](const uint8_t* st, int kb) {
-        load(st + wrow(0) * SCALE_BLOCK, 0, wraw);
+    auto read_w = [&](const uint8_t* st, int f) {
+        load(st + wrow(f / C::ROUNDS) * SCALE_BLOCK, f % C::ROUNDS, wraw[f & 1]);
+    };
+    auto read_x = [&](const uint8_t* st, int kb) {
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -376,7 +387,9 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
         wait_loads_and_meet<(C::S - 1) * C::LOADS>();
     else
         wait_loads_and_meet<0>();
-    read_ahead(lds, 0);
+    read_w(lds, 0);
+    read_w(lds, 1);
+    read_x(lds, 0);
     int slot = 0;
     // One block.  `steady`: stage kb+S exists and is loaded into the slot that
     // this block frees; else (the last S blocks) nothing more is loaded.
@@ -391,7 +404,7 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
             su[i] = xsc[i] * us;
         }
         Operand<C> xf[C::MT][C::ROUNDS], wf;
-        wf.from(wraw);
+        wf.from(wraw[0]);
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
 #pragma unroll
@@ -405,23 +418,24 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
                 t[i] = zero;
 #pragma unroll
             for (int r = 0; r < C::ROUNDS; ++r) {
-                Operand<C> wnext = wf;
-                if (j + 1 < C::NT || r + 1 < C::ROUNDS) {
-                    const int jn = r + 1 < C::ROUNDS ? j : j + 1;
-                    load(st + wrow(jn) * SCALE_BLOCK, r + 1 < C::ROUNDS ? r + 1 : 0, wraw);
-                    wnext.from(wraw);
-                } else {
-                    // stage kb has been read by this wave: once every wave is
-                    // here its slot is free, and stage kb+1 has arrived (the
-                    // S-2 stages behind it may still be in flight; row scales
-                    // among them only make the wait longer)
+                // operand f is in wf, f+1 has been read, f+2 is read now
+                const int f = j * C::ROUNDS + r;
+                if (f == C::FRAGS - 2) {
+                    // the rest of stage kb has been read by this wave: once
+                    // every wave is here its slot is free, and stage kb+1 has
+                    // arrived (the S-2 stages behind it may still be in flight;
+                    // row scales among them only make the wait longer)
                     wait_loads_and_meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
                     if constexpr (decltype(steady)::value)
                         issue(kb + C::S, slot);
                     slot = slot + 1 == C::S ? 0 : slot + 1;
-                    // (past the last block: a stale stage, never used)
-                    read_ahead(lds + slot * C::STAGE, kb + 1);
                 }
+                Operand<C> wnext;
+                wnext.from(wraw[(f + 1) & 1]);
+                // (past the last block: a stale stage, never used)
+                read_w(f + 2 < C::FRAGS ? st : lds + slot * C::STAGE, (f + 2) % C::FRAGS);
+                if (f == C::FRAGS - 1)
+                    read_x(lds + slot * C::STAGE, kb + 1);
 #pragma unroll
                 for (int s = 0; s < C::STEPS; ++s)
 #pragma unroll
@@ -557,15 +571,15 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
     const int64_t mean = p.rows / p.E;
     constexpr bool EIGHT = !GATE_UP;
     if (mean <= 12)
-        return launch<Tile<16, 256, 1, 8, 3, EIGHT, 16>, GATE_UP>(p, stream);
+        return launch<Tile<16, 256, 1, 8, 2, EIGHT, 16, true>, GATE_UP>(p, stream);
     if (mean <= 48)
-        return launch<Tile<64, 256, 1, 8, 3, EIGHT, 16>, GATE_UP>(p, stream);
+        return launch<Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, GATE_UP>(p, stream);
     if constexpr (EIGHT) {
         if (mean <= 96)
-            return launch<Tile<128, 256, 2, 4, 3, true, 16>, GATE_UP>(p, stream);
-        return launch<Tile<256, 256, 4, 2, 2, true, 16>, GATE_UP>(p, stream);
+            return launch<Tile<128, 256, 2, 4, 3, true, 16, true>, GATE_UP>(p, stream);
+        return launch<Tile<256, 256, 4, 2, 2, true, 16, false>, GATE_UP>(p, stream);
     } else {
-        return launch<Tile<128, 256, 2, 4, 3, false, 32>, GATE_UP>(p, stream);
+        return launch<Tile<128, 256, 2, 4, 3, false, 32, false>, GATE_UP>(p, stream);
     }
 }
 
