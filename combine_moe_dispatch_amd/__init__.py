@@ -328,69 +328,97 @@ def moe_hbm_probe(kind: int, dst, src, nbytes: int, stream=None) -> None:
 # at least as many bytes as the call reads or writes); sizes are the library's
 # to check, so a bad size raises the same MoeError.
 
-_BF16, _E4M3, _F32, _I32 = ("bfloat16",), ("float8_e4m3fn", "uint8"), ("float32",), ("int32",)
+try:
+    import torch as _torch
+except ImportError:             # raw addresses and stream handles only
+    _torch = None
+
+if _torch is not None:
+    _BF16, _F32, _I32 = (_torch.bfloat16,), (_torch.float32,), (_torch.int32,)
+    _E4M3, _U8 = (_torch.float8_e4m3fn, _torch.uint8), (_torch.uint8,)
+    # the current stream's handle without building a Stream object: a small
+    # operator's call takes longer on the host than on the device
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_device = getattr(_torch._C, "_cuda_getDevice", None)
+else:
+    _BF16 = _F32 = _I32 = _E4M3 = _U8 = ()
+    _raw_stream = _raw_device = None
 
 
-def _op_arg(a, call: str, name: str, numel: int, width: int, dtypes, dev):
-    if a is None or isinstance(a, int):
+def _op_device() -> int:
+    if _raw_device is not None and _torch.cuda.is_initialized():
+        return _raw_device()
+    return _current_device()
+
+
+def _op_stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _op_arg(a, call: str, name: str, numel: int, width: int, dtypes, dev: int):
+    if a is None or type(a) is int:
+        return a
+    if a.dtype in dtypes and a.get_device() == dev and a.is_contiguous() and a.numel() >= numel:
+        return a.data_ptr()
+    if isinstance(a, int):
         return a
     if not a.is_cuda:
         bad = "not a device tensor"
-    elif a.device.index != dev:
-        bad = f"on device {a.device.index}, the current device is {dev}"
+    elif a.get_device() != dev:
+        bad = f"on device {a.get_device()}, the current device is {dev}"
     elif not a.is_contiguous():
         bad = "not contiguous"
-    elif str(a.dtype)[6:] not in dtypes:
-        bad = f"dtype {a.dtype}, expected {' or '.join(dtypes)}"
-    elif a.numel() < numel:
-        bad = f"{a.numel() * width} bytes, the call needs {numel * width}"
+    elif a.dtype not in dtypes:
+        bad = f"dtype {a.dtype}, expected {' or '.join(map(str, dtypes))}"
     else:
-        return a.data_ptr()
+        bad = f"{a.numel() * width} bytes, the call needs {numel * width}"
     raise MoeError(MOE_ERR_INVALID, f"{call}: {name} {bad}")
 
 
 def moe_add_rmsnorm(rows: int, hidden: int, x, residual, weight, eps: float, residual_out, y,
                     y_q, y_scale, stream=None) -> None:
     c = "moe_add_rmsnorm"
-    dev, n = _current_device(), rows * hidden
+    dev, n = _op_device(), rows * hidden
     _check(_lib.moe_add_rmsnorm(
         rows, hidden, _op_arg(x, c, "x", n, 2, _BF16, dev),
         _op_arg(residual, c, "residual", n, 2, _BF16, dev),
         _op_arg(weight, c, "weight", hidden, 2, _BF16, dev), eps,
         _op_arg(residual_out, c, "residual_out", n, 2, _BF16, dev),
         _op_arg(y, c, "y", n, 2, _BF16, dev), _op_arg(y_q, c, "y_q", n, 1, _E4M3, dev),
-        _op_arg(y_scale, c, "y_scale", n // 128, 4, _F32, dev), _stream(stream)), c)
+        _op_arg(y_scale, c, "y_scale", n // 128, 4, _F32, dev), _op_stream(stream, dev)), c)
 
 
 def moe_topk_route(tokens: int, num_experts: int, top_k: int, logits, logits_dtype: int,
                    renormalise: bool, topk_idx, topk_weights, stream=None) -> None:
     c = "moe_topk_route"
-    dev, n = _current_device(), tokens * top_k
+    dev, n = _op_device(), tokens * top_k
     kind, width = (_BF16, 2) if logits_dtype == MOE_BF16 else (_F32, 4)
     _check(_lib.moe_topk_route(
         tokens, num_experts, top_k,
         _op_arg(logits, c, "logits", tokens * num_experts, width, kind, dev), logits_dtype,
         1 if renormalise else 0, _op_arg(topk_idx, c, "topk_idx", n, 4, _I32, dev),
-        _op_arg(topk_weights, c, "topk_weights", n, 4, _F32, dev), _stream(stream)), c)
+        _op_arg(topk_weights, c, "topk_weights", n, 4, _F32, dev), _op_stream(stream, dev)), c)
 
 
 def moe_expert_matmul(rows: int, num_experts: int, n: int, k: int, x, x_scale, expert_offsets, w,
                       w_scale, y, stream=None) -> None:
     c = "moe_expert_matmul"
-    dev, kb, E = _current_device(), k // 128, num_experts
+    dev, kb, E = _op_device(), k // 128, num_experts
     _check(_lib.moe_expert_matmul(
         rows, E, n, k, _op_arg(x, c, "x", rows * k, 1, _E4M3, dev),
         _op_arg(x_scale, c, "x_scale", rows * kb, 4, _F32, dev),
         _op_arg(expert_offsets, c, "expert_offsets", E + 1, 4, _I32, dev),
         _op_arg(w, c, "w", E * n * k, 1, _E4M3, dev),
         _op_arg(w_scale, c, "w_scale", E * -(-n // 128) * kb, 4, _F32, dev),
-        _op_arg(y, c, "y", rows * n, 2, _BF16, dev), _stream(stream)), c)
+        _op_arg(y, c, "y", rows * n, 2, _BF16, dev), _op_stream(stream, dev)), c)
 
 
 def moe_expert_gate_up(rows: int, num_experts: int, f: int, k: int, x, x_scale, expert_offsets,
                        w13, w13_scale, h, h_scale, stream=None) -> None:
     c = "moe_expert_gate_up"
-    dev, kb, E = _current_device(), k // 128, num_experts
+    dev, kb, E = _op_device(), k // 128, num_experts
     _check(_lib.moe_expert_gate_up(
         rows, E, f, k, _op_arg(x, c, "x", rows * k, 1, _E4M3, dev),
         _op_arg(x_scale, c, "x_scale", rows * kb, 4, _F32, dev),
@@ -398,7 +426,7 @@ def moe_expert_gate_up(rows: int, num_experts: int, f: int, k: int, x, x_scale, 
         _op_arg(w13, c, "w13", E * 2 * f * k, 1, _E4M3, dev),
         _op_arg(w13_scale, c, "w13_scale", E * (f // 64) * kb, 4, _F32, dev),
         _op_arg(h, c, "h", rows * f, 1, _E4M3, dev),
-        _op_arg(h_scale, c, "h_scale", rows * (f // 128), 4, _F32, dev), _stream(stream)), c)
+        _op_arg(h_scale, c, "h_scale", rows * (f // 128), 4, _F32, dev), _op_stream(stream, dev)), c)
 
 
 def moe_few_token_workspace(num_tokens: int, top_k: int, hidden: int, f: int) -> int:
@@ -410,7 +438,7 @@ def moe_few_token_layer(num_tokens: int, num_experts: int, top_k: int, hidden: i
                         workspace_bytes: int = None, stream=None) -> None:
     """workspace_bytes may be left out where workspace is a tensor."""
     c = "moe_few_token_layer"
-    dev, T, E, H = _current_device(), num_tokens, num_experts, hidden
+    dev, T, E, H = _op_device(), num_tokens, num_experts, hidden
     kb, fb = H // 128, f // 128
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() if hasattr(workspace, "numel") else 0
@@ -423,5 +451,5 @@ def moe_few_token_layer(num_tokens: int, num_experts: int, top_k: int, hidden: i
         _op_arg(w2, c, "w2", E * H * f, 1, _E4M3, dev),
         _op_arg(w2_scale, c, "w2_scale", E * kb * fb, 4, _F32, dev),
         _op_arg(out, c, "out", T * H, 2, _BF16, dev),
-        _op_arg(workspace, c, "workspace", workspace_bytes, 1, ("uint8",), dev), workspace_bytes,
-        _stream(stream)), c)
+        _op_arg(workspace, c, "workspace", workspace_bytes, 1, _U8, dev), workspace_bytes,
+        _op_stream(stream, dev)), c)

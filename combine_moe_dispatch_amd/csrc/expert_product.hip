@@ -28,6 +28,7 @@
 // magnitude over the block of 128 and writes codes and scale, so the fp32
 // intermediate never leaves the registers.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "moe_ops.h"
@@ -555,10 +556,20 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
     constexpr int ring = C::RING;
     constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
     const int bytes = std::max(ring + 2 * (p.k / SCALE_BLOCK + 1) * 4, epi);
-    hipError_t e = hipFuncSetAttribute((const void*)expert_product_kernel<C, GATE_UP>,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    // once per device: the kernel may use all of a CU's LDS
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess)
         return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
+        e = hipFuncSetAttribute((const void*)expert_product_kernel<C, GATE_UP>,
+                                hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e != hipSuccess)
+            return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     expert_product_kernel<C, GATE_UP><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
     return hipGetLastError();
 }

@@ -12,7 +12,7 @@ A = 4096        # an aligned address
 
 @pytest.fixture(autouse=True)
 def no_device(monkeypatch):
-    monkeypatch.setattr(mep, "_current_device", lambda: 0)
+    monkeypatch.setattr(mep, "_op_device", lambda: 0)
 
 
 def refused(fn, *args):
