@@ -346,9 +346,7 @@ else:
 
 
 def _op_device() -> int:
-    if _raw_device is not None and _torch.cuda.is_initialized():
-        return _raw_device()
-    return _current_device()
+    return _current_device() if _raw_device is None else _raw_device()
 
 
 def _op_stream(stream, dev: int):
