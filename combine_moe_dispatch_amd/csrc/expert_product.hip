@@ -157,31 +157,28 @@ struct Place {
 
 // Tile t of the launch: experts in order, each expert's tiles in groups of up
 // to 8 row tiles, row tiles fastest inside a group.  Every wave finds it for
-// itself: lane l holds experts [l*per, (l+1)*per).
-template <int BM>
+// itself: lane l holds experts [l*per, (l+1)*per), PER >= per of them in
+// registers, so that one trip to memory is enough.
+template <int BM, int PER>
 __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int64_t rows_max, int n_tiles,
                                  Place& out)
 {
     const int lane = threadIdx.x & (WAVE - 1);
     const int per = (E + WAVE - 1) / WAVE;
     const int rmax = (int)rows_max;
-    int mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = lane * per + i;
-        if (e < E) {
-            const int a = min(max(offsets[e], 0), rmax), b = min(max(offsets[e + 1], 0), rmax);
-            mine += b > a ? (b - a + BM - 1) / BM : 0;
-        }
-    }
-    int incl = mine;
+    int o[PER + 1];
 #pragma unroll
-    for (int d = 1; d < WAVE; d <<= 1) {
-        const int o = __shfl_up(incl, d, WAVE);
-        if (lane >= d)
-            incl += o;
+    for (int i = 0; i <= PER; ++i)
+        o[i] = offsets[min(lane * per + min(i, per), E)];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i <= PER; ++i) {
+        o[i] = min(max(o[i], 0), rmax);
+        if (i > 0)
+            mine += max(o[i] - o[i - 1] + BM - 1, 0) / BM;
     }
-    const int total = __builtin_amdgcn_readlane(incl, WAVE - 1);
-    const int64_t tiles = (int64_t)total * n_tiles;
+    const int upto = wave_scan(mine);
+    const int64_t tiles = (int64_t)__builtin_amdgcn_readlane(upto, WAVE - 1) * n_tiles;
     // consecutive workgroups go to the 8 XCDs in turn: each XCD takes one
     // contiguous run of tiles, so that the tiles sharing weights share its L2
     const int64_t per_xcd = (tiles + 7) / 8;
@@ -190,33 +187,34 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     const int64_t t = (id & 7) * per_xcd + at;
     if (at >= per_xcd || t >= tiles)
         return false;
-    // the lane whose experts hold the tile
-    const uint64_t below = __ballot((int64_t)incl * n_tiles <= t);
-    const int src = __popcll(below);                   // lanes whose experts end before t
-    int first = __builtin_amdgcn_readlane(incl - mine, src);
-    for (int i = 0; i < per; ++i) {
-        const int e = src * per + i;
-        if (e >= E)
-            return false;
-        const int a = min(max(offsets[e], 0), rmax), b = min(max(offsets[e + 1], 0), rmax);
-        const int m_tiles = b > a ? (b - a + BM - 1) / BM : 0;
-        const int64_t u = t - (int64_t)first * n_tiles;
-        if (u < (int64_t)m_tiles * n_tiles) {
-            constexpr int GROUP = 8;
-            const int per_group = GROUP * n_tiles;
-            const int g = (int)(u / per_group);
-            const int in = (int)(u - (int64_t)g * per_group);
-            const int gm = min(GROUP, m_tiles - g * GROUP);
-            const int mt = g * GROUP + in % gm;
-            out.e = e;
-            out.m0 = a + mt * BM;
-            out.rows = min(BM, b - out.m0);
-            out.n_tile = in / gm;
-            return true;
+    // the lane whose experts hold the tile, and there the expert
+    const int src = __popcll(__ballot((int64_t)upto * n_tiles <= t));
+    int64_t u = t - (int64_t)(upto - mine) * n_tiles;
+    int e = lane * per, a = o[0], b = o[1], m_tiles = max(b - a + BM - 1, 0) / BM;
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+        if (u >= (int64_t)m_tiles * n_tiles) {
+            u -= (int64_t)m_tiles * n_tiles;
+            e = lane * per + i;
+            a = o[i];
+            b = o[i + 1];
+            m_tiles = max(b - a + BM - 1, 0) / BM;
         }
-        first += m_tiles;
-    }
-    return false;
+    out.e = __builtin_amdgcn_readlane(e, src);
+    a = __builtin_amdgcn_readlane(a, src);
+    b = __builtin_amdgcn_readlane(b, src);
+    m_tiles = (b - a + BM - 1) / BM;
+    const int64_t v = (int64_t)__builtin_amdgcn_readlane((int)(u >> 32), src) << 32 |
+                      (uint32_t)__builtin_amdgcn_readlane((int)u, src);
+    constexpr int GROUP = 8;
+    const int64_t per_group = (int64_t)GROUP * n_tiles;
+    const int g = (int)(v / per_group);
+    const int in = (int)(v - g * per_group);
+    const int gm = min(GROUP, m_tiles - g * GROUP);
+    out.m0 = a + (g * GROUP + in % gm) * BM;
+    out.rows = min(BM, b - out.m0);
+    out.n_tile = in / gm;
+    return true;
 }
 
 template <class C, bool GATE_UP>
@@ -224,7 +222,8 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
 {
     extern __shared__ __align__(1024) uint8_t lds[];
     Place at;
-    if (!find_tile<C::BM>(p.offsets, p.E, p.rows, n_tiles, at))
+    if (!(p.E <= 4 * WAVE ? find_tile<C::BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
+                          : find_tile<C::BM, 16>(p.offsets, p.E, p.rows, n_tiles, at)))
         return;
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
@@ -288,22 +287,29 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
         }
     };
 
-    // The tile's weight scales, [2][KB + 1] (two blocks of 128 columns; gate_up:
+    // The tile's weight scales, [2][ws_row] (two blocks of 128 columns; gate_up:
     // the gate block and the up block), wait in LDS behind the ring: a load of
-    // them inside the loop would wait for every stage in flight.
-    float* wsc = (float*)(lds + C::RING);
+    // them inside the loop would wait for every stage in flight.  One more is
+    // read past the last block.
+    float* const wsc = (float*)(lds + C::RING);
+    const int ws_row = (KB + WAVE) & ~(WAVE - 1);
     {
         const int b0 = n0 / SCALE_BLOCK;
         const int b1 = GATE_UP ? F / SCALE_BLOCK + b0 : min(b0 + 1, nb - 1);
-        const float* s0 = p.ws + ((int64_t)at.e * nb + b0) * KB;
-        const float* s1 = p.ws + ((int64_t)at.e * nb + b1) * KB;
-        for (int i = threadIdx.x; i < KB; i += C::THREADS) {
-            wsc[i] = s0[i];
-            wsc[KB + 1 + i] = s1[i];
+        const float* ws = p.ws + (int64_t)at.e * nb * KB;
+        for (int c = wave; c < 2 * ws_row / WAVE; c += C::WAVES) {
+            const int block = c < ws_row / WAVE ? 0 : 1;
+            const int k = min(c * WAVE + lane - block * ws_row, KB - 1);
+            load_lds4(ws + (int64_t)(block ? b1 : b0) * KB + k, (uint8_t*)wsc + c * 256);
         }
     }
+    issue_scales(0);
+#pragma unroll
+    for (int s = 0; s < C::S; ++s)
+        if (s < KB)
+            issue(s, s);
     static_assert(C::BN == 2 * SCALE_BLOCK, "two weight scale blocks per tile");
-    const float* wsc_mine = GATE_UP || wn * C::TN < SCALE_BLOCK ? wsc : wsc + KB + 1;
+    const float* wsc_mine = GATE_UP || wn * C::TN < SCALE_BLOCK ? wsc : wsc + ws_row;
 
     typedef typename Outs<C::SUB>::type outs;
     outs acc[C::NT][C::MT];
@@ -370,7 +376,7 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
             for (int r = 0; r < C::ROUNDS; ++r)
                 load(st + C::W_BYTES + (wm * C::TM + i * C::SUB) * SCALE_BLOCK, r, xraw[i][r]);
         gs = wsc_mine[kb];
-        us = GATE_UP ? wsc[KB + 1 + kb] : 0.0f;
+        us = GATE_UP ? wsc[ws_row + kb] : 0.0f;
         const uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES + (kb % C::SC_STEPS) * 32;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i) {
@@ -379,11 +385,6 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
         }
     };
 
-    issue_scales(0);
-#pragma unroll
-    for (int s = 0; s < C::S; ++s)
-        if (s < KB)
-            issue(s, s);
     if (KB >= C::S)
         wait_loads_and_meet<(C::S - 1) * C::LOADS>();
     else
@@ -470,24 +471,33 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
     // in its outputs 4q .. 4q+3 the rows 4*GROUPS*q + 4*fg .. +3.
     constexpr int QUADS = C::OUTS / 4;
     auto row_of = [&](int j, int q) { return wrow(j) + 4 * C::GROUPS * q + 4 * fg; };
-    if (!GATE_UP) {
+    if constexpr (!GATE_UP) {
 #pragma unroll
         for (int i = 0; i < C::MT; ++i) {
             const int m = wm * C::TM + i * C::SUB + fr;
             if (m >= at.rows)
                 continue;
             uint16_t* yr = p.y + (int64_t)(at.m0 + m) * p.n;
+            // Two subtiles at a time: lanes trade halves between the rows of 16
+            // so that each holds eight consecutive outputs and four lanes write
+            // 64 bytes of a row (as 8-byte pieces, 32 bytes of a row at once, the
+            // results of a round of tiles took 3.8 us to leave the chip).
+            static_assert(C::SUB == 16 && C::NT % 2 == 0, "pairs of 16-row subtiles");
 #pragma unroll
-            for (int j = 0; j < C::NT; ++j)
+            for (int j = 0; j < C::NT; j += 2) {
+                v4u o;
 #pragma unroll
-                for (int q = 0; q < QUADS; ++q) {
-                    const int n = n0 + row_of(j, q);
-                    if (n < p.n) {
-                        const v2u o{bf16_pack(acc[j][i][4 * q], acc[j][i][4 * q + 1]),
-                                    bf16_pack(acc[j][i][4 * q + 2], acc[j][i][4 * q + 3])};
-                        *(v2u*)(yr + n) = o;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const auto two = __builtin_amdgcn_permlane16_swap(
+                        bf16_pack(acc[j][i][2 * h], acc[j][i][2 * h + 1]),
+                        bf16_pack(acc[j + 1][i][2 * h], acc[j + 1][i][2 * h + 1]), false, false);
+                    o[h] = two[0];
+                    o[2 + h] = two[1];
                 }
+                const int n = n0 + wrow(j) + (fg & 1) * 16 + (fg >> 1) * 8;
+                if (n < p.n)
+                    *(v4u*)(yr + n) = o;
+            }
         }
         return;
     }
@@ -555,7 +565,7 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
     const dim3 blocks((uint32_t)std::min(grid, ROW), (uint32_t)((grid + ROW - 1) / ROW));
     constexpr int ring = C::RING;
     constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
-    const int bytes = std::max(ring + 2 * (p.k / SCALE_BLOCK + 1) * 4, epi);
+    const int bytes = std::max(ring + 2 * ((p.k / SCALE_BLOCK + WAVE) & ~(WAVE - 1)) * 4, epi);
     // once per device: the kernel may use all of a CU's LDS
     static std::atomic<uint64_t> allowed{0};
     int dev = 0;

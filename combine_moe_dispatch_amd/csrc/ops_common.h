@@ -63,6 +63,17 @@ __device__ inline uint32_t wave_max(uint32_t v)
     v = max(v, move_rows<0x143, 0xC>(v));
     return (uint32_t)__builtin_amdgcn_readlane((int)v, WAVE - 1);
 }
+// Inclusive sum over the lanes up to and with this one.
+__device__ inline int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);       // row shifts by 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += (int)move_rows<0x142, 0xA>((uint32_t)v);
+    v += (int)move_rows<0x143, 0xC>((uint32_t)v);
+    return v;
+}
 __device__ inline float wave_sum(float v)
 {
     v += rotate16<8>(v);
