@@ -369,12 +369,7 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
     auto read_w = [&](const uint8_t* st, int f) {
         load(st + wrow(f / C::ROUNDS) * SCALE_BLOCK, f % C::ROUNDS, wraw[f & 1]);
     };
-    auto read_x = [&](const uint8_t* st, int kb) {
-#pragma unroll
-        for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-            for (int r = 0; r < C::ROUNDS; ++r)
-                load(st + C::W_BYTES + (wm * C::TM + i * C::SUB) * SCALE_BLOCK, r, xraw[i][r]);
+    auto read_scales = [&](int kb) {
         gs = wsc_mine[kb];
         us = GATE_UP ? wsc[ws_row + kb] : 0.0f;
         const uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES + (kb % C::SC_STEPS) * 32;
@@ -384,18 +379,24 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
             xsc[i] = *(const float*)(sc + (m >> 3) * 256 + (m & 7) * 4);
         }
     };
+    auto read_x = [&](const uint8_t* st) {
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+            for (int r = 0; r < C::ROUNDS; ++r)
+                load(st + C::W_BYTES + (wm * C::TM + i * C::SUB) * SCALE_BLOCK, r, xraw[i][r]);
+    };
 
     if (KB >= C::S)
         wait_loads_and_meet<(C::S - 1) * C::LOADS>();
     else
         wait_loads_and_meet<0>();
-    read_w(lds, 0);
-    read_w(lds, 1);
-    read_x(lds, 0);
     int slot = 0;
-    // One block.  `steady`: stage kb+S exists and is loaded into the slot that
-    // this block frees; else (the last S blocks) nothing more is loaded.
-    auto step = [&](const int kb, auto steady) {
+    read_scales(0);
+    // One block, with the e4m3 instruction.  `steady`: stage kb+S exists and is
+    // loaded into the slot that this block frees; else (the last S blocks)
+    // nothing more is loaded.
+    auto step8 = [&](const int kb, auto steady) {
         const uint8_t* st = lds + slot * C::STAGE;
         if (steady && (kb + C::S) % C::SC_STEPS == 0)
             issue_scales(kb + C::S);
@@ -436,8 +437,10 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
                 wnext.from(wraw[(f + 1) & 1]);
                 // (past the last block: a stale stage, never used)
                 read_w(f + 2 < C::FRAGS ? st : lds + slot * C::STAGE, (f + 2) % C::FRAGS);
-                if (f == C::FRAGS - 1)
-                    read_x(lds + slot * C::STAGE, kb + 1);
+                if (f == C::FRAGS - 1) {
+                    read_x(lds + slot * C::STAGE);
+                    read_scales(kb + 1);
+                }
 #pragma unroll
                 for (int s = 0; s < C::STEPS; ++s)
 #pragma unroll
@@ -458,14 +461,121 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
             }
         }
     };
-    int kb = 0;
-    for (; kb + C::S < KB; ++kb)
-        step(kb, std::true_type{});
-    for (; kb < KB; ++kb)
-        step(kb, std::false_type{});
+    // The same through fp16, round by round: each round converts the next one's
+    // pieces of both operands while its products run, so that no conversion
+    // waits for the block to end.  All of a block's products stay open to its
+    // last round; the first half of them joins there, the second half in the
+    // next block's first round.
+    outs open[C::NT][C::MT];
+    Operand<C> xf[2][C::MT], wf[2][C::NT];
+    v4u xr[2][C::MT][C::PIECES], wr[2][C::NT][C::PIECES];
+    float last_su[C::MT];
+    auto read_round = [&](const uint8_t* st, int r) {
 #pragma unroll
-    for (int r = 0; r < C::ROUNDS; ++r)
-        join(C::NT - 1, r);
+        for (int j = 0; j < C::NT; ++j)
+            load(st + wrow(j) * SCALE_BLOCK, r, wr[r & 1][j]);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            load(st + C::W_BYTES + (wm * C::TM + i * C::SUB) * SCALE_BLOCK, r, xr[r & 1][i]);
+    };
+    auto convert_round = [&](int r) {
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j)
+            wf[r & 1][j].from(wr[r & 1][j]);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            xf[r & 1][i].from(xr[r & 1][i]);
+    };
+    auto join_half = [&](int j0, const float (&sc)[C::MT]) {
+#pragma unroll
+        for (int j = j0; j < j0 + C::NT / 2; ++j)
+#pragma unroll
+            for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                for (int c = 0; c < C::OUTS; ++c)
+                    acc[j][i][c] = fmaf(open[j][i][c], sc[i], acc[j][i][c]);
+    };
+    auto step16 = [&](const int kb, auto steady) {
+        const uint8_t* st = lds + slot * C::STAGE;
+        if (steady && (kb + C::S) % C::SC_STEPS == 0)
+            issue_scales(kb + C::S);
+        float sg[C::MT], su[C::MT];
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            sg[i] = xsc[i] * gs;
+            su[i] = xsc[i] * (GATE_UP ? us : gs);
+        }
+#pragma unroll
+        for (int r = 0; r < C::ROUNDS; ++r) {
+            // round r is converted, r+1 has been read, r+2 is read now
+            if (r == C::ROUNDS - 2) {
+                wait_loads_and_meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
+                if constexpr (decltype(steady)::value)
+                    issue(kb + C::S, slot);
+                slot = slot + 1 == C::S ? 0 : slot + 1;
+            }
+            if (r == 0)
+                join_half(C::NT / 2, last_su);
+            convert_round((r + 1) % C::ROUNDS);
+            read_round(r + 2 < C::ROUNDS ? st : lds + slot * C::STAGE, (r + 2) % C::ROUNDS);
+            if (r == C::ROUNDS - 1)
+                read_scales(kb + 1);
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+                for (int i = 0; i < C::MT; ++i)
+#pragma unroll
+                    for (int s = 0; s < C::STEPS; ++s)
+                        open[j][i] = product_step(wf[r & 1][j].f[s], xf[r & 1][i].f[s],
+                                                  r == 0 && s == 0 ? zero : open[j][i]);
+            if (r == C::ROUNDS - 1)
+                join_half(0, sg);
+            constexpr int PRODUCTS = C::NT * C::MT * C::STEPS;
+            constexpr int CONVERTS = (C::NT + C::MT) * 8, HALF = C::NT * C::MT * C::OUTS / 2;
+            __builtin_amdgcn_sched_group_barrier(0x100, C::NT + C::MT, 0);
+#pragma unroll
+            for (int i = 0; i < PRODUCTS; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (r == 0 || r == C::ROUNDS - 1)
+                    __builtin_amdgcn_sched_group_barrier(0x002, (CONVERTS + HALF) / PRODUCTS, 0);
+                else
+                    __builtin_amdgcn_sched_group_barrier(0x002, CONVERTS / PRODUCTS, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            last_su[i] = su[i];
+    };
+
+    int kb = 0;
+    if constexpr (C::EIGHT) {
+        read_w(lds, 0);
+        read_w(lds, 1);
+        read_x(lds);
+        for (; kb + C::S < KB; ++kb)
+            step8(kb, std::true_type{});
+        for (; kb < KB; ++kb)
+            step8(kb, std::false_type{});
+#pragma unroll
+        for (int r = 0; r < C::ROUNDS; ++r)
+            join(C::NT - 1, r);
+    } else {
+        read_round(lds, 0);
+        read_round(lds, 1);
+        convert_round(0);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+            last_su[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j)
+                open[j][i] = zero;
+        }
+        for (; kb + C::S < KB; ++kb)
+            step16(kb, std::true_type{});
+        for (; kb < KB; ++kb)
+            step16(kb, std::false_type{});
+        join_half(C::NT / 2, last_su);
+    }
 
     // Lane (fr, fg) holds, of subtile (j, i), column fr (token i*SUB + fr) and
     // in its outputs 4q .. 4q+3 the rows 4*GROUPS*q + 4*fg .. +3.
@@ -514,7 +624,7 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
 #pragma unroll
             for (int c = 0; c < C::OUTS; ++c) {
                 const float g = acc[j][i][c], u = acc[(j + HALF) % C::NT][i][c];
-                const float h = g / (1.0f + __expf(-g)) * u;
+                const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
                 acc[j][i][c] = h;
                 top = fmaxf(top, fabsf(h));
             }
@@ -598,6 +708,8 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
     if constexpr (EIGHT) {
         if (mean <= 96)
             return launch<Tile<128, 256, 2, 4, 3, true, 16, true>, GATE_UP>(p, stream);
+        if (mean <= 144)
+            return launch<Tile<160, 256, 2, 4, 2, true, 16, false>, GATE_UP>(p, stream);
         return launch<Tile<256, 256, 4, 2, 2, true, 16, false>, GATE_UP>(p, stream);
     } else {
         return launch<Tile<128, 256, 2, 4, 3, false, 32, false>, GATE_UP>(p, stream);
