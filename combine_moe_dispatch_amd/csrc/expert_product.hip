@@ -69,7 +69,8 @@ struct Tile {
     // loads of one stage that each wave issues (1 KB each)
     static constexpr int W_LOADS = W_BYTES / 1024 / WAVES;
     static constexpr int X_LOADS_ALL = X_BYTES / 1024;
-    static constexpr int X_LOADS = (X_LOADS_ALL + WAVES - 1) / WAVES;
+    static constexpr int X_LOADS = (X_LOADS_ALL + WAVES - 1) / WAVES;   // some parts twice if uneven
+    static_assert(X_LOADS_ALL % 2 == 0, "a wave's parts share the swizzle");
     static constexpr int LOADS = W_LOADS + X_LOADS;
     // row scales come SC_STEPS blocks at a time, 8 rows by 8 blocks per load
     static constexpr int SC_STEPS = 8;
@@ -281,8 +282,7 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
 #pragma unroll
         for (int i = 0; i < C::X_LOADS; ++i) {
             const int part = (i * C::WAVES + wave) % C::X_LOADS_ALL;
-            const uint32_t m = min(C::X_LOADS_ALL >= C::WAVES ? r + i * C::WAVES * 8 : part * 8 + (lane >> 3),
-                                   at.rows - 1);
+            const uint32_t m = min(r + (part - wave) * 8, at.rows - 1);
             load_lds16<false>(xbase + k0 + (__umul24(m, p.k) + place), st + C::W_BYTES + part * 1024);
         }
     };

@@ -267,6 +267,13 @@ def test_matmul(E, rows, n, k, kind, spare):
     assert bool((y[rows:] == 9.0).all())
 
 
+@pytest.mark.parametrize("E,rows,n,k,kind,spare", [
+    (1, 97, 264, 384, "even", 0), (1, 144, 520, 256, "even", 1), (2, 250, 256, 128, "even", 0),
+    (3, 390, 136, 640, "spread", 2), (5, 700, 512, 1280, "spread", 0), (4, 500, 256, 384, "last", 0)])
+def test_matmul_near_128_rows(E, rows, n, k, kind, spare):
+    test_matmul(E, rows, n, k, kind, spare)
+
+
 def run_gate_up(x, xs, w, ws, offsets):
     E, n, k = w.shape
     f, rows = n // 2, x.shape[0]
@@ -335,6 +342,23 @@ def test_products_odd_values(rows):
     wild[-1] = rows + 1000
     y = run_matmul(x, xs, w, ws, wild, rows)
     assert torch.equal(y[:rows], clean[:rows]) and bool((y[rows:] == 9.0).all())
+
+
+@pytest.mark.parametrize("rows", [2, 30, 130, 200])
+def test_widest_rows(rows):
+    """The widest rows that the calls take: 512 blocks of 128."""
+    say(f"[gpu] products of the widest rows rows={rows}")
+    g = rng(14, rows)
+    k = 65536
+    ins = grouped_inputs(g, 1, 16, k, [rows], 0, 0.3)
+    ref, big = R.product(*ins)
+    check_product(R.f64(run_matmul(*ins)[:rows]), ref, big, big * R.BLOCK)
+    if rows > 130:
+        return
+    x, xs, w, ws, offsets = grouped_inputs(g, 1, 256, k, [rows], 0, 0.3)
+    ws *= np.float32(2.0 ** -4 / np.sqrt(k / 128))
+    h, hs = run_gate_up(x, xs, w, ws, offsets)
+    check_gate_up(h[:rows].cpu().numpy(), R.f64(hs[:rows]), x, xs, w, ws, offsets)
 
 
 def test_matmul_long_offsets():
@@ -423,7 +447,8 @@ def check_few(out, ref, noise):
 @pytest.mark.parametrize("T,E,K,H,F", [
     (1, 1, 1, 128, 128), (1, 8, 3, 384, 256), (2, 8, 8, 256, 640), (3, 300, 8, 128, 128),
     (15, 8, 2, 1152, 128), (16, 3, 3, 256, 256), (17, 4, 2, 384, 128), (32, 2, 2, 256, 128),
-    (33, 5, 2, 128, 384), (64, 3, 2, 256, 128), (64, 64, 4, 128, 128), (5, 1024, 64, 128, 128)])
+    (33, 5, 2, 128, 384), (64, 3, 2, 256, 128), (64, 64, 4, 128, 128), (5, 1024, 64, 128, 128),
+    (64, 70, 64, 128, 128), (40, 2, 64, 128, 128)])
 def test_few(T, E, K, H, F):
     say(f"[gpu] few T={T} E={E} K={K} H={H} F={F}")
     ins = few_inputs(rng(9, T, E, K, H, F), T, E, K, H, F)
@@ -596,6 +621,26 @@ def test_captured_layers():
     finally:
         for L in layers:
             L.close()
+
+
+def test_first_call_captured():
+    """The first call of a tile size may be the captured one."""
+    say("[gpu] first call captured")
+    E, n, k, rows = 2, 264, 256, 240
+    g = rng(15)
+    ins = grouped_inputs(g, E, n, k, counts_of("even", E, rows, g), 0)
+    d = [dev(a) for a in ins]
+    y = torch.zeros((rows, n), dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mep.moe_expert_matmul(rows, E, n, k, d[0], d[1], d[4], d[2], d[3], y)
+    want = run_matmul(*ins)[:rows]
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
 
 
 def test_two_streams_at_once():
