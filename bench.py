@@ -178,11 +178,15 @@ def _code_only(text: str) -> str:
     return " ".join("".join(out).split())
 
 
+# the sources of the dispatch/combine path, whose traffic the profiles record
+PATH_SOURCES = ("moe_ep.hip", "moe_kernels.h", "moe_kernels.hip")
+
+
 def kernel_source_hash() -> str:
-    """Hash of the library's sources, comments and whitespace ignored."""
+    """Hash of the path's sources, comments and whitespace ignored."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "combine_moe_dispatch_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in PATH_SOURCES:
         with open(os.path.join(csrc, name), encoding="utf-8") as f:
             h.update(name.encode() + _code_only(f.read()).encode())
     return h.hexdigest()[:16]

@@ -23,6 +23,8 @@
 // partial combine's rows (at most N*T*K) reuse whichever pools combine uses.
 #include <hip/hip_runtime.h>
 
+#include <rocprofiler-sdk-roctx/roctx.h>
+
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
@@ -30,7 +32,6 @@
 #include <vector>
 
 #include "moe_ep.h"
-#include "moe_host.h"
 #include "moe_kernels.h"
 
 namespace {
@@ -89,9 +90,9 @@ const char* const kKernelNames[MOE_KERNEL_COUNT] = {
     "recv_map_kernel",
 };
 
-using moe::aligned16;
-using moe::CallRange;
-using moe::from_hip;
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 int validate_desc(const moe_group_desc* d)
 {
@@ -323,6 +324,15 @@ int timed_launch(moe_group_s* g, int kernel, hipStream_t st, bool launches, F&& 
     }
     return launch(L) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
+
+// A ROCTX range around one call of the C ABI (shown by rocprofv3
+// --marker-trace; a few tens of nanoseconds when no tool listens).
+struct CallRange {
+    explicit CallRange(const char* name) { roctxRangePushA(name); }
+    ~CallRange() { roctxRangePop(); }
+    CallRange(const CallRange&) = delete;
+    CallRange& operator=(const CallRange&) = delete;
+};
 
 bool debug_from_env()
 {

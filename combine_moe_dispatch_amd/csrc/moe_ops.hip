@@ -3,15 +3,24 @@
 // on the caller's stream.
 #include "moe_ops.h"
 
+#include <rocprofiler-sdk-roctx/roctx.h>
+
 #include "moe_ep.h"
-#include "moe_host.h"
 #include "moe_kernels.h"
 
-using moe::aligned16;
-using moe::CallRange;
-using moe::from_hip;
-
 namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// A ROCTX range around one call, as around the four of moe_ep.hip.
+struct CallRange {
+    explicit CallRange(const char* name) { roctxRangePushA(name); }
+    ~CallRange() { roctxRangePop(); }
+    CallRange(const CallRange&) = delete;
+    CallRange& operator=(const CallRange&) = delete;
+};
 
 constexpr int MAX_WIDTH = 65536;
 
