@@ -537,6 +537,82 @@ def overlap_demo(cfg, args) -> dict:
     return res
 
 
+def layer_run(cfg, args) -> dict:
+    """A whole expert layer on the workload's tokens, with real experts of
+    width args.expert_width: add + RMS norm, routing, e4m3 dispatch, gate/up
+    and down products, combine.  Median time of every operator and of the
+    layer, and of the few-token layer for a handful of the same tokens."""
+    import numpy as np
+    import torch
+
+    import combine_moe_dispatch_amd as mep
+    N, T, K, E, H, F = cfg.N, cfg.T, cfg.K, cfg.E, cfg.H, args.expert_width
+    tokens, R = N * T, cfg.rows
+    dev = torch.device("cuda", 0)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(cfg.seed)
+
+    def empty(*shape, dt=torch.float32):
+        return torch.empty(shape, dtype=dt, device=dev)
+
+    def weights(n, k):
+        w = empty(E, n, k, dt=torch.float8_e4m3fn)
+        for e in range(E):
+            w[e] = (96.0 * torch.randn((n, k), generator=gen, device=dev)).clamp_(-448, 448).to(w.dtype)
+        return w, torch.full((E, n // 128, k // 128), 1.0 / (96.0 * k ** 0.5), device=dev)
+
+    bf16, e4m3, i32 = torch.bfloat16, torch.float8_e4m3fn, torch.int32
+    x = torch.randn((tokens, H), generator=gen, device=dev).to(bf16)
+    res = torch.randn((tokens, H), generator=gen, device=dev).to(bf16)
+    norm_w = torch.ones(H, dtype=bf16, device=dev)
+    logits = torch.randn((tokens, E), generator=gen, device=dev)
+    (w13, s13), (w2, s2) = weights(2 * F, H), weights(H, F)
+    res_out, y, out = empty(tokens, H, dt=bf16), empty(tokens, H, dt=bf16), empty(tokens, H, dt=bf16)
+    idx, w = empty(tokens, K, dt=i32), empty(tokens, K)
+    ex, es, off = empty(R, H, dt=e4m3), empty(R, H // 128), empty(E + 1, dt=i32)
+    h, hs, ey = empty(R, F, dt=e4m3), empty(R, F // 128), empty(R, H, dt=bf16)
+    g = mep.moe_group_create(N, E, K, H, T, mep.MOE_FP8_E4M3)
+    calls = {
+        "add_rmsnorm": lambda: mep.moe_add_rmsnorm(tokens, H, x, res, norm_w, 1e-6, res_out, y, None, None),
+        "topk_route": lambda: mep.moe_topk_route(tokens, E, K, logits, mep.MOE_FP32, True, idx, w),
+        "dispatch": lambda: (mep.moe_dispatch_send(g, T, y, idx), mep.moe_dispatch_recv(g, ex, es, off)),
+        "expert_gate_up": lambda: mep.moe_expert_gate_up(R, E, F, H, ex, es, off, w13, s13, h, hs),
+        "expert_matmul": lambda: mep.moe_expert_matmul(R, E, H, F, h, hs, off, w2, s2, ey),
+        "combine": lambda: (mep.moe_combine_send(g, ey), mep.moe_combine_recv(g, w, out)),
+    }
+    steps = min(args.steps, 50)
+    marks = [[torch.cuda.Event(enable_timing=True) for _ in range(len(calls) + 1)] for _ in range(steps)]
+    for n in range(args.warmup + steps):
+        ev = marks[max(n - args.warmup, 0)]
+        ev[0].record()
+        for i, call in enumerate(calls.values()):
+            call()
+            ev[i + 1].record()
+    torch.cuda.synchronize()
+    if mep.moe_group_status(g) != mep.MOE_OK:
+        raise RuntimeError("the layer's cycle failed")
+    mep.moe_group_destroy(g)
+
+    def median(pairs):
+        return round(float(np.median([a.elapsed_time(b) for a, b in pairs])) * 1e3, 1)
+
+    rec = {"metric": "expert layer", "unit": "us", "value": median([(m[0], m[-1]) for m in marks]),
+           "us": {name: median([(m[i], m[i + 1]) for m in marks]) for i, name in enumerate(calls)},
+           "few_token_us": {}, "workload": cfg.describe() + f" expert width {F}"}
+    for n in (1, 8, 32):
+        if n > min(tokens, mep.MOE_FEW_TOKENS_MAX):
+            break
+        ws = empty(mep.moe_few_token_workspace(n, K, H, F), dt=torch.uint8)
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(steps + 1)]
+        for i in range(args.warmup + steps + 1):
+            if i >= args.warmup:
+                ev[i - args.warmup].record()
+            mep.moe_few_token_layer(n, E, K, H, F, y, idx, w, w13, s13, w2, s2, out, ws)
+        torch.cuda.synchronize()
+        rec["few_token_us"][str(n)] = median(list(zip(ev, ev[1:])))
+    return rec
+
+
 def hbm_ceiling(torch, mep, nbytes: int = 1 << 30, iters: int = 10, batches: int = 5) -> dict:
     """What HBM delivers to the library's streaming probes (16-byte
     nontemporal vectors, the movers' access style) on buffers of nbytes: a
@@ -712,6 +788,11 @@ def main() -> int:
                     help="also time the step captured once as a HIP graph and replayed")
     ap.add_argument("--overlap", action="store_true",
                     help="measure the send/recv split hiding a concurrent GEMM (prints one JSON line)")
+    ap.add_argument("--layer", action="store_true",
+                    help="time a whole expert layer on the workload's tokens, operator by operator "
+                         "(prints one JSON line)")
+    ap.add_argument("--expert-width", type=int, default=2048,
+                    help="with --layer: the experts' inner width (a multiple of 128)")
     ap.add_argument("--trace-summary", metavar="DB",
                     help="print a table of the library's kernels from a rocprofv3 kernel trace")
     ap.add_argument("--trace-timed", action="store_true",
@@ -738,6 +819,10 @@ def main() -> int:
     if args.overlap:
         from workloads import CONFIGS
         print(json.dumps(overlap_demo(CONFIGS[args.config], args)), flush=True)
+        return 0
+    if args.layer:
+        from workloads import CONFIGS
+        print(json.dumps(layer_run(CONFIGS[args.config], args)), flush=True)
         return 0
     if args.traffic_from or args.trace_summary or args.traffic_xcheck:
         from workloads import CONFIGS

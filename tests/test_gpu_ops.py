@@ -681,3 +681,17 @@ def test_tensor_refusals():
     refused("weight not a device tensor", 4, 256, x, None, w.cpu(), 1e-6, None, x, None, None)
     big = torch.zeros((5, 256), dtype=torch.bfloat16, device=DEV)
     refused("invalid argument", 4, 256, big.view(-1)[1:1025].view(4, 256), None, w, 1e-6, None, x, None, None)
+
+
+def test_bench_layer():
+    """The bench's layer run: every operator and the few-token layer timed."""
+    import argparse
+
+    import bench
+    from workloads import CONFIGS
+    say("[gpu] bench layer, tiny")
+    rec = bench.layer_run(CONFIGS["A"], argparse.Namespace(steps=3, warmup=1, expert_width=256))
+    assert list(rec["us"]) == ["add_rmsnorm", "topk_route", "dispatch", "expert_gate_up", "expert_matmul",
+                               "combine"]
+    assert rec["value"] > 0 and all(t > 0 for t in rec["us"].values())
+    assert list(rec["few_token_us"]) == ["1", "8", "32"]
