@@ -219,13 +219,8 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
 }
 
 template <class C, bool GATE_UP>
-__global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const ExpertProduct p, int n_tiles)
+__device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place& at, uint8_t* lds)
 {
-    extern __shared__ __align__(1024) uint8_t lds[];
-    Place at;
-    if (!(p.E <= 4 * WAVE ? find_tile<C::BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
-                          : find_tile<C::BM, 16>(p.offsets, p.E, p.rows, n_tiles, at)))
-        return;
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % C::WM, wn = wave / C::WM;
@@ -663,7 +658,26 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
     }
 }
 
-template <class C, bool GATE_UP>
+// Tiles of C::BM rows; an expert's last tile is one of REST's where that holds
+// the rows that are left.
+template <bool GATE_UP, class C, class REST>
+__global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const ExpertProduct p, int n_tiles)
+{
+    static_assert(REST::THREADS == C::THREADS && REST::BN == C::BN, "one launch for both");
+    extern __shared__ __align__(1024) uint8_t lds[];
+    Place at;
+    if (!(p.E <= 4 * WAVE ? find_tile<C::BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
+                          : find_tile<C::BM, 16>(p.offsets, p.E, p.rows, n_tiles, at)))
+        return;
+    if constexpr (REST::BM < C::BM)
+        if (at.rows <= REST::BM) {
+            product_tile<REST, GATE_UP>(p, at, lds);
+            return;
+        }
+    product_tile<C, GATE_UP>(p, at, lds);
+}
+
+template <bool GATE_UP, class C, class REST = C>
 hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 {
     const int n_tiles = GATE_UP ? p.n / C::BN : (p.n + C::BN - 1) / C::BN;
@@ -673,7 +687,7 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
     const int64_t grid = (m_tiles * n_tiles + 7) / 8 * 8;
     constexpr int64_t ROW = 1 << 20;              // a grid dimension times the threads stays below 2^32
     const dim3 blocks((uint32_t)std::min(grid, ROW), (uint32_t)((grid + ROW - 1) / ROW));
-    constexpr int ring = C::RING;
+    constexpr int ring = std::max(C::RING, REST::RING);
     constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
     const int bytes = std::max(ring + 2 * ((p.k / SCALE_BLOCK + WAVE) & ~(WAVE - 1)) * 4, epi);
     // once per device: the kernel may use all of a CU's LDS
@@ -684,16 +698,38 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
         return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
-        e = hipFuncSetAttribute((const void*)expert_product_kernel<C, GATE_UP>,
+        e = hipFuncSetAttribute((const void*)expert_product_kernel<GATE_UP, C, REST>,
                                 hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != hipSuccess)
             return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    expert_product_kernel<C, GATE_UP><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
+    expert_product_kernel<GATE_UP, C, REST><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
     return hipGetLastError();
 }
 
+// The tile, by the mean number of rows per expert.  With few rows the weights
+// are what costs, each read once: low tiles, several workgroups per CU,
+// nontemporal loads.  With many, the matrix unit: high tiles, whose loads and
+// LDS reads serve more products, and a lower tile for an expert's last rows.
+// Measured (us; 64 experts, n = 7168, k = 2048 for the product, f = 2048,
+// k = 4096 for gate/up, unless said otherwise):
+//  - gate/up of 256 experts, 4 rows each: 604 (16 rows alone 604, 32 alone
+//    609; 16 alone with plain loads 752);
+//  - 32 + 16 against 16 alone, gate/up: mean 9 157 against 181, mean 16 162
+//    against 196; against 64 + 32: mean 6 157 against 169, mean 16 162-186
+//    against 170-173, mean 24 186-190 against 174-201; the product alike (mean
+//    6 140 / 142, 24 170-181 / 162-171);
+//  - 64 + 32 against 32 + 16, mean 32: gate/up 206 against 214, the product
+//    171 against 216; 64 against 128, mean 60 of the product 211 against 204;
+//  - 128 rows nontemporal against 256 + 128 plain: mean 60 193-204 against
+//    201-210, mean 96 208-222 against 216-224, mean 112 228-259 against
+//    222-241, mean 128 277-296 against 254-261;
+//  - 256 + 128 against 256 alone: ragged means of 200-512 315-341 against
+//    316-391; against 128 + 32, mean 192 298-302 against 328-334;
+//  - gate/up, 128 + 64 against 128 alone: mean 75 316 against 343, 128
+//    405-452 against 418-469, 200 567 against 598, 256 662 against 686.  (256
+//    rows would need twice the accumulators.)
 template <bool GATE_UP>
 hipError_t choose(const ExpertProduct& p, hipStream_t stream)
 {
@@ -701,18 +737,20 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
         return hipSuccess;
     const int64_t mean = p.rows / p.E;
     constexpr bool EIGHT = !GATE_UP;
-    if (mean <= 12)
-        return launch<Tile<16, 256, 1, 8, 2, EIGHT, 16, true>, GATE_UP>(p, stream);
+    if (mean <= 20)
+        return launch<GATE_UP, Tile<32, 256, 1, 8, 2, EIGHT, 16, true>, Tile<16, 256, 1, 8, 2, EIGHT, 16, true>>(
+            p, stream);
     if (mean <= 48)
-        return launch<Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, GATE_UP>(p, stream);
+        return launch<GATE_UP, Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, Tile<32, 256, 1, 8, 3, EIGHT, 16, true>>(
+            p, stream);
     if constexpr (EIGHT) {
         if (mean <= 96)
-            return launch<Tile<128, 256, 2, 4, 3, true, 16, true>, GATE_UP>(p, stream);
-        if (mean <= 144)
-            return launch<Tile<160, 256, 2, 4, 2, true, 16, false>, GATE_UP>(p, stream);
-        return launch<Tile<256, 256, 4, 2, 2, true, 16, false>, GATE_UP>(p, stream);
+            return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>>(p, stream);
+        return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<128, 256, 2, 4, 3, true, 16, false>>(
+            p, stream);
     } else {
-        return launch<Tile<128, 256, 2, 4, 3, false, 32, false>, GATE_UP>(p, stream);
+        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<64, 256, 1, 8, 3, false, 16, false>>(
+            p, stream);
     }
 }
 

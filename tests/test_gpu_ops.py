@@ -344,7 +344,7 @@ def test_products_odd_values(rows):
     assert torch.equal(y[:rows], clean[:rows]) and bool((y[rows:] == 9.0).all())
 
 
-@pytest.mark.parametrize("rows", [2, 30, 130, 200])
+@pytest.mark.parametrize("rows", [2, 30, 130, 200, 300])
 def test_widest_rows(rows):
     """The widest rows that the calls take: 512 blocks of 128."""
     say(f"[gpu] products of the widest rows rows={rows}")
