@@ -677,16 +677,130 @@ __global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const Expert
     product_tile<C, GATE_UP>(p, at, lds);
 }
 
+// The product where tiles of 256 columns would leave most CUs idle: 32 columns
+// by 16 rows per workgroup, its 8 waves sharing the blocks of k in turn and
+// adding up through LDS, in wave order.  Operands go from memory to registers,
+// NARROW_AHEAD blocks ahead, with no barrier until the end: a step of the LDS
+// ring costs a trip to memory over its depth (1.1 us with 2 stages, 0.7 with
+// 4), here each wave takes only every eighth block.
+constexpr int NARROW_WAVES = 8;
+constexpr int NARROW_COLS = 32;
+constexpr int NARROW_ROWS = 16;
+constexpr int NARROW_AHEAD = 2;
+
+__global__ __launch_bounds__(NARROW_WAVES* WAVE, 4) void narrow_product_kernel(const ExpertProduct p, int n_tiles)
+{
+    __shared__ float part[NARROW_WAVES][NARROW_ROWS][NARROW_COLS + 1];
+    Place at;
+    if (!(p.E <= 4 * WAVE ? find_tile<NARROW_ROWS, 4>(p.offsets, p.E, p.rows, n_tiles, at)
+                          : find_tile<NARROW_ROWS, 16>(p.offsets, p.E, p.rows, n_tiles, at)))
+        return;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int r = lane & 15, g = lane >> 4;
+    const int KB = p.k / SCALE_BLOCK;
+    const int n0 = at.n_tile * NARROW_COLS;
+    const int nb = (p.n + SCALE_BLOCK - 1) / SCALE_BLOCK;
+    const float* ws = p.ws + ((int64_t)at.e * nb + n0 / SCALE_BLOCK) * KB;
+    // 16-byte pieces g and g + 4 of a row's block, in both operands
+    const uint8_t* w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        w[j] = p.w + ((int64_t)at.e * p.n + min(n0 + j * 16 + r, p.n - 1)) * p.k + g * 16;
+    const int64_t m0 = at.m0 + min(r, at.rows - 1);
+    const uint8_t* x = p.x + m0 * p.k + g * 16;
+    const float* xs = p.xs + m0 * KB;
+    v4u wr[NARROW_AHEAD][2][2], xr[NARROW_AHEAD][2];
+    float sr[NARROW_AHEAD], wsr[NARROW_AHEAD];
+    auto fetch = [&](int block, int u) {
+        const int kb = min(block, KB - 1);
+        const int o = kb * SCALE_BLOCK;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            wr[u][j][0] = *(const v4u*)(w[j] + o);
+            wr[u][j][1] = *(const v4u*)(w[j] + o + 64);
+        }
+        xr[u][0] = *(const v4u*)(x + o);
+        xr[u][1] = *(const v4u*)(x + o + 64);
+        sr[u] = xs[kb];
+        wsr[u] = ws[kb];
+    };
+    auto words = [](const v4u(&a)[2]) {
+        return v8i{(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w,
+                   (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
+    };
+    const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc[2] = {zero, zero};
+#pragma unroll
+    for (int u = 0; u < NARROW_AHEAD; ++u)
+        fetch(wave + u * NARROW_WAVES, u);
+    for (int kb = wave; kb < KB; kb += NARROW_AHEAD * NARROW_WAVES) {
+#pragma unroll
+        for (int u = 0; u < NARROW_AHEAD; ++u) {
+            const int block = kb + u * NARROW_WAVES;
+            if (block >= KB)
+                break;
+            const float scale = sr[u] * wsr[u];
+            v4f t[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                t[j] = product_step(words(wr[u][j]), words(xr[u]), zero);
+            fetch(block + NARROW_AHEAD * NARROW_WAVES, u);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[j][c] = fmaf(t[j][c], scale, acc[j][c]);
+        }
+    }
+    // lane (r, g) has columns 4g .. 4g+3 of each subtile, of token r
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        for (int c = 0; c < 4; ++c)
+            part[wave][r][j * 16 + g * 4 + c] = acc[j][c];
+    __syncthreads();
+    for (int v = threadIdx.x; v < at.rows * (NARROW_COLS / 2); v += NARROW_WAVES * WAVE) {
+        const int m = v / (NARROW_COLS / 2), c = v % (NARROW_COLS / 2) * 2;
+        if (n0 + c >= p.n)
+            continue;
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int q = 0; q < NARROW_WAVES; ++q) {
+            a += part[q][m][c];
+            b += part[q][m][c + 1];
+        }
+        *(uint32_t*)(p.y + (int64_t)(at.m0 + m) * p.n + n0 + c) = bf16_pack(a, b);
+    }
+}
+
+// Workgroups of a launch that covers every way the rows can fall to the
+// experts, for tiles of BM rows: sum of ceil(rows_e / BM) over the experts
+// that can have rows, at most, times the tiles of columns; a multiple of 8.
+inline int64_t workgroups(const ExpertProduct& p, int bm, int n_tiles)
+{
+    const int64_t used = std::min<int64_t>(p.rows, p.E);
+    return (((p.rows - used) / bm + used) * n_tiles + 7) / 8 * 8;
+}
+
+inline dim3 grid_of(int64_t blocks)
+{
+    constexpr int64_t ROW = 1 << 20;              // a grid dimension times the threads stays below 2^32
+    return dim3((uint32_t)std::min(blocks, ROW), (uint32_t)((blocks + ROW - 1) / ROW));
+}
+
+hipError_t launch_narrow(const ExpertProduct& p, hipStream_t stream)
+{
+    const int n_tiles = (p.n + NARROW_COLS - 1) / NARROW_COLS;
+    narrow_product_kernel<<<grid_of(workgroups(p, NARROW_ROWS, n_tiles)), dim3(NARROW_WAVES * WAVE), 0, stream>>>(
+        p, n_tiles);
+    return hipGetLastError();
+}
+
 template <bool GATE_UP, class C, class REST = C>
 hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 {
     const int n_tiles = GATE_UP ? p.n / C::BN : (p.n + C::BN - 1) / C::BN;
-    const int64_t used = p.rows < p.E ? p.rows : p.E;   // experts that can have rows
-    // sum of ceil(rows_e / BM) over the used experts, at most
-    const int64_t m_tiles = (p.rows - used) / C::BM + used;
-    const int64_t grid = (m_tiles * n_tiles + 7) / 8 * 8;
-    constexpr int64_t ROW = 1 << 20;              // a grid dimension times the threads stays below 2^32
-    const dim3 blocks((uint32_t)std::min(grid, ROW), (uint32_t)((grid + ROW - 1) / ROW));
+    const dim3 blocks = grid_of(workgroups(p, C::BM, n_tiles));
     constexpr int ring = std::max(C::RING, REST::RING);
     constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
     const int bytes = std::max(ring + 2 * ((p.k / SCALE_BLOCK + WAVE) & ~(WAVE - 1)) * 4, epi);
@@ -708,12 +822,28 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-// The tile, by the mean number of rows per expert.  With few rows the weights
-// are what costs, each read once: low tiles, several workgroups per CU,
-// nontemporal loads.  With many, the matrix unit: high tiles, whose loads and
-// LDS reads serve more products, and a lower tile for an expert's last rows.
-// Measured (us; 64 experts, n = 7168, k = 2048 for the product, f = 2048,
-// k = 4096 for gate/up, unless said otherwise):
+// The tile.  With few rows per expert the weights are what costs, each read
+// once: low tiles, several workgroups per CU, nontemporal loads.  With many,
+// the matrix unit: high tiles, whose loads and LDS reads serve more products,
+// and a lower tile for an expert's last rows.  And a launch of fewer workgroups
+// than CUs waits for memory step by step: lower tiles, narrower ones, a deeper
+// ring.  Measured (us; E experts, means and rows spread at random):
+//  - the narrow kernel against the 256-column tile with four stages: E 6, rows
+//    8, k 4352, n 944 (180 narrow workgroups) 8.0 against 15; E 7, rows 13, k
+//    6656, n 3016 (665) 27 against 38; E 1, rows 64, k = n = 7168 (896) 51
+//    against 44.  Both sides' cost is proportional to k: the narrow one to its
+//    workgroups times k (32 weight rows each, 4.5 TB/s), the other to its
+//    steps, 0.65 us each.
+//  - four stages against two, one workgroup per CU: gate/up of E 6, rows 9, k
+//    6656, f 768 38 against 55, E 7, rows 479, k 1920, f 640 17.9 against 21.8;
+//    with 430 workgroups (E 2, rows 709, k 1024, n 4416) 17 against 15.
+//  - under 200 workgroups of the higher tile against the lower: E 2, rows 709,
+//    n 4416 64 rows 10.2, 128 (126 workgroups) 12.7, 256 19; E 5, rows 1574, n
+//    1672 12.2, 14.9 (119), 22; gate/up of one expert, rows 2048, f 1024 64
+//    rows 42, 128 (128) 57.  With 202 of 128 (E 17, rows 10740, n 392) 8.2
+//    against 11.2.
+// The rest at 64 experts, n = 7168, k = 2048 for the product, f = 2048, k =
+// 4096 for gate/up, unless said otherwise:
 //  - gate/up of 256 experts, 4 rows each: 604 (16 rows alone 604, 32 alone
 //    609; 16 alone with plain loads 752);
 //  - 32 + 16 against 16 alone, gate/up: mean 9 157 against 181, mean 16 162
@@ -737,14 +867,20 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
         return hipSuccess;
     const int64_t mean = p.rows / p.E;
     constexpr bool EIGHT = !GATE_UP;
+    const int n_tiles = GATE_UP ? p.n / 256 : (p.n + 255) / 256;
+    if (EIGHT && workgroups(p, NARROW_ROWS, (p.n + NARROW_COLS - 1) / NARROW_COLS) <= 720)
+        return launch_narrow(p, stream);
+    if (workgroups(p, 32, n_tiles) <= 256)
+        return launch<GATE_UP, Tile<32, 256, 1, 8, 4, EIGHT, 16, true>, Tile<16, 256, 1, 8, 4, EIGHT, 16, true>>(
+            p, stream);
     if (mean <= 20)
         return launch<GATE_UP, Tile<32, 256, 1, 8, 2, EIGHT, 16, true>, Tile<16, 256, 1, 8, 2, EIGHT, 16, true>>(
             p, stream);
-    if (mean <= 48)
+    if (mean <= 48 || workgroups(p, 128, n_tiles) < 200)
         return launch<GATE_UP, Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, Tile<32, 256, 1, 8, 3, EIGHT, 16, true>>(
             p, stream);
     if constexpr (EIGHT) {
-        if (mean <= 96)
+        if (mean <= 96 || workgroups(p, 256, n_tiles) < 200)
             return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>>(p, stream);
         return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<128, 256, 2, 4, 3, true, 16, false>>(
             p, stream);

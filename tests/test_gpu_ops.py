@@ -344,6 +344,23 @@ def test_products_odd_values(rows):
     assert torch.equal(y[:rows], clean[:rows]) and bool((y[rows:] == 9.0).all())
 
 
+# many workgroups: the tiles that the cases above are too small for
+WIDE_PRODUCTS = [
+    (64, 300, 1024, 256, "even", 3), (64, 400, 1024, 640, "spread", 0), (16, 500, 4096, 256, "spread", 0),
+    (16, 1200, 4096, 128, "spread", 2), (16, 2400, 4096, 384, "spread", 0), (2, 709, 4416, 256, "even", 0),
+    (3, 700, 4600, 128, "first", 1), (1, 64, 7168, 384, "even", 0)]
+
+
+@pytest.mark.parametrize("E,rows,n,k,kind,spare", WIDE_PRODUCTS)
+def test_wide_matmul(E, rows, n, k, kind, spare):
+    test_matmul(E, rows, n, k, kind, spare)
+
+
+@pytest.mark.parametrize("E,rows,n,k,kind,spare", WIDE_PRODUCTS)
+def test_wide_gate_up(E, rows, n, k, kind, spare):
+    test_gate_up(E, rows, n // 256 * 128, k, kind, spare)
+
+
 @pytest.mark.parametrize("rows", [2, 30, 130, 200, 300])
 def test_widest_rows(rows):
     """The widest rows that the calls take: 512 blocks of 128."""
