@@ -738,9 +738,8 @@ __global__ __launch_bounds__(NARROW_WAVES* WAVE, 4) void narrow_product_kernel(c
 #pragma unroll
         for (int u = 0; u < NARROW_AHEAD; ++u) {
             const int block = kb + u * NARROW_WAVES;
-            if (block >= KB)
-                break;
-            const float scale = sr[u] * wsr[u];
+            const bool live = block < KB;                      // a repeated block adds nothing
+            const float scale = live ? sr[u] * wsr[u] : 0.0f;
             v4f t[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -750,7 +749,7 @@ __global__ __launch_bounds__(NARROW_WAVES* WAVE, 4) void narrow_product_kernel(c
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    acc[j][c] = fmaf(t[j][c], scale, acc[j][c]);
+                    acc[j][c] = fmaf(live ? t[j][c] : 0.0f, scale, acc[j][c]);
         }
     }
     // lane (r, g) has columns 4g .. 4g+3 of each subtile, of token r
