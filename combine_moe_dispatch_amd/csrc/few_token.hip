@@ -1,4 +1,4 @@
-// A whole expert layer for a few tokens, in two kernels.
+// A whole expert layer for a few tokens.
 //
 //   x       -> codec (e4m3, scale per 128)
 //   g, u    =  block-scaled products with the chosen expert's gate / up rows
@@ -9,14 +9,21 @@
 // With a few tokens every weight is used once or a few times, so the layer is
 // a stream of the distinct chosen experts' weights; everything else (x, h,
 // scales) is small and stays in L2.  Weights go from HBM straight to the
-// matrix instruction's registers, 16 rows by 128 bytes per instruction; the
-// tokens of an expert (16 columns at a time) are coded on the way in by every
-// wave for itself, which costs the vector unit less than the wait for the
-// weights, and saves a launch and a pass.
+// matrix instruction's registers, 16 rows by 128 bytes per instruction, the
+// tokens of an expert are its columns, 16 at a time.
 //
-// Both kernels work out who needs an expert from topk_idx alone: lane t of a
-// wave looks through token t's K ids (at most 64 tokens).  A token that names
-// an expert twice is one column with the sum of its weights.
+// Few tokens per expert: two kernels; every wave codes its columns on the way
+// in, which costs the vector unit less than the wait for the weights and saves
+// two launches.  More: x and h are coded once, by launches of their own, and
+// the products read the codes; and where the output is too narrow to occupy
+// the chip, the experts of the down product are split over workgroups, whose
+// fp32 parts one more launch adds in order.
+//
+// The product kernels work out who needs an expert from topk_idx alone: lane t
+// of a wave looks through token t's K ids (at most 64 tokens).  A token that
+// names an expert twice is one column with the sum of its weights.
+#include <algorithm>
+
 #include "moe_ops.h"
 #include "ops_common.h"
 
@@ -118,30 +125,37 @@ __device__ inline void own_lds_written()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Coded blocks in a wave's own LDS, at a stride that spreads the reads over the
-// banks: either AHEAD blocks of four columns or one block of sixteen.
+// Coded blocks in a wave's own LDS, AHEAD blocks of FEW columns, at a stride
+// that spreads the reads over the banks.
 constexpr int AHEAD = 2;
-constexpr int FEW = 4;                    // columns of the fast path
+constexpr int FEW = 4;                    // columns that a product kernel codes at a time
+constexpr int DIRECT_TOKENS = 16;         // most tokens that the product kernels code themselves
 constexpr int CODE_STRIDE = SCALE_BLOCK + 16;
 struct Coded {
-    uint8_t codes[16 * CODE_STRIDE];
-    float scale[16];
+    uint8_t codes[AHEAD * FEW * CODE_STRIDE];
+    float scale[AHEAD * FEW];
 };
 
-// Codes four columns' block, rows row .. row+3 of `to`: 16 lanes share a
-// column, eight elements each.
-__device__ inline void encode8(Coded* to, int row, const float (&f)[8])
+// Codes a block that 16 lanes share, eight elements each.
+__device__ inline v2u encode8(const float (&f)[8], float& scale)
 {
-    const int l = threadIdx.x & 15;
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         top = fmaxf(top, fabsf(f[i]));
     top = max16(top);
-    float inv, scale;
+    float inv;
     block_scale(top, inv, scale);
-    const v2u q{e4m3_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                e4m3_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+    return v2u{e4m3_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+               e4m3_pack4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+}
+
+// The same to rows row .. row+3 of `to`.
+__device__ inline void encode8(Coded* to, int row, const float (&f)[8])
+{
+    const int l = threadIdx.x & 15;
+    float scale;
+    const v2u q = encode8(f, scale);
     const int at = row + (threadIdx.x >> 4 & 3);
     *(v2u*)(to->codes + at * CODE_STRIDE + l * 8) = q;
     if (l == 0)
@@ -198,16 +212,79 @@ constexpr int DOWN_WAVES = 8;
 // the 16-byte pieces g and g + 4 of row r; the columns' codes use the same
 // order.
 
-// h[t*K+k][f]: one workgroup per (distinct expert, 16 columns f); its waves
-// share the blocks of H and add up through LDS.  NC: sets of 16 tokens.
-template <int NC>
-__global__ __launch_bounds__(GATE_WAVES* WAVE, NC == 1 ? 4 : 2) void few_gate_up_kernel(const FewTokens p, float* hbuf)
+// Weight rows of 16 columns f of an expert's gate and up products.
+struct GateUpRows {
+    const uint8_t *gate, *up;
+    const float *sg, *su;
+    int KB;
+    __device__ inline GateUpRows(const FewTokens& p, int e, int f0)
+    {
+        const int lane = threadIdx.x & (WAVE - 1);
+        KB = p.H / SCALE_BLOCK;
+        gate = p.w13 + ((int64_t)e * 2 * p.F + f0 + (lane & 15)) * p.H + (lane >> 4) * 16;
+        up = gate + (int64_t)p.F * p.H;
+        sg = p.s13 + ((int64_t)e * (2 * p.F / SCALE_BLOCK) + f0 / SCALE_BLOCK) * KB;
+        su = sg + (int64_t)(p.F / SCALE_BLOCK) * KB;
+    }
+    __device__ inline void fetch(int kb, v4u (&to)[4]) const
+    {
+        const int64_t o = (int64_t)min(kb, KB - 1) * SCALE_BLOCK;
+        to[0] = load16(gate + o);
+        to[1] = load16(gate + o + 64);
+        to[2] = load16(up + o);
+        to[3] = load16(up + o + 64);
+    }
+};
+
+struct DownRows {
+    const uint8_t* down;
+    const float* sd;
+    int FB;
+    __device__ inline DownRows(const FewTokens& p, int e, int n0)
+    {
+        const int lane = threadIdx.x & (WAVE - 1);
+        FB = p.F / SCALE_BLOCK;
+        down = p.w2 + ((int64_t)e * p.H + n0 + (lane & 15)) * p.F + (lane >> 4) * 16;
+        sd = p.s2 + ((int64_t)e * (p.H / SCALE_BLOCK) + n0 / SCALE_BLOCK) * FB;
+    }
+    __device__ inline void fetch(int kb, v4u (&to)[2]) const
+    {
+        const int64_t o = (int64_t)min(kb, FB - 1) * SCALE_BLOCK;
+        to[0] = load16(down + o);
+        to[1] = load16(down + o + 64);
+    }
+};
+
+// acc + t * s, or acc alone for a block that is read only to keep the loop
+// whole (whatever its numbers are).
+__device__ inline void add_block(v4f& acc, const v4f& t, float s, bool live)
+{
+    s = live ? s : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        acc[i] = fmaf(live ? t[i] : 0.0f, s, acc[i]);
+}
+
+// Lane t: the router weight of token t for expert e.
+__device__ inline float weight_of(const FewTokens& p, const int32_t* ids, int e)
+{
+    const int t = threadIdx.x & (WAVE - 1);
+    float w = 0.0f;
+    for (int k = 0; k < p.K; ++k)
+        if (ids[t * p.K + k] == e)
+            w += p.w[t * p.K + k];
+    return w;
+}
+
+// h[t*K+k][f] of up to DIRECT_TOKENS tokens, FEW at a time: one workgroup per (distinct expert, 16
+// columns f); its waves share the blocks of H and add up through LDS.
+__global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const FewTokens p, float* hbuf)
 {
     extern __shared__ int32_t ids[];
     __shared__ uint32_t used[MAX_E_WORDS];
-    __shared__ int32_t cols[MOE_TOKENS];
+    __shared__ int32_t cols[DIRECT_TOKENS];
     __shared__ Coded coded[GATE_WAVES];
-    __shared__ float part[GATE_WAVES][2][NC * 16][17];
+    __shared__ float part[GATE_WAVES][2][FEW][17];
     read_ids(p, ids, used);
     const int e = nth_expert(used, blockIdx.y);
     if (e < 0)
@@ -215,55 +292,34 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, NC == 1 ? 4 : 2) void few_gate_up
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int r = lane & 15, g = lane >> 4;
-    const int KB = p.H / SCALE_BLOCK;
     const int f0 = blockIdx.x * 16;
-    const uint8_t* gate = p.w13 + ((int64_t)e * 2 * p.F + f0 + r) * p.H + g * 16;
-    const uint8_t* up = gate + (int64_t)p.F * p.H;
-    const float* sg = p.s13 + ((int64_t)e * (2 * p.F / SCALE_BLOCK) + f0 / SCALE_BLOCK) * KB;
-    const float* su = sg + (int64_t)(p.F / SCALE_BLOCK) * KB;
+    const GateUpRows rows(p, e, f0);
+    const int KB = rows.KB;
     const int k0 = KB * wave / GATE_WAVES, k1 = KB * (wave + 1) / GATE_WAVES;
     v4u w[AHEAD][4];
-    auto fetch = [&](int kb, v4u(&to)[4]) {
-        const int64_t o = (int64_t)min(kb, KB - 1) * SCALE_BLOCK;
-        to[0] = load16(gate + o);
-        to[1] = load16(gate + o + 64);
-        to[2] = load16(up + o);
-        to[3] = load16(up + o + 64);
-    };
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
-        fetch(k0 + u, w[u]);
+        rows.fetch(k0 + u, w[u]);
     const Member me = member(p, ids, e);
     if (wave == 0)
         list_columns(p, me, cols);
     const int n = __popcll(__ballot(me.is));
     __syncthreads();
-    v4f ag[NC], au[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-        ag[c] = au[c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    auto columns = [&](const Half32& wg, const Half32& wu, int row, float s0, float s1, int c) {
-        const Half32 q = coded_columns(&coded[wave], row, g);
-        const float xs = coded[wave].scale[row];
-        const v4f tg = product(wg, q), tu = product(wu, q);
-        const float a0 = xs * s0, a1 = xs * s1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ag[c][i] = fmaf(tg[i], a0, ag[c][i]);
-            au[c][i] = fmaf(tu[i], a1, au[c][i]);
-        }
-    };
-    if (n <= FEW) {
-        // at most four tokens (by far the most frequent): their rows come
-        // ahead like the weights, and AHEAD blocks are coded at a time
-        const uint16_t* xp = p.x + (int64_t)(cols[min(g, n - 1)] / p.K) * p.H + r * 8;
+    for (int c0 = 0; c0 < n; c0 += FEW) {
+        // the tokens' rows come ahead like the weights; AHEAD blocks are coded at a time
+        const uint16_t* xp = p.x + (int64_t)(cols[min(c0 + g, n - 1)] / p.K) * p.H + r * 8;
         v4u x[AHEAD];
         auto xrows = [&](int kb0) {
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u)
                 x[u] = *(const v4u*)(xp + min(kb0 + u, KB - 1) * SCALE_BLOCK);
         };
+        v4f ag{0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
         xrows(k0);
+        if (c0 > 0)
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                rows.fetch(k0 + u, w[u]);
         for (int kb0 = k0; kb0 < k1; kb0 += AHEAD) {
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
@@ -275,75 +331,69 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, NC == 1 ? 4 : 2) void few_gate_up
             own_lds_written();
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
-                const int kb = min(kb0 + u, KB - 1);
-                const float live = kb0 + u < k1 ? 1.0f : 0.0f;   // a repeated block adds nothing
+                const int kb = min(kb0 + u, KB - 1), row = u * FEW + (r & (FEW - 1));
+                const bool live = kb0 + u < k1;
                 const Half32 wg = convert32(w[u][0], w[u][1]), wu = convert32(w[u][2], w[u][3]);
-                fetch(kb0 + u + AHEAD, w[u]);
-                columns(wg, wu, u * FEW + (r & (FEW - 1)), sg[kb] * live, su[kb] * live, 0);
+                rows.fetch(kb0 + u + AHEAD, w[u]);
+                const Half32 q = coded_columns(&coded[wave], row, g);
+                const float xs = coded[wave].scale[row];
+                add_block(ag, product(wg, q), xs * rows.sg[kb], live);
+                add_block(au, product(wu, q), xs * rows.su[kb], live);
             }
             own_lds_written();
         }
-    } else {
-        for (int kb0 = k0; kb0 < k1; kb0 += AHEAD) {
+        // lane (r, g) has rows 4g .. 4g+3 of column r
+        if (r < FEW)
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const int kb = min(kb0 + u, KB - 1);
-                const float live = kb0 + u < k1 ? 1.0f : 0.0f;
-                const Half32 wg = convert32(w[u][0], w[u][1]), wu = convert32(w[u][2], w[u][3]);
-                fetch(kb0 + u + AHEAD, w[u]);
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (c * 16 >= n)
-                        break;
-                    const int nc = min(16, n - c * 16);
-                    for (int q = 0; q < nc; q += FEW) {
-                        float f[8];
-                        unpack8(*(const v4u*)(p.x + (int64_t)(cols[min(c * 16 + q + g, n - 1)] / p.K) * p.H +
-                                              kb * SCALE_BLOCK + r * 8),
-                                f);
-                        encode8(&coded[wave], q, f);
-                    }
-                    own_lds_written();
-                    columns(wg, wu, r, sg[kb] * live, su[kb] * live, c);
-                    own_lds_written();
-                }
+            for (int i = 0; i < 4; ++i) {
+                part[wave][0][r][g * 4 + i] = ag[i];
+                part[wave][1][r][g * 4 + i] = au[i];
             }
-        }
-    }
-    // lane (r, g) has rows 4g .. 4g+3 of column r
+        __syncthreads();
+        for (int v = threadIdx.x; v < min(n - c0, FEW) * 16; v += GATE_WAVES * WAVE) {
+            const int col = v >> 4, f = v & 15;
+            float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            part[wave][0][c * 16 + r][g * 4 + i] = ag[c][i];
-            part[wave][1][c * 16 + r][g * 4 + i] = au[c][i];
+            for (int q = 0; q < GATE_WAVES; ++q) {
+                a += part[q][0][col][f];
+                b += part[q][1][col][f];
+            }
+            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = a / (1.0f + __expf(-a)) * b;
         }
-    __syncthreads();
-    for (int v = threadIdx.x; v < n * 16; v += GATE_WAVES * WAVE) {
-        const int col = v >> 4, f = v & 15;
-        float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int q = 0; q < GATE_WAVES; ++q) {
-            a += part[q][0][col][f];
-            b += part[q][1][col][f];
-        }
-        hbuf[(int64_t)cols[col] * p.F + f0 + f] = a / (1.0f + __expf(-a)) * b;
+        __syncthreads();
     }
 }
 
-// out[t][n0 .. n0+15] of every token: the waves share the (expert, block of F)
-// pairs in order; a wave adds an expert's finished part, times the router
-// weight, to its own copy of the tile, and the copies are added in order.
-template <int NC>
-__global__ __launch_bounds__(DOWN_WAVES* WAVE, NC == 1 ? 4 : 2) void few_down_kernel(const FewTokens p, const float* hbuf)
+// The tile [T][16] of the output that a workgroup's waves have summed in copies
+// of their own, added in order.
+template <int TOKENS, class Store>
+__device__ inline void join_tile(const float (&tile)[DOWN_WAVES][TOKENS][17], int T, Store store)
+{
+    __syncthreads();
+    for (int v = threadIdx.x; v < T * 8; v += DOWN_WAVES * WAVE) {
+        const int t = v >> 3, n = (v & 7) * 2;
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int q = 0; q < DOWN_WAVES; ++q) {
+            a += tile[q][t][n];
+            b += tile[q][t][n + 1];
+        }
+        store(t, n, a, b);
+    }
+}
+
+// out[t][n0 .. n0+15] of up to DIRECT_TOKENS tokens: the waves share the (expert, block
+// of F) pairs in order; a wave adds an expert's finished part, times the router
+// weight, to its own copy of the tile.
+__global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const FewTokens p, const float* hbuf)
 {
     extern __shared__ int32_t ids[];
     __shared__ uint32_t used[MAX_E_WORDS];
-    __shared__ int32_t cols[DOWN_WAVES][MOE_TOKENS];
-    __shared__ float weight[DOWN_WAVES][MOE_TOKENS];
+    __shared__ int32_t cols[DOWN_WAVES][DIRECT_TOKENS];
+    __shared__ float weight[DOWN_WAVES][DIRECT_TOKENS];
     __shared__ Coded coded[DOWN_WAVES];
-    __shared__ float tile[DOWN_WAVES][NC * 16][17];
-    for (int i = threadIdx.x; i < DOWN_WAVES * NC * 16 * 17; i += DOWN_WAVES * WAVE)
+    __shared__ float tile[DOWN_WAVES][DIRECT_TOKENS][17];
+    for (int i = threadIdx.x; i < DOWN_WAVES * DIRECT_TOKENS * 17; i += DOWN_WAVES * WAVE)
         (&tile[0][0][0])[i] = 0.0f;
     read_ids(p, ids, used);
     const int lane = threadIdx.x & (WAVE - 1);
@@ -357,45 +407,18 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, NC == 1 ? 4 : 2) void few_down_ke
         const int u0 = q / FB;
         const int kb0 = q - u0 * FB, kb1 = min(FB, kb0 + q1 - q);
         const int e = nth_expert(used, u0);
-        const uint8_t* down = p.w2 + ((int64_t)e * p.H + n0 + r) * p.F + g * 16;
-        const float* sd = p.s2 + ((int64_t)e * (p.H / SCALE_BLOCK) + n0 / SCALE_BLOCK) * FB;
+        const DownRows rows(p, e, n0);
         v4u w[AHEAD][2];
-        auto fetch = [&](int kb, v4u(&to)[2]) {
-            const int64_t o = (int64_t)min(kb, FB - 1) * SCALE_BLOCK;
-            to[0] = load16(down + o);
-            to[1] = load16(down + o + 64);
-        };
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
-            fetch(kb0 + u, w[u]);
+            rows.fetch(kb0 + u, w[u]);
         const Member me = member(p, ids, e);
         const int n = list_columns(p, me, cols[wave]);
-        if (me.is) {                            // the token's weight for this expert
-            float mine = 0.0f;
-            for (int k = 0; k < p.K; ++k)
-                if (ids[lane * p.K + k] == e)
-                    mine += p.w[lane * p.K + k];
-            weight[wave][lane] = mine;
-        }
+        if (me.is)
+            weight[wave][lane] = weight_of(p, ids, e);
         own_lds_written();
-        v4f acc[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            acc[c] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        auto columns = [&](const Half32& wd, int row, float s0, int c) {
-            const Half32 hq = coded_columns(&coded[wave], row, g);
-            const float s = coded[wave].scale[row] * s0;
-            const v4f t = product(wd, hq);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[c][i] = fmaf(t[i], s, acc[c][i]);
-        };
-        auto encode_h = [&](const v4f(&v)[2], int row) {
-            const float f[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-            encode8(&coded[wave], row, f);
-        };
-        if (n <= FEW) {
-            const float* hp = hbuf + (int64_t)cols[wave][min(g, n - 1)] * p.F + r * 8;
+        for (int c0 = 0; c0 < n; c0 += FEW) {
+            const float* hp = hbuf + (int64_t)cols[wave][min(c0 + g, n - 1)] * p.F + r * 8;
             v4f hv[AHEAD][2];
             auto hrows = [&](int k) {
 #pragma unroll
@@ -405,84 +428,345 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, NC == 1 ? 4 : 2) void few_down_ke
                     hv[u][1] = h[1];
                 }
             };
+            v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
             hrows(kb0);
-            for (int k = kb0; k < kb1; k += AHEAD) {
+            if (c0 > 0)
 #pragma unroll
                 for (int u = 0; u < AHEAD; ++u)
-                    encode_h(hv[u], u * FEW);
+                    rows.fetch(kb0 + u, w[u]);
+            for (int k = kb0; k < kb1; k += AHEAD) {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    const float f[8] = {hv[u][0].x, hv[u][0].y, hv[u][0].z, hv[u][0].w,
+                                        hv[u][1].x, hv[u][1].y, hv[u][1].z, hv[u][1].w};
+                    encode8(&coded[wave], u * FEW, f);
+                }
                 hrows(k + AHEAD);
                 own_lds_written();
 #pragma unroll
                 for (int u = 0; u < AHEAD; ++u) {
-                    const float s0 = k + u < kb1 ? sd[min(k + u, FB - 1)] : 0.0f;
+                    const int row = u * FEW + (r & (FEW - 1));
+                    const float s = coded[wave].scale[row] * rows.sd[min(k + u, FB - 1)];
                     const Half32 wd = convert32(w[u][0], w[u][1]);
-                    fetch(k + u + AHEAD, w[u]);
-                    columns(wd, u * FEW + (r & (FEW - 1)), s0, 0);
+                    rows.fetch(k + u + AHEAD, w[u]);
+                    add_block(acc, product(wd, coded_columns(&coded[wave], row, g)), s, k + u < kb1);
                 }
                 own_lds_written();
             }
-        } else {
-            for (int k = kb0; k < kb1; k += AHEAD) {
-#pragma unroll
-                for (int u = 0; u < AHEAD; ++u) {
-                    const int kb = min(k + u, FB - 1);
-                    const float s0 = k + u < kb1 ? sd[kb] : 0.0f;
-                    const Half32 wd = convert32(w[u][0], w[u][1]);
-                    fetch(k + u + AHEAD, w[u]);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        if (c * 16 >= n)
-                            break;
-                        const int nc = min(16, n - c * 16);
-                        for (int i = 0; i < nc; i += FEW) {
-                            const v4f* h = (const v4f*)(hbuf + (int64_t)cols[wave][min(c * 16 + i + g, n - 1)] * p.F +
-                                                        kb * SCALE_BLOCK + r * 8);
-                            const v4f v[2] = {h[0], h[1]};
-                            encode_h(v, i);
-                        }
-                        own_lds_written();
-                        columns(wd, r, s0, c);
-                        own_lds_written();
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (c * 16 + r < n) {
-                const int t = cols[wave][c * 16 + r] / p.K;
+            if (r < FEW && c0 + r < n) {
+                const int t = cols[wave][c0 + r] / p.K;
                 const float wt = weight[wave][t];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    tile[wave][t][g * 4 + i] += wt * acc[c][i];
+                    tile[wave][t][g * 4 + i] += wt * acc[i];
             }
+        }
         own_lds_written();
         q += kb1 - kb0;
     }
-    __syncthreads();
-    for (int v = threadIdx.x; v < p.T * 8; v += DOWN_WAVES * WAVE) {
-        const int t = v >> 3, n = (v & 7) * 2;
-        float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int q = 0; q < DOWN_WAVES; ++q) {
-            a += tile[q][t][n];
-            b += tile[q][t][n + 1];
-        }
+    join_tile(tile, p.T, [&](int t, int n, float a, float b) {
         *(uint32_t*)(p.out + (int64_t)t * p.H + n0 + n) = bf16_pack(a, b);
+    });
+}
+
+// ---- more tokens: codes made once ----
+
+__device__ inline void read8(const uint16_t* from, float (&f)[8]) { unpack8(*(const v4u*)from, f); }
+__device__ inline void read8(const float* from, float (&f)[8])
+{
+    const v4f a = *(const v4f*)from, b = *(const v4f*)(from + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[i] = a[i];
+        f[4 + i] = b[i];
     }
 }
 
-template <int NC>
+constexpr int CODE_THREADS = 256;
+template <class V>
+__global__ __launch_bounds__(CODE_THREADS) void code_kernel(const V* from, int64_t blocks, uint8_t* codes, float* scales)
+{
+    const int64_t b = (int64_t)blockIdx.x * (CODE_THREADS / 16) + threadIdx.x / 16;
+    if (b >= blocks)
+        return;
+    const int64_t at = b * SCALE_BLOCK + (threadIdx.x & 15) * 8;
+    float f[8], scale;
+    read8(from + at, f);
+    *(v2u*)(codes + at) = encode8(f, scale);
+    if ((threadIdx.x & 15) == 0)
+        scales[b] = scale;
+}
+
+// Blocks of 16 coded rows as the product's columns, AHEAD at a time.
+struct CodedRows {
+    const uint8_t* codes;
+    const float* scales;
+    int blocks;
+    v4u q[AHEAD][2];
+    float s[AHEAD];
+    __device__ inline CodedRows(const uint8_t* code_rows, const float* scale_rows, int64_t row, int blocks_)
+        : codes(code_rows + row * blocks_ * SCALE_BLOCK + ((threadIdx.x & (WAVE - 1)) >> 4) * 16),
+          scales(scale_rows + row * blocks_), blocks(blocks_)
+    {
+    }
+    __device__ inline void fetch(int u, int kb)
+    {
+        kb = min(kb, blocks - 1);
+        q[u][0] = load16(codes + kb * SCALE_BLOCK);
+        q[u][1] = load16(codes + kb * SCALE_BLOCK + 64);
+        s[u] = scales[kb];
+    }
+};
+
+// h as above, 16 columns at a time (an expert with more reads its weights
+// again, from the caches: 32 at a time, with fewer waves in flight, took 1475
+// us against 1258 for 32 tokens of the 256-expert layer, and 77 against 83 for
+// 64 tokens of one with 8 experts).
+__global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void coded_gate_up_kernel(const FewTokens p, const uint8_t* xq,
+                                                                             const float* xs, float* hbuf)
+{
+    extern __shared__ int32_t ids[];
+    __shared__ uint32_t used[MAX_E_WORDS];
+    __shared__ int32_t cols[MOE_TOKENS];
+    __shared__ float part[GATE_WAVES][2][16][17];
+    read_ids(p, ids, used);
+    const int e = nth_expert(used, blockIdx.y);
+    if (e < 0)
+        return;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int r = lane & 15, g = lane >> 4;
+    const int f0 = blockIdx.x * 16;
+    const GateUpRows rows(p, e, f0);
+    const int KB = rows.KB;
+    const int k0 = KB * wave / GATE_WAVES, k1 = KB * (wave + 1) / GATE_WAVES;
+    v4u w[AHEAD][4];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        rows.fetch(k0 + u, w[u]);
+    const Member me = member(p, ids, e);
+    if (wave == 0)
+        list_columns(p, me, cols);
+    const int n = __popcll(__ballot(me.is));
+    __syncthreads();
+    for (int c0 = 0; c0 < n; c0 += 16) {
+        CodedRows x(xq, xs, cols[min(c0 + r, n - 1)] / p.K, KB);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            x.fetch(u, k0 + u);
+            if (c0 > 0)
+                rows.fetch(k0 + u, w[u]);
+        }
+        v4f ag{0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
+        for (int kb0 = k0; kb0 < k1; kb0 += AHEAD)
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int kb = min(kb0 + u, KB - 1);
+                const bool live = kb0 + u < k1;
+                const Half32 wg = convert32(w[u][0], w[u][1]), wu = convert32(w[u][2], w[u][3]);
+                rows.fetch(kb0 + u + AHEAD, w[u]);
+                const Half32 q = convert32(x.q[u][0], x.q[u][1]);
+                add_block(ag, product(wg, q), x.s[u] * rows.sg[kb], live);
+                add_block(au, product(wu, q), x.s[u] * rows.su[kb], live);
+                x.fetch(u, kb0 + u + AHEAD);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            part[wave][0][r][g * 4 + i] = ag[i];
+            part[wave][1][r][g * 4 + i] = au[i];
+        }
+        __syncthreads();
+        for (int v = threadIdx.x; v < min(n - c0, 16) * 16; v += GATE_WAVES * WAVE) {
+            const int col = v >> 4, f = v & 15;
+            float a = 0.0f, b = 0.0f;
+#pragma unroll
+            for (int q = 0; q < GATE_WAVES; ++q) {
+                a += part[q][0][col][f];
+                b += part[q][1][col][f];
+            }
+            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = a / (1.0f + __expf(-a)) * b;
+        }
+        __syncthreads();
+    }
+}
+
+// The down product as above; workgroup (x, y) takes its share of the (expert,
+// block) pairs.  One share: the result; else fp32 parts [share][T][H].
+__global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const FewTokens p, const uint8_t* hq,
+                                                                          const float* hs, float* parts)
+{
+    extern __shared__ int32_t ids[];
+    __shared__ uint32_t used[MAX_E_WORDS];
+    __shared__ int32_t cols[DOWN_WAVES][MOE_TOKENS];
+    __shared__ float weight[DOWN_WAVES][MOE_TOKENS];
+    __shared__ float tile[DOWN_WAVES][MOE_TOKENS][17];
+    for (int i = threadIdx.x; i < DOWN_WAVES * MOE_TOKENS * 17; i += DOWN_WAVES * WAVE)
+        (&tile[0][0][0])[i] = 0.0f;
+    read_ids(p, ids, used);
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int r = lane & 15, g = lane >> 4;
+    const int FB = p.F / SCALE_BLOCK;
+    const int n0 = blockIdx.x * 16;
+    const int pairs = count_experts(used) * FB;
+    const int at = blockIdx.y * DOWN_WAVES + wave, shares = gridDim.y * DOWN_WAVES;
+    const int q0 = (int)((int64_t)pairs * at / shares), q1 = (int)((int64_t)pairs * (at + 1) / shares);
+    for (int q = q0; q < q1;) {
+        const int u0 = q / FB;
+        const int kb0 = q - u0 * FB, kb1 = min(FB, kb0 + q1 - q);
+        const int e = nth_expert(used, u0);
+        const DownRows rows(p, e, n0);
+        v4u w[AHEAD][2];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            rows.fetch(kb0 + u, w[u]);
+        const Member me = member(p, ids, e);
+        const int n = list_columns(p, me, cols[wave]);
+        if (me.is)
+            weight[wave][lane] = weight_of(p, ids, e);
+        own_lds_written();
+        for (int c0 = 0; c0 < n; c0 += 16) {
+            CodedRows h(hq, hs, cols[wave][min(c0 + r, n - 1)], FB);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                h.fetch(u, kb0 + u);
+                if (c0 > 0)
+                    rows.fetch(kb0 + u, w[u]);
+            }
+            v4f acc{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = kb0; k < kb1; k += AHEAD)
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    const float sd = rows.sd[min(k + u, FB - 1)];
+                    const Half32 wd = convert32(w[u][0], w[u][1]);
+                    rows.fetch(k + u + AHEAD, w[u]);
+                    add_block(acc, product(wd, convert32(h.q[u][0], h.q[u][1])), h.s[u] * sd, k + u < kb1);
+                    h.fetch(u, k + u + AHEAD);
+                }
+            if (c0 + r < n) {
+                const int t = cols[wave][c0 + r] / p.K;
+                const float wt = weight[wave][t];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tile[wave][t][g * 4 + i] += wt * acc[i];
+            }
+        }
+        own_lds_written();
+        q += kb1 - kb0;
+    }
+    join_tile(tile, p.T, [&](int t, int n, float a, float b) {
+        const int64_t o = (int64_t)t * p.H + n0 + n;
+        if (gridDim.y == 1)
+            *(uint32_t*)(p.out + o) = bf16_pack(a, b);
+        else
+            *(float2*)(parts + (int64_t)blockIdx.y * p.T * p.H + o) = float2{a, b};
+    });
+}
+
+__global__ __launch_bounds__(CODE_THREADS) void add_parts_kernel(const float* parts, int shares, int64_t elements,
+                                                                 uint16_t* out)
+{
+    const int64_t at = ((int64_t)blockIdx.x * CODE_THREADS + threadIdx.x) * 4;
+    if (at >= elements)
+        return;
+    v4f sum{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < shares; ++s) {
+        const v4f v = *(const v4f*)(parts + s * elements + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sum[i] += v[i];
+    }
+    *(v2u*)(out + at) = v2u{bf16_pack(sum[0], sum[1]), bf16_pack(sum[2], sum[3])};
+}
+
+// Whether the product kernels code their columns themselves: when an expert
+// has few of them.  Measured (us, direct against coded): 16 tokens, 64 experts,
+// top 4, hidden 4096, f 2048 194 against 198; 8 tokens, 8 experts, top 2 41
+// against 54; 13 tokens of hidden 6400, f 256, 117 experts, top 2 38 against
+// 46; but 29 tokens, 5 experts, top 5, hidden 1024, f 1536 65 against 44, 32
+// tokens, 8 experts, top 2, hidden 4096 90 against 60, and 64 tokens of the
+// 256-expert layer 2146 against 1874.
+inline bool direct(const FewTokens& p)
+{
+    return p.T <= FEW || (p.T <= DIRECT_TOKENS && p.T * p.K <= FEW * p.E);
+}
+
+// Shares of the down product: about two workgroups per CU, and no more shares
+// than the most experts.  61 tokens, 177 experts, hidden 384 (24 workgroups
+// without): 152 -> 74 us; with twice as many shares 32 tokens, 8 experts,
+// hidden 4096 took 66 against 60.
+inline int down_shares(int T, int K, int H)
+{
+    const int wide = H / 16;
+    return std::max(1, std::min({(512 + wide / 2) / wide, 16, T * K}));
+}
+
+// The workspace: h in fp32, and where x and h may be coded once their codes,
+// scales and the parts.
+struct Workspace {
+    size_t h = 0, xq = 0, hq = 0, parts = 0, xs = 0, hs = 0, bytes = 0;
+    Workspace(int T, int K, int H, int F)
+    {
+        const size_t x = (size_t)T * H, items = (size_t)T * K * F;
+        const int shares = down_shares(T, K, H);
+        bytes = items * 4;
+        if (T <= FEW)
+            return;
+        auto take = [&](size_t n) {
+            const size_t at = bytes;
+            bytes += (n + 15) / 16 * 16;
+            return at;
+        };
+        xq = take(x);
+        hq = take(items);
+        parts = take(shares > 1 ? shares * x * 4 : 0);
+        xs = take(x / SCALE_BLOCK * 4);
+        hs = take(items / SCALE_BLOCK * 4);
+    }
+};
+
 hipError_t few(const FewTokens& p, hipStream_t stream)
 {
     float* hbuf = (float*)p.workspace;
     const int experts = p.T * p.K < p.E ? p.T * p.K : p.E;     // distinct ones, at most
     const uint32_t ids = (uint32_t)(p.T * p.K) * 4;
-    few_gate_up_kernel<NC><<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, hbuf);
+    few_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, hbuf);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    few_down_kernel<NC><<<dim3(p.H / 16), dim3(DOWN_WAVES * WAVE), ids, stream>>>(p, hbuf);
+    few_down_kernel<<<dim3(p.H / 16), dim3(DOWN_WAVES * WAVE), ids, stream>>>(p, hbuf);
+    return hipGetLastError();
+}
+
+hipError_t coded(const FewTokens& p, hipStream_t stream)
+{
+    const Workspace at(p.T, p.K, p.H, p.F);
+    uint8_t* ws = (uint8_t*)p.workspace;
+    float *hbuf = (float*)(ws + at.h), *xs = (float*)(ws + at.xs), *hs = (float*)(ws + at.hs);
+    float* parts = (float*)(ws + at.parts);
+    const int experts = p.T * p.K < p.E ? p.T * p.K : p.E;
+    const int shares = down_shares(p.T, p.K, p.H);
+    const uint32_t ids = (uint32_t)(p.T * p.K) * 4;
+    const int64_t x = (int64_t)p.T * p.H;
+    auto grid = [](int64_t n, int per) { return dim3((uint32_t)((n + per - 1) / per)); };
+    const int64_t xb = x / SCALE_BLOCK, hb = (int64_t)p.T * p.K * p.F / SCALE_BLOCK;
+    code_kernel<<<grid(xb, CODE_THREADS / 16), dim3(CODE_THREADS), 0, stream>>>(p.x, xb, ws + at.xq, xs);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    coded_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, ws + at.xq, xs, hbuf);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    code_kernel<<<grid(hb, CODE_THREADS / 16), dim3(CODE_THREADS), 0, stream>>>((const float*)hbuf, hb, ws + at.hq, hs);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    coded_down_kernel<<<dim3(p.H / 16, shares), dim3(DOWN_WAVES * WAVE), ids, stream>>>(p, ws + at.hq, hs, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess || shares == 1)
+        return e;
+    add_parts_kernel<<<grid(x, CODE_THREADS * 4), dim3(CODE_THREADS), 0, stream>>>(parts, shares, x, p.out);
     return hipGetLastError();
 }
 
@@ -490,19 +774,14 @@ hipError_t few(const FewTokens& p, hipStream_t stream)
 
 size_t few_token_workspace(int T, int K, int H, int F)
 {
-    (void)H;
-    return (size_t)T * K * F * sizeof(float);
+    return Workspace(T, K, H, F).bytes;
 }
 
 hipError_t launch_few_token_layer(const FewTokens& p, hipStream_t stream)
 {
     if (p.T == 0)
         return hipSuccess;
-    if (p.T <= 16)
-        return few<1>(p, stream);
-    if (p.T <= 32)
-        return few<2>(p, stream);
-    return few<4>(p, stream);
+    return direct(p) ? few(p, stream) : coded(p, stream);
 }
 
 }  // namespace ops

@@ -472,6 +472,17 @@ def test_few(T, E, K, H, F):
     check_few(run_few(*ins), *few_ref(*ins))
 
 
+@pytest.mark.parametrize("T", [3, 13, 16, 21, 50])
+def test_few_one_expert(T):
+    """Every token names the same expert, and one more each."""
+    say(f"[gpu] few, one expert T={T}")
+    E, K, H, F = 64, 2, 384, 256
+    x, idx, w, *wts = few_inputs(rng(16, T), T, E, K, H, F)
+    idx[:, 1] = 7
+    idx[:, 0] = np.where(np.arange(T) % 3 == 0, 7, (np.arange(T) * 5) % E)
+    check_few(run_few(x, idx, w, *wts), *few_ref(x, idx, w, *wts))
+
+
 def test_few_padding_and_repeats():
     """Ids outside the experts name none; a token with none gets zeros; an
     expert named twice counts twice; what pads a batch cannot reach it."""
