@@ -27,7 +27,8 @@ __device__ inline void store_row(const v4u& v, v4u* p)
 //
 // One pass: a row is read once, stays in registers as fp32 (V vectors of 8
 // elements per thread) through the sum of squares, and every output is
-// written from there.  A row belongs to W waves; the norm is of the fp32 sum,
+// written from there.  A row belongs to one or more waves, a short one to LANES
+// lanes of a wave; the norm is of the fp32 sum,
 // not of its bf16 rounding, and the codes are of the fp32 result, not of y's
 // bf16 rounding, so each output is rounded once.
 // ---------------------------------------------------------------------------
@@ -44,17 +45,17 @@ struct NormArgs {
     float* ys;
 };
 
-template <int V, bool STREAM>
+template <int V, bool STREAM, int LANES>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int waves_per_row)
 {
     __shared__ float part[16];
-    const int lane = threadIdx.x & (WAVE - 1);
-    const int wave = threadIdx.x / WAVE;
-    const int per_block = blockDim.x / WAVE / waves_per_row;
+    const int lane = threadIdx.x % LANES;
+    const int wave = threadIdx.x / LANES;
+    const int per_block = blockDim.x / LANES / waves_per_row;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int64_t row = block * per_block + wave / waves_per_row;
-    const int t = (wave % waves_per_row) * WAVE + lane;      // thread of the row
-    const int nt = waves_per_row * WAVE;
+    const int t = (wave % waves_per_row) * LANES + lane;     // thread of the row
+    const int nt = waves_per_row * LANES;
     const bool live = row < a.rows;
     const int64_t at = row * a.hidden;
     float s[V][8];
@@ -80,9 +81,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
             sum = fmaf(s[u][2 * c + 1], s[u][2 * c + 1], sum);
         }
 #pragma unroll
-    for (int d = WAVE / 2; d; d >>= 1)
-        sum += __shfl_xor(sum, d, WAVE);
-    if (waves_per_row > 1) {
+    for (int d = LANES / 2; d; d >>= 1)
+        sum += __shfl_xor(sum, d, LANES);
+    if (LANES == WAVE && waves_per_row > 1) {
         if (lane == 0)
             part[wave] = sum;
         __syncthreads();
@@ -354,6 +355,24 @@ inline dim3 grid_of(int64_t blocks)
 
 }  // namespace
 
+template <int V, bool STREAM, int LANES>
+static hipError_t norm_lanes(const NormArgs& a, hipStream_t stream)
+{
+    constexpr int PER = 256 / LANES;
+    add_rmsnorm_kernel<V, STREAM, LANES><<<grid_of((a.rows + PER - 1) / PER), dim3(256), 0, stream>>>(a, 1);
+    return hipGetLastError();
+}
+
+// short rows: several to a workgroup of up to four waves
+template <int V, bool STREAM>
+static hipError_t norm_waves(const NormArgs& a, int waves, hipStream_t stream)
+{
+    const int per = waves < 4 ? 4 / waves : 1;
+    add_rmsnorm_kernel<V, STREAM, WAVE>
+        <<<grid_of((a.rows + per - 1) / per), dim3(per * waves * WAVE), 0, stream>>>(a, waves);
+    return hipGetLastError();
+}
+
 hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const uint16_t* residual,
                               const uint16_t* weight, float eps, uint16_t* residual_out, uint16_t* y,
                               uint8_t* yq, float* ys, hipStream_t stream_)
@@ -365,22 +384,19 @@ hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const
     // 4096, 512 MB, take 172 us with the hint and 180 without; 4096 rows of
     // 7168 with a residual, 118 MB, 46.5 with it and 41.8 without.
     const bool stream = rows * hidden * 2 * (residual ? 2 : 1) > (int64_t)256 << 20;
+    // Up to 512 elements, some lanes of a wave per row: 65536 rows of 32 with a
+    // residual 7.5 us against 26 with a wave each, of 128 with codes 13.6 against
+    // 36, of 384 23.8 against 38.
+    if (a.vecs <= 4)
+        return stream ? norm_lanes<1, true, 4>(a, stream_) : norm_lanes<1, false, 4>(a, stream_);
+    if (a.vecs <= 16)
+        return stream ? norm_lanes<1, true, 16>(a, stream_) : norm_lanes<1, false, 16>(a, stream_);
+    if (a.vecs <= 64)
+        return stream ? norm_lanes<4, true, 16>(a, stream_) : norm_lanes<4, false, 16>(a, stream_);
     const int waves = (a.vecs + 2 * WAVE - 1) / (2 * WAVE);     // at two vectors per thread
-    if (waves <= 16) {
-        // short rows: several to a workgroup of up to four waves
-        const int per = waves < 4 ? 4 / waves : 1;
-        const dim3 grid = grid_of((rows + per - 1) / per), block(per * waves * WAVE);
-        if (stream)
-            add_rmsnorm_kernel<2, true><<<grid, block, 0, stream_>>>(a, waves);
-        else
-            add_rmsnorm_kernel<2, false><<<grid, block, 0, stream_>>>(a, waves);
-    } else {
-        if (stream)
-            add_rmsnorm_kernel<8, true><<<grid_of(rows), dim3(1024), 0, stream_>>>(a, 16);
-        else
-            add_rmsnorm_kernel<8, false><<<grid_of(rows), dim3(1024), 0, stream_>>>(a, 16);
-    }
-    return hipGetLastError();
+    if (waves <= 16)
+        return stream ? norm_waves<2, true>(a, waves, stream_) : norm_waves<2, false>(a, waves, stream_);
+    return stream ? norm_waves<8, true>(a, 16, stream_) : norm_waves<8, false>(a, 16, stream_);
 }
 
 template <int G, int V>

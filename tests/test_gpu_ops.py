@@ -62,7 +62,8 @@ def check_norm(x, r, w, y, yq, ys, ro, eps):
 
 
 NORM_SHAPES = [(1, 8), (3, 24), (5, 128), (2, 136), (7, 1024), (9, 1032), (1, 4096), (3, 7168),
-               (2, 16384), (2, 16392), (1, 65536), (513, 256), (130, 7168)]
+               (2, 16384), (2, 16392), (1, 65536), (513, 256), (130, 7168),
+               (131, 32), (65, 40), (37, 384), (35, 504), (33, 512), (9, 520)]
 
 
 @pytest.mark.parametrize("rows,hidden", NORM_SHAPES)
