@@ -208,6 +208,19 @@ def test_route_masks(renorm):
     check_route(torch.from_numpy(z).to(DEV), E, K, renorm)
 
 
+@pytest.mark.parametrize("T,E,K", [(16385, 100, 8), (16390, 128, 64), (16400, 65, 3), (1003, 16, 16), (77, 12, 5),
+                                   (4099, 33, 12)])
+def test_route_many_tokens(T, E, K):
+    say(f"[gpu] route T={T} E={E} K={K}")
+    g = rng(17, T, E)
+    z = np.round(2 * g.standard_normal((T, E))) / 2                # many ties
+    z[g.random((T, E)) < 0.2] = -np.inf
+    z[::97] = -np.inf
+    z[5::101] = np.nan
+    check_route(torch.from_numpy(z.astype(np.float32)).to(DEV), E, K, True)
+    check_route(torch.from_numpy(z.astype(np.float32)).to(torch.bfloat16).to(DEV), E, K, False)
+
+
 # --- products -------------------------------------------------------------------------------------
 
 def counts_of(kind, E, rows, g):
