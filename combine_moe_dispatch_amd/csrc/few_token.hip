@@ -365,12 +365,13 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const 
 }
 
 // The tile [T][16] of the output that a workgroup's waves have summed in copies
-// of their own, added in order.
-template <int TOKENS, class Store>
-__device__ inline void join_tile(const float (&tile)[DOWN_WAVES][TOKENS][17], int T, Store store)
+// of their own, added in order: the result, or with several shares this one's
+// part of it, [share][T][H] in fp32.
+template <bool SPLIT, int TOKENS>
+__device__ inline void join_tile(const FewTokens& p, const float (&tile)[DOWN_WAVES][TOKENS][17], int n0, float* parts)
 {
     __syncthreads();
-    for (int v = threadIdx.x; v < T * 8; v += DOWN_WAVES * WAVE) {
+    for (int v = threadIdx.x; v < p.T * 8; v += DOWN_WAVES * WAVE) {
         const int t = v >> 3, n = (v & 7) * 2;
         float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -378,14 +379,29 @@ __device__ inline void join_tile(const float (&tile)[DOWN_WAVES][TOKENS][17], in
             a += tile[q][t][n];
             b += tile[q][t][n + 1];
         }
-        store(t, n, a, b);
+        const int64_t o = (int64_t)t * p.H + n0 + n;
+        if (SPLIT)
+            *(float2*)(parts + (int64_t)blockIdx.y * p.T * p.H + o) = float2{a, b};
+        else
+            *(uint32_t*)(p.out + o) = bf16_pack(a, b);
     }
 }
 
-// out[t][n0 .. n0+15] of up to DIRECT_TOKENS tokens: the waves share the (expert, block
-// of F) pairs in order; a wave adds an expert's finished part, times the router
+// The (expert, block of F) pairs of this wave, in order, of those that the
+// shares' waves divide among them.
+template <bool SPLIT>
+__device__ inline int share_start(int pairs, int wave)
+{
+    const int at = SPLIT ? blockIdx.y * DOWN_WAVES + wave : wave;
+    return (int)((int64_t)pairs * at / (SPLIT ? (int)gridDim.y * DOWN_WAVES : DOWN_WAVES));
+}
+
+// out[t][n0 .. n0+15] of up to DIRECT_TOKENS tokens: the waves of the workgroups
+// (n0, share) divide the (expert, block of F) pairs in order; a wave adds an expert's finished part, times the router
 // weight, to its own copy of the tile.
-__global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const FewTokens p, const float* hbuf)
+template <bool SPLIT>
+__global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const FewTokens p, const float* hbuf,
+                                                                       float* parts)
 {
     extern __shared__ int32_t ids[];
     __shared__ uint32_t used[MAX_E_WORDS];
@@ -402,7 +418,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const Few
     const int FB = p.F / SCALE_BLOCK;
     const int n0 = blockIdx.x * 16;
     const int pairs = count_experts(used) * FB;
-    const int q0 = (int)((int64_t)pairs * wave / DOWN_WAVES), q1 = (int)((int64_t)pairs * (wave + 1) / DOWN_WAVES);
+    const int q0 = share_start<SPLIT>(pairs, wave), q1 = share_start<SPLIT>(pairs, wave + 1);
     for (int q = q0; q < q1;) {
         const int u0 = q / FB;
         const int kb0 = q - u0 * FB, kb1 = min(FB, kb0 + q1 - q);
@@ -464,9 +480,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const Few
         own_lds_written();
         q += kb1 - kb0;
     }
-    join_tile(tile, p.T, [&](int t, int n, float a, float b) {
-        *(uint32_t*)(p.out + (int64_t)t * p.H + n0 + n) = bf16_pack(a, b);
-    });
+    join_tile<SPLIT>(p, tile, n0, parts);
 }
 
 // ---- more tokens: codes made once ----
@@ -590,8 +604,8 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void coded_gate_up_kernel(cons
     }
 }
 
-// The down product as above; workgroup (x, y) takes its share of the (expert,
-// block) pairs.  One share: the result; else fp32 parts [share][T][H].
+// The down product as above.
+template <bool SPLIT>
 __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const FewTokens p, const uint8_t* hq,
                                                                           const float* hs, float* parts)
 {
@@ -609,8 +623,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const F
     const int FB = p.F / SCALE_BLOCK;
     const int n0 = blockIdx.x * 16;
     const int pairs = count_experts(used) * FB;
-    const int at = blockIdx.y * DOWN_WAVES + wave, shares = gridDim.y * DOWN_WAVES;
-    const int q0 = (int)((int64_t)pairs * at / shares), q1 = (int)((int64_t)pairs * (at + 1) / shares);
+    const int q0 = share_start<SPLIT>(pairs, wave), q1 = share_start<SPLIT>(pairs, wave + 1);
     for (int q = q0; q < q1;) {
         const int u0 = q / FB;
         const int kb0 = q - u0 * FB, kb1 = min(FB, kb0 + q1 - q);
@@ -654,13 +667,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const F
         own_lds_written();
         q += kb1 - kb0;
     }
-    join_tile(tile, p.T, [&](int t, int n, float a, float b) {
-        const int64_t o = (int64_t)t * p.H + n0 + n;
-        if (gridDim.y == 1)
-            *(uint32_t*)(p.out + o) = bf16_pack(a, b);
-        else
-            *(float2*)(parts + (int64_t)blockIdx.y * p.T * p.H + o) = float2{a, b};
-    });
+    join_tile<SPLIT>(p, tile, n0, parts);
 }
 
 __global__ __launch_bounds__(CODE_THREADS) void add_parts_kernel(const float* parts, int shares, int64_t elements,
@@ -691,14 +698,17 @@ inline bool direct(const FewTokens& p)
     return p.T <= FEW || (p.T <= DIRECT_TOKENS && p.T * p.K <= FEW * p.E);
 }
 
-// Shares of the down product: about two workgroups per CU, and no more shares
-// than the most experts.  61 tokens, 177 experts, hidden 384 (24 workgroups
-// without): 152 -> 74 us; with twice as many shares 32 tokens, 8 experts,
-// hidden 4096 took 66 against 60.
-inline int down_shares(int T, int K, int H)
+// Shares of the down product: 512 workgroups, two per CU, as long as each wave
+// has some eight blocks to its share; none where that is two shares or less.  61 tokens, 177 experts, hidden 384 (24
+// workgroups without): 152 -> 74 us; 10 tokens, top 6 of 187, hidden 384, f 2432
+// 151 -> 87.  Hidden 4096 gains nothing from a second share (8 tokens, 8 experts
+// 42 against 46, 32 tokens 55 against 59); hidden 2048 (26 tokens, 79 experts)
+// takes 241 with two, 249 with three, 233 with four.
+inline int down_shares(int T, int K, int H, int F)
 {
     const int wide = H / 16;
-    return std::max(1, std::min({(512 + wide / 2) / wide, 16, T * K}));
+    const int blocks = (int)std::min<int64_t>((int64_t)T * K * (F / SCALE_BLOCK) / (8 * DOWN_WAVES), 16);
+    return wide > 200 ? 1 : std::max(1, std::min(512 / wide, blocks));
 }
 
 // The workspace: h in fp32, and where x and h may be coded once their codes,
@@ -708,67 +718,89 @@ struct Workspace {
     Workspace(int T, int K, int H, int F)
     {
         const size_t x = (size_t)T * H, items = (size_t)T * K * F;
-        const int shares = down_shares(T, K, H);
-        bytes = items * 4;
-        if (T <= FEW)
-            return;
+        const int shares = down_shares(T, K, H, F);
         auto take = [&](size_t n) {
             const size_t at = bytes;
             bytes += (n + 15) / 16 * 16;
             return at;
         };
+        h = take(items * 4);
+        parts = take(shares > 1 ? shares * x * 4 : 0);
+        if (T <= FEW)
+            return;
         xq = take(x);
         hq = take(items);
-        parts = take(shares > 1 ? shares * x * 4 : 0);
         xs = take(x / SCALE_BLOCK * 4);
         hs = take(items / SCALE_BLOCK * 4);
     }
 };
 
-hipError_t few(const FewTokens& p, hipStream_t stream)
-{
-    float* hbuf = (float*)p.workspace;
-    const int experts = p.T * p.K < p.E ? p.T * p.K : p.E;     // distinct ones, at most
-    const uint32_t ids = (uint32_t)(p.T * p.K) * 4;
-    few_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, hbuf);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    few_down_kernel<<<dim3(p.H / 16), dim3(DOWN_WAVES * WAVE), ids, stream>>>(p, hbuf);
-    return hipGetLastError();
-}
+inline dim3 grid_of(int64_t n, int per) { return dim3((uint32_t)((n + per - 1) / per)); }
 
-hipError_t coded(const FewTokens& p, hipStream_t stream)
-{
-    const Workspace at(p.T, p.K, p.H, p.F);
-    uint8_t* ws = (uint8_t*)p.workspace;
-    float *hbuf = (float*)(ws + at.h), *xs = (float*)(ws + at.xs), *hs = (float*)(ws + at.hs);
-    float* parts = (float*)(ws + at.parts);
-    const int experts = p.T * p.K < p.E ? p.T * p.K : p.E;
-    const int shares = down_shares(p.T, p.K, p.H);
-    const uint32_t ids = (uint32_t)(p.T * p.K) * 4;
-    const int64_t x = (int64_t)p.T * p.H;
-    auto grid = [](int64_t n, int per) { return dim3((uint32_t)((n + per - 1) / per)); };
-    const int64_t xb = x / SCALE_BLOCK, hb = (int64_t)p.T * p.K * p.F / SCALE_BLOCK;
-    code_kernel<<<grid(xb, CODE_THREADS / 16), dim3(CODE_THREADS), 0, stream>>>(p.x, xb, ws + at.xq, xs);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    coded_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, ws + at.xq, xs, hbuf);
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    code_kernel<<<grid(hb, CODE_THREADS / 16), dim3(CODE_THREADS), 0, stream>>>((const float*)hbuf, hb, ws + at.hq, hs);
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    coded_down_kernel<<<dim3(p.H / 16, shares), dim3(DOWN_WAVES * WAVE), ids, stream>>>(p, ws + at.hq, hs, parts);
-    e = hipGetLastError();
-    if (e != hipSuccess || shares == 1)
-        return e;
-    add_parts_kernel<<<grid(x, CODE_THREADS * 4), dim3(CODE_THREADS), 0, stream>>>(parts, shares, x, p.out);
-    return hipGetLastError();
-}
+// The workspace's places, and how the layer is divided among launches.
+struct Launches {
+    const FewTokens& p;
+    hipStream_t stream;
+    Workspace at;
+    uint8_t* ws;
+    float *h, *parts;
+    int experts, shares;
+    uint32_t ids;
+    Launches(const FewTokens& p_, hipStream_t stream_)
+        : p(p_), stream(stream_), at(p.T, p.K, p.H, p.F), ws((uint8_t*)p.workspace), h((float*)(ws + at.h)),
+          parts((float*)(ws + at.parts)), experts(std::min(p.T * p.K, p.E)),       // distinct ones, at most
+          shares(down_shares(p.T, p.K, p.H, p.F)), ids((uint32_t)(p.T * p.K) * 4)
+    {
+    }
+    hipError_t direct() const
+    {
+        few_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, h);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        const dim3 grid(p.H / 16, shares), block(DOWN_WAVES * WAVE);
+        if (shares > 1)
+            few_down_kernel<true><<<grid, block, ids, stream>>>(p, h, parts);
+        else
+            few_down_kernel<false><<<grid, block, ids, stream>>>(p, h, parts);
+        return hipGetLastError();
+    }
+    template <class V>
+    hipError_t code(const V* from, int64_t elements, uint8_t* codes, float* scales) const
+    {
+        const int64_t blocks = elements / SCALE_BLOCK;
+        code_kernel<<<grid_of(blocks, CODE_THREADS / 16), dim3(CODE_THREADS), 0, stream>>>(from, blocks, codes, scales);
+        return hipGetLastError();
+    }
+    hipError_t coded() const
+    {
+        uint8_t *xq = ws + at.xq, *hq = ws + at.hq;
+        float *xs = (float*)(ws + at.xs), *hs = (float*)(ws + at.hs);
+        hipError_t e = code(p.x, (int64_t)p.T * p.H, xq, xs);
+        if (e != hipSuccess)
+            return e;
+        coded_gate_up_kernel<<<dim3(p.F / 16, experts), dim3(GATE_WAVES * WAVE), ids, stream>>>(p, xq, xs, h);
+        e = hipGetLastError();
+        if (e == hipSuccess)
+            e = code((const float*)h, (int64_t)p.T * p.K * p.F, hq, hs);
+        if (e != hipSuccess)
+            return e;
+        const dim3 grid(p.H / 16, shares), block(DOWN_WAVES * WAVE);
+        if (shares > 1)
+            coded_down_kernel<true><<<grid, block, ids, stream>>>(p, hq, hs, parts);
+        else
+            coded_down_kernel<false><<<grid, block, ids, stream>>>(p, hq, hs, parts);
+        return hipGetLastError();
+    }
+    hipError_t add_parts() const
+    {
+        if (shares == 1)
+            return hipSuccess;
+        const int64_t x = (int64_t)p.T * p.H;
+        add_parts_kernel<<<grid_of(x, CODE_THREADS * 4), dim3(CODE_THREADS), 0, stream>>>(parts, shares, x, p.out);
+        return hipGetLastError();
+    }
+};
 
 }  // namespace
 
@@ -781,7 +813,9 @@ hipError_t launch_few_token_layer(const FewTokens& p, hipStream_t stream)
 {
     if (p.T == 0)
         return hipSuccess;
-    return direct(p) ? few(p, stream) : coded(p, stream);
+    const Launches layer(p, stream);
+    const hipError_t e = direct(p) ? layer.direct() : layer.coded();
+    return e == hipSuccess ? layer.add_parts() : e;
 }
 
 }  // namespace ops
