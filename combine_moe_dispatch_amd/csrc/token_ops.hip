@@ -45,7 +45,9 @@ struct NormArgs {
     float* ys;
 };
 
-template <int V, bool STREAM, int LANES>
+// STREAM: 0 plain accesses, 1 the nontemporal hint for all rows but x, which the
+// operator before has just written, 2 for x too.
+template <int V, int STREAM, int LANES>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int waves_per_row)
 {
     __shared__ float part[16];
@@ -66,9 +68,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
         const int v = u * nt + t;
         xv[u] = rv[u] = v4u{0, 0, 0, 0};
         if (live && v < a.vecs) {
-            xv[u] = load_row<STREAM>((const v4u*)(a.x + at) + v);
+            xv[u] = load_row<STREAM == 2>((const v4u*)(a.x + at) + v);
             if (a.residual)
-                rv[u] = load_row<STREAM>((const v4u*)(a.residual + at) + v);
+                rv[u] = load_row<(STREAM > 0)>((const v4u*)(a.residual + at) + v);
         }
     }
 #pragma unroll
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 o[c] = bf16_pack(s[u][2 * c], s[u][2 * c + 1]);
-            store_row<STREAM>(o, (v4u*)(a.y + at) + v);
+            store_row<(STREAM > 0)>(o, (v4u*)(a.y + at) + v);
         }
         if (a.yq) {
             // a block of 128 is 16 consecutive lanes
@@ -380,7 +382,7 @@ inline dim3 grid_of(int64_t blocks)
 
 }  // namespace
 
-template <int V, bool STREAM, int LANES>
+template <int V, int STREAM, int LANES>
 static hipError_t norm_lanes(const NormArgs& a, hipStream_t stream)
 {
     constexpr int PER = 256 / LANES;
@@ -389,7 +391,7 @@ static hipError_t norm_lanes(const NormArgs& a, hipStream_t stream)
 }
 
 // short rows: several to a workgroup of up to four waves
-template <int V, bool STREAM>
+template <int V, int STREAM>
 static hipError_t norm_waves(const NormArgs& a, int waves, hipStream_t stream)
 {
     const int per = waves < 4 ? 4 / waves : 1;
@@ -398,30 +400,41 @@ static hipError_t norm_waves(const NormArgs& a, int waves, hipStream_t stream)
     return hipGetLastError();
 }
 
-hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const uint16_t* residual,
-                              const uint16_t* weight, float eps, uint16_t* residual_out, uint16_t* y,
-                              uint8_t* yq, float* ys, hipStream_t stream_)
+template <int STREAM>
+static hipError_t norm(const NormArgs& a, hipStream_t stream)
 {
-    if (rows == 0)
-        return hipSuccess;
-    const NormArgs a{rows, hidden, hidden / 8, x, residual, weight, eps, residual_out, y, yq, ys};
-    // Inputs larger than the 256 MB of the memory-side cache are streamed: 65536 rows of
-    // 4096, 512 MB, take 172 us with the hint and 180 without; 4096 rows of
-    // 7168 with a residual, 118 MB, 46.5 with it and 41.8 without.
-    const bool stream = rows * hidden * 2 * (residual ? 2 : 1) > (int64_t)256 << 20;
     // Up to 512 elements, some lanes of a wave per row: 65536 rows of 32 with a
     // residual 7.5 us against 26 with a wave each, of 128 with codes 13.6 against
     // 36, of 384 23.8 against 38.
     if (a.vecs <= 4)
-        return stream ? norm_lanes<1, true, 4>(a, stream_) : norm_lanes<1, false, 4>(a, stream_);
+        return norm_lanes<1, STREAM, 4>(a, stream);
     if (a.vecs <= 16)
-        return stream ? norm_lanes<1, true, 16>(a, stream_) : norm_lanes<1, false, 16>(a, stream_);
+        return norm_lanes<1, STREAM, 16>(a, stream);
     if (a.vecs <= 64)
-        return stream ? norm_lanes<4, true, 16>(a, stream_) : norm_lanes<4, false, 16>(a, stream_);
+        return norm_lanes<4, STREAM, 16>(a, stream);
     const int waves = (a.vecs + 2 * WAVE - 1) / (2 * WAVE);     // at two vectors per thread
-    if (waves <= 16)
-        return stream ? norm_waves<2, true>(a, waves, stream_) : norm_waves<2, false>(a, waves, stream_);
-    return stream ? norm_waves<8, true>(a, 16, stream_) : norm_waves<8, false>(a, 16, stream_);
+    return waves <= 16 ? norm_waves<2, STREAM>(a, waves, stream) : norm_waves<8, STREAM>(a, 16, stream);
+}
+
+hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const uint16_t* residual,
+                              const uint16_t* weight, float eps, uint16_t* residual_out, uint16_t* y,
+                              uint8_t* yq, float* ys, hipStream_t stream)
+{
+    if (rows == 0)
+        return hipSuccess;
+    const NormArgs a{rows, hidden, hidden / 8, x, residual, weight, eps, residual_out, y, yq, ys};
+    // What no cache will hold is streamed.  Inputs beyond the 256 MB of the
+    // memory-side cache, all of them: 65536 rows of 4096, 512 MB, take 171 us with
+    // the hint, 180 without, 174 with x left out.  Beyond half of it, inputs and
+    // outputs together, all but x: 4096 rows of 7168 with a residual and codes
+    // (265 MB) take 45 us where each call has rows of its own and 46 where all
+    // have the same ones; without the hint 52 and 42, with x too 46 and 48.
+    const int64_t each = rows * hidden * 2;
+    const int64_t in = each * (residual ? 2 : 1);
+    const int64_t all = in + (residual_out ? each : 0) + (y ? each : 0) + (yq ? each / 2 : 0);
+    if (in > (int64_t)256 << 20)
+        return norm<2>(a, stream);
+    return all > (int64_t)128 << 20 ? norm<1>(a, stream) : norm<0>(a, stream);
 }
 
 template <int G, int V>

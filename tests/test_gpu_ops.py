@@ -92,6 +92,26 @@ def test_norm(rows, hidden, residual):
             assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
 
 
+@pytest.mark.parametrize("rows,hidden", [(9000, 4096), (33000, 4096), (700000, 128)])
+def test_norm_past_the_caches(rows, hidden):
+    """Rows that the caches do not hold take other accesses: the same bits as in parts."""
+    say(f"[gpu] norm past the caches rows={rows} hidden={hidden}")
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    x, r = (torch.randn((rows, hidden), generator=gen, device=DEV).to(torch.bfloat16) for _ in range(2))
+    w = torch.randn(hidden, generator=gen, device=DEV).to(torch.bfloat16)
+    whole, parts = ([torch.empty_like(x), torch.empty_like(x), torch.empty((rows, hidden), dtype=torch.uint8, device=DEV),
+                     torch.empty((rows, hidden // 128), device=DEV)] for _ in range(2))
+    mep.moe_add_rmsnorm(rows, hidden, x, r, w, 1e-6, *whole)
+    step = (1 << 21) // hidden
+    for a in range(0, rows, step):
+        n = min(step, rows - a)
+        mep.moe_add_rmsnorm(n, hidden, x[a:a + n], r[a:a + n], w, 1e-6, *(t[a:a + n] for t in parts))
+    torch.cuda.synchronize()
+    for a, b in zip(whole, parts):
+        assert torch.equal(a, b)
+
+
 def test_norm_in_place_and_neighbours():
     say("[gpu] norm in place; rows behind the last")
     rows, hidden = 37, 7168
