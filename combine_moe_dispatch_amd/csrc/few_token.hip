@@ -171,30 +171,67 @@ __device__ inline void unpack8(v4u v, float (&f)[8])
     }
 }
 
-// 32 codes of a lane's row (its 16-byte pieces g and g + 4) as fp16.
-struct Half32 {
-    v8h v[4];
+// Operand layout.  A load instruction should take whole 128-byte lines, eight
+// lanes each, but the matrix instruction gives a row only four lanes.  So a
+// weight load brings 8 rows of 128 codes, the lanes l and l ^ 1 (l & 15 = 2a,
+// 2a + 1) holding the pieces 2g and 2g + 1 of row a (16 codes each, g = l >> 4),
+// and the instruction sees 16 rows: row a's even pieces and its odd ones.  It
+// runs once with the columns' even pieces and once with the odd; of the first
+// the even rows count, of the second the odd, and a lane that holds rows 4g ..
+// 4g+3 of the results holds both halves of two weight rows.  Half the products
+// are for nothing, but the matrix unit has time: the kernels wait for memory.
+
+// 16 weight codes of a lane, and 32 codes of a column (pieces 2g and 2g + 1), as
+// fp16.
+struct Half16 {
+    v8h v[2];
 };
-__device__ inline Half32 convert32(v4u lo, v4u hi)
+struct Half32 {
+    Half16 even, odd;
+};
+struct Rows16 {                           // two loads of 8 weight rows
+    Half16 a[2];
+};
+__device__ inline Half16 convert16(v4u raw)
 {
-    return Half32{{e4m3_to_f16(lo.x, lo.y), e4m3_to_f16(lo.z, lo.w), e4m3_to_f16(hi.x, hi.y),
-                   e4m3_to_f16(hi.z, hi.w)}};
+    return Half16{{e4m3_to_f16(raw.x, raw.y), e4m3_to_f16(raw.z, raw.w)}};
 }
+
+__device__ inline Rows16 convert_rows(const v4u (&raw)[2]) { return Rows16{{convert16(raw[0]), convert16(raw[1])}}; }
 
 __device__ inline Half32 coded_columns(const Coded* from, int r, int g)
 {
-    const uint8_t* row = from->codes + r * CODE_STRIDE + g * 16;
-    return convert32(*(const v4u*)row, *(const v4u*)(row + 64));
+    const v4u* at = (const v4u*)(from->codes + r * CODE_STRIDE + g * 32);
+    return Half32{convert16(at[0]), convert16(at[1])};
 }
 
-// The block's products of 16 weight rows and 16 columns, in fp32 from zero.
-__device__ inline v4f product(const Half32& a, const Half32& b)
+__device__ inline v4f product(const Half16& a, const Half16& b)
 {
-    v4f t{0.0f, 0.0f, 0.0f, 0.0f};
+    const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(
+        a.v[1], b.v[1], __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[0], b.v[0], zero, 0, 0, 0), 0, 0, 0);
+}
+
+// The block's products of 16 weight rows (two loads of 8) and 16 columns, in
+// fp32 from zero: of column l & 15, the rows out_row(g, 0 .. 3).
+__device__ inline v4f product(const Rows16& rows, const Half32& b)
+{
+    v4f t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        t = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], t, 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+        const v4f even = product(rows.a[i], b.even), odd = product(rows.a[i], b.odd);
+        t[2 * i] = even[0] + odd[1];
+        t[2 * i + 1] = even[2] + odd[3];
+    }
     return t;
+}
+__device__ inline int out_row(int g, int i) { return (i >> 1) * 8 + 2 * g + (i & 1); }
+
+// Where in its 8 rows of `stride` bytes a lane's weight piece lies.
+__device__ inline uint32_t piece_of(int stride)
+{
+    const int l = threadIdx.x & (WAVE - 1);
+    return ((l & 15) >> 1) * stride + ((l >> 4) * 2 + (l & 1)) * 16;
 }
 
 __device__ inline v4u load16(const uint8_t* p) { return *(const v4u*)p; }
@@ -203,55 +240,61 @@ __device__ inline v4u load16(const uint8_t* p) { return *(const v4u*)p; }
 // time: the weights of the next ones are in flight while a wave works on the
 // last.  Occupancy matters more than depth: four blocks ahead (two waves per
 // SIMD instead of four) took 82 us for one token of a hidden-7168, 256-expert
-// layer, two ahead 71.  Plain loads: with the nontemporal hint the two halves
-// of a 128-byte line are fetched twice, 102 us against 82.
+// layer, two ahead 71.  Whole lines per load against 64-byte halves (a row's
+// pieces g, then g + 4): that layer 68 us against 73, 32 tokens of it 1187
+// against 1255, 64 tokens of 8 experts, hidden 4096 68 against 79.  Plain loads:
+// the nontemporal hint gains up to 3% on those that come from HBM (32 tokens
+// 1174) and costs up to 20% where the weights stay in the memory-side cache or
+// are read again for more columns (64 tokens of 8 experts 82).
 constexpr int GATE_WAVES = 4;
 constexpr int DOWN_WAVES = 8;
-
-// Lane (row r = l & 15, group g = l >> 4) of a 16 x 128 block of weights holds
-// the 16-byte pieces g and g + 4 of row r; the columns' codes use the same
-// order.
 
 // Weight rows of 16 columns f of an expert's gate and up products.
 struct GateUpRows {
     const uint8_t *gate, *up;
     const float *sg, *su;
+    int64_t next8;
+    uint32_t piece;
     int KB;
     __device__ inline GateUpRows(const FewTokens& p, int e, int f0)
     {
-        const int lane = threadIdx.x & (WAVE - 1);
         KB = p.H / SCALE_BLOCK;
-        gate = p.w13 + ((int64_t)e * 2 * p.F + f0 + (lane & 15)) * p.H + (lane >> 4) * 16;
+        next8 = (int64_t)8 * p.H;
+        piece = piece_of(p.H);
+        gate = p.w13 + ((int64_t)e * 2 * p.F + f0) * p.H;
         up = gate + (int64_t)p.F * p.H;
         sg = p.s13 + ((int64_t)e * (2 * p.F / SCALE_BLOCK) + f0 / SCALE_BLOCK) * KB;
         su = sg + (int64_t)(p.F / SCALE_BLOCK) * KB;
     }
-    __device__ inline void fetch(int kb, v4u (&to)[4]) const
+    __device__ inline void fetch(int kb, v4u (&to)[2][2]) const
     {
         const int64_t o = (int64_t)min(kb, KB - 1) * SCALE_BLOCK;
-        to[0] = load16(gate + o);
-        to[1] = load16(gate + o + 64);
-        to[2] = load16(up + o);
-        to[3] = load16(up + o + 64);
+        to[0][0] = load16(gate + o + piece);
+        to[0][1] = load16(gate + o + next8 + piece);
+        to[1][0] = load16(up + o + piece);
+        to[1][1] = load16(up + o + next8 + piece);
     }
 };
 
 struct DownRows {
     const uint8_t* down;
     const float* sd;
+    int64_t next8;
+    uint32_t piece;
     int FB;
     __device__ inline DownRows(const FewTokens& p, int e, int n0)
     {
-        const int lane = threadIdx.x & (WAVE - 1);
         FB = p.F / SCALE_BLOCK;
-        down = p.w2 + ((int64_t)e * p.H + n0 + (lane & 15)) * p.F + (lane >> 4) * 16;
+        next8 = (int64_t)8 * p.F;
+        piece = piece_of(p.F);
+        down = p.w2 + ((int64_t)e * p.H + n0) * p.F;
         sd = p.s2 + ((int64_t)e * (p.H / SCALE_BLOCK) + n0 / SCALE_BLOCK) * FB;
     }
     __device__ inline void fetch(int kb, v4u (&to)[2]) const
     {
         const int64_t o = (int64_t)min(kb, FB - 1) * SCALE_BLOCK;
-        to[0] = load16(down + o);
-        to[1] = load16(down + o + 64);
+        to[0] = load16(down + o + piece);
+        to[1] = load16(down + o + next8 + piece);
     }
 };
 
@@ -296,7 +339,7 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const 
     const GateUpRows rows(p, e, f0);
     const int KB = rows.KB;
     const int k0 = KB * wave / GATE_WAVES, k1 = KB * (wave + 1) / GATE_WAVES;
-    v4u w[AHEAD][4];
+    v4u w[AHEAD][2][2];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
         rows.fetch(k0 + u, w[u]);
@@ -333,7 +376,7 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const 
             for (int u = 0; u < AHEAD; ++u) {
                 const int kb = min(kb0 + u, KB - 1), row = u * FEW + (r & (FEW - 1));
                 const bool live = kb0 + u < k1;
-                const Half32 wg = convert32(w[u][0], w[u][1]), wu = convert32(w[u][2], w[u][3]);
+                const Rows16 wg = convert_rows(w[u][0]), wu = convert_rows(w[u][1]);
                 rows.fetch(kb0 + u + AHEAD, w[u]);
                 const Half32 q = coded_columns(&coded[wave], row, g);
                 const float xs = coded[wave].scale[row];
@@ -342,12 +385,12 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const 
             }
             own_lds_written();
         }
-        // lane (r, g) has rows 4g .. 4g+3 of column r
+        // lane (r, g) has rows out_row(g, 0 .. 3) of column r
         if (r < FEW)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                part[wave][0][r][g * 4 + i] = ag[i];
-                part[wave][1][r][g * 4 + i] = au[i];
+                part[wave][0][r][out_row(g, i)] = ag[i];
+                part[wave][1][r][out_row(g, i)] = au[i];
             }
         __syncthreads();
         for (int v = threadIdx.x; v < min(n - c0, FEW) * 16; v += GATE_WAVES * WAVE) {
@@ -463,7 +506,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const Few
                 for (int u = 0; u < AHEAD; ++u) {
                     const int row = u * FEW + (r & (FEW - 1));
                     const float s = coded[wave].scale[row] * rows.sd[min(k + u, FB - 1)];
-                    const Half32 wd = convert32(w[u][0], w[u][1]);
+                    const Rows16 wd = convert_rows(w[u]);
                     rows.fetch(k + u + AHEAD, w[u]);
                     add_block(acc, product(wd, coded_columns(&coded[wave], row, g)), s, k + u < kb1);
                 }
@@ -474,7 +517,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void few_down_kernel(const Few
                 const float wt = weight[wave][t];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    tile[wave][t][g * 4 + i] += wt * acc[i];
+                    tile[wave][t][out_row(g, i)] += wt * acc[i];
             }
         }
         own_lds_written();
@@ -519,7 +562,7 @@ struct CodedRows {
     v4u q[AHEAD][2];
     float s[AHEAD];
     __device__ inline CodedRows(const uint8_t* code_rows, const float* scale_rows, int64_t row, int blocks_)
-        : codes(code_rows + row * blocks_ * SCALE_BLOCK + ((threadIdx.x & (WAVE - 1)) >> 4) * 16),
+        : codes(code_rows + row * blocks_ * SCALE_BLOCK + ((threadIdx.x & (WAVE - 1)) >> 4) * 32),
           scales(scale_rows + row * blocks_), blocks(blocks_)
     {
     }
@@ -527,16 +570,18 @@ struct CodedRows {
     {
         kb = min(kb, blocks - 1);
         q[u][0] = load16(codes + kb * SCALE_BLOCK);
-        q[u][1] = load16(codes + kb * SCALE_BLOCK + 64);
+        q[u][1] = load16(codes + kb * SCALE_BLOCK + 16);
         s[u] = scales[kb];
     }
+    __device__ inline Half32 columns(int u) const { return Half32{convert16(q[u][0]), convert16(q[u][1])}; }
 };
 
 // h as above, 16 columns at a time (an expert with more reads its weights
-// again, from the caches: 32 at a time, with fewer waves in flight, took 1475
-// us against 1258 for 32 tokens of the 256-expert layer, and 77 against 83 for
-// 64 tokens of one with 8 experts).
-__global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void coded_gate_up_kernel(const FewTokens p, const uint8_t* xq,
+// again, from the caches: 32 at a time took 1475 us against 1258 for 32 tokens
+// of the 256-expert layer, and 77 against 83 for 64 tokens of one with 8
+// experts).  Three waves per SIMD: four leave too few registers (1367 against
+// 1187 for the 32 tokens).
+__global__ __launch_bounds__(GATE_WAVES* WAVE, 3) void coded_gate_up_kernel(const FewTokens p, const uint8_t* xq,
                                                                              const float* xs, float* hbuf)
 {
     extern __shared__ int32_t ids[];
@@ -554,7 +599,7 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void coded_gate_up_kernel(cons
     const GateUpRows rows(p, e, f0);
     const int KB = rows.KB;
     const int k0 = KB * wave / GATE_WAVES, k1 = KB * (wave + 1) / GATE_WAVES;
-    v4u w[AHEAD][4];
+    v4u w[AHEAD][2][2];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
         rows.fetch(k0 + u, w[u]);
@@ -577,17 +622,17 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void coded_gate_up_kernel(cons
             for (int u = 0; u < AHEAD; ++u) {
                 const int kb = min(kb0 + u, KB - 1);
                 const bool live = kb0 + u < k1;
-                const Half32 wg = convert32(w[u][0], w[u][1]), wu = convert32(w[u][2], w[u][3]);
+                const Rows16 wg = convert_rows(w[u][0]), wu = convert_rows(w[u][1]);
                 rows.fetch(kb0 + u + AHEAD, w[u]);
-                const Half32 q = convert32(x.q[u][0], x.q[u][1]);
+                const Half32 q = x.columns(u);
                 add_block(ag, product(wg, q), x.s[u] * rows.sg[kb], live);
                 add_block(au, product(wu, q), x.s[u] * rows.su[kb], live);
                 x.fetch(u, kb0 + u + AHEAD);
             }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            part[wave][0][r][g * 4 + i] = ag[i];
-            part[wave][1][r][g * 4 + i] = au[i];
+            part[wave][0][r][out_row(g, i)] = ag[i];
+            part[wave][1][r][out_row(g, i)] = au[i];
         }
         __syncthreads();
         for (int v = threadIdx.x; v < min(n - c0, 16) * 16; v += GATE_WAVES * WAVE) {
@@ -651,9 +696,9 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const F
 #pragma unroll
                 for (int u = 0; u < AHEAD; ++u) {
                     const float sd = rows.sd[min(k + u, FB - 1)];
-                    const Half32 wd = convert32(w[u][0], w[u][1]);
+                    const Rows16 wd = convert_rows(w[u]);
                     rows.fetch(k + u + AHEAD, w[u]);
-                    add_block(acc, product(wd, convert32(h.q[u][0], h.q[u][1])), h.s[u] * sd, k + u < kb1);
+                    add_block(acc, product(wd, h.columns(u)), h.s[u] * sd, k + u < kb1);
                     h.fetch(u, k + u + AHEAD);
                 }
             if (c0 + r < n) {
@@ -661,7 +706,7 @@ __global__ __launch_bounds__(DOWN_WAVES* WAVE, 4) void coded_down_kernel(const F
                 const float wt = weight[wave][t];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    tile[wave][t][g * 4 + i] += wt * acc[i];
+                    tile[wave][t][out_row(g, i)] += wt * acc[i];
             }
         }
         own_lds_written();
