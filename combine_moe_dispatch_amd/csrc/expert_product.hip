@@ -207,6 +207,10 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     m_tiles = (b - a + BM - 1) / BM;
     const int64_t v = (int64_t)__builtin_amdgcn_readlane((int)(u >> 32), src) << 32 |
                       (uint32_t)__builtin_amdgcn_readlane((int)u, src);
+    // (ascending offsets always pass; others, whose tiles may be beyond counting,
+    // stay inside the rows)
+    if (b <= a || v < 0 || v >= (int64_t)m_tiles * n_tiles)
+        return false;
     constexpr int GROUP = 8;
     const int64_t per_group = (int64_t)GROUP * n_tiles;
     const int g = (int)(v / per_group);

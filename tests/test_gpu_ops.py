@@ -442,6 +442,26 @@ def test_matmul_long_offsets():
     assert bool((y[:, -1] == k).all()) and bool((y[:, :-1] == 0).all())
 
 
+@pytest.mark.parametrize("E,rows,n,k", [(8, 60, 256, 256), (70, 300, 1024, 256), (6, 1200, 4096, 128),
+                                        (6, 2400, 4096, 256)])
+def test_offsets_out_of_order(E, rows, n, k):
+    """Offsets that break their contract: any result, nothing outside it."""
+    say(f"[gpu] offsets out of order E={E} rows={rows} n={n} k={k}")
+    g = rng(18, E, rows)
+    ins = list(grouped_inputs(g, E, n, k, counts_of("even", E, rows, g), 0))
+    want = run_matmul(*ins)
+    fine = run_gate_up(*ins[:4], ins[4])
+    for bad in (np.linspace(rows, 0, E + 1), np.where(np.arange(E + 1) % 2, rows, 0),
+                g.integers(-2 ** 31, 2 ** 31 - 1, E + 1), np.full(E + 1, -5), np.full(E + 1, rows + 99)):
+        y = run_matmul(*ins[:4], bad.astype(np.int32))
+        assert bool((y[rows:] == 9.0).all())
+        h, hs = run_gate_up(*ins[:4], bad.astype(np.int32))
+        assert bool((h[rows:] == 5).all()) and bool((hs[rows:] == 9.0).all())
+    assert torch.equal(run_matmul(*ins), want)
+    again = run_gate_up(*ins[:4], ins[4])
+    assert all(torch.equal(a, b) for a, b in zip(fine, again))
+
+
 # --- the few-token layer ----------------------------------------------------------------------------
 
 def few_inputs(g, T, E, K, H, F):
@@ -703,6 +723,38 @@ def test_first_call_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("E,rows,n,k", [(3, 40, 512, 640), (16, 500, 4096, 256), (16, 2400, 4096, 384)])
+def test_products_captured_and_at_once(E, rows, n, k):
+    """Captured products of each size, replayed on two streams at once."""
+    say(f"[gpu] products captured E={E} rows={rows} n={n} k={k}")
+    g = rng(19, E, rows)
+    x, xs, w, ws, offsets = grouped_inputs(g, E, n, k, counts_of("spread", E, rows, g), 0)
+    y = run_matmul(x, xs, w, ws, offsets)[:rows]
+    h, hs = (t[:rows] for t in run_gate_up(x, xs, w, ws, offsets))
+    d = [dev(a) for a in (x, xs, offsets, w, ws)]
+    outs = [(torch.empty_like(y), torch.empty_like(h), torch.empty_like(hs)) for _ in range(2)]
+    graphs = []
+    torch.cuda.synchronize()
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mep.moe_expert_matmul(rows, E, n, k, *d, o[0])
+            mep.moe_expert_gate_up(rows, E, n // 2, k, *d, o[1], o[2])
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for o in outs:
+            for t in o:
+                t.view(torch.uint8).fill_(0xFF)
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, (y, h, hs)))
 
 
 def test_two_streams_at_once():
