@@ -662,23 +662,29 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
     }
 }
 
-// Tiles of C::BM rows; an expert's last tile is one of REST's where that holds
-// the rows that are left.
-template <bool GATE_UP, class C, class REST>
-__global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const ExpertProduct p, int n_tiles)
+// The tile at `at`, which has at most C::BM rows, as the smallest of C and RESTS
+// (from high to low) that holds them.
+template <bool GATE_UP, class C, class... RESTS>
+__device__ __forceinline__ void smallest_tile(const ExpertProduct& p, const Place& at, uint8_t* lds)
 {
-    static_assert(REST::THREADS == C::THREADS && REST::BN == C::BN, "one launch for both");
-    extern __shared__ __align__(1024) uint8_t lds[];
-    Place at;
-    if (!(p.E <= 4 * WAVE ? find_tile<C::BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
-                          : find_tile<C::BM, 16>(p.offsets, p.E, p.rows, n_tiles, at)))
-        return;
-    if constexpr (REST::BM < C::BM)
-        if (at.rows <= REST::BM) {
-            product_tile<REST, GATE_UP>(p, at, lds);
+    if constexpr (sizeof...(RESTS) > 0)
+        if (at.rows <= std::max({RESTS::BM...})) {
+            smallest_tile<GATE_UP, RESTS...>(p, at, lds);
             return;
         }
     product_tile<C, GATE_UP>(p, at, lds);
+}
+
+// Tiles of C::BM rows; an expert's last tile may be one of RESTS'.
+template <bool GATE_UP, class C, class... RESTS>
+__global__ __launch_bounds__(C::THREADS) void expert_product_kernel(const ExpertProduct p, int n_tiles)
+{
+    static_assert(((RESTS::THREADS == C::THREADS && RESTS::BN == C::BN && RESTS::BM < C::BM) && ...), "one launch");
+    extern __shared__ __align__(1024) uint8_t lds[];
+    Place at;
+    if (p.E <= 4 * WAVE ? find_tile<C::BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
+                        : find_tile<C::BM, 16>(p.offsets, p.E, p.rows, n_tiles, at))
+        smallest_tile<GATE_UP, C, RESTS...>(p, at, lds);
 }
 
 // The product where tiles of 256 columns would leave most CUs idle: 32 columns
@@ -799,12 +805,12 @@ hipError_t launch_narrow(const ExpertProduct& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <bool GATE_UP, class C, class REST = C>
+template <bool GATE_UP, class C, class... RESTS>
 hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 {
     const int n_tiles = GATE_UP ? p.n / C::BN : (p.n + C::BN - 1) / C::BN;
     const dim3 blocks = grid_of(workgroups(p, C::BM, n_tiles));
-    constexpr int ring = std::max(C::RING, REST::RING);
+    constexpr int ring = std::max({C::RING, RESTS::RING...});
     constexpr int epi = GATE_UP ? C::WN * C::BM * 4 + C::BM * SCALE_BLOCK : 0;
     const int bytes = std::max(ring + 2 * ((p.k / SCALE_BLOCK + WAVE) & ~(WAVE - 1)) * 4, epi);
     // once per device: the kernel may use all of a CU's LDS
@@ -815,13 +821,13 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
         return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (!(allowed.load(std::memory_order_relaxed) & bit) || !bit) {
-        e = hipFuncSetAttribute((const void*)expert_product_kernel<GATE_UP, C, REST>,
+        e = hipFuncSetAttribute((const void*)expert_product_kernel<GATE_UP, C, RESTS...>,
                                 hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != hipSuccess)
             return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    expert_product_kernel<GATE_UP, C, REST><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
+    expert_product_kernel<GATE_UP, C, RESTS...><<<blocks, dim3(C::THREADS), bytes, stream>>>(p, n_tiles);
     return hipGetLastError();
 }
 
@@ -859,9 +865,13 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 //    201-210, mean 96 208-222 against 216-224, mean 112 228-259 against
 //    222-241, mean 128 277-296 against 254-261;
 //  - 256 + 128 against 256 alone: ragged means of 200-512 315-341 against
-//    316-391; against 128 + 32, mean 192 298-302 against 328-334;
+//    316-391; with 192 and 64 besides: mean 128 242-245 against 253-260, 160
+//    268-275 against 286-289, 200 290-311 against 299-325, 256 experts of
+//    about 128 930 against 971; against 128 + 32, mean 192 298-302 against
+//    328-334;
 //  - gate/up, 128 + 64 against 128 alone: mean 75 316 against 343, 128
-//    405-452 against 418-469, 200 567 against 598, 256 662 against 686.  (256
+//    405-452 against 418-469, 200 567 against 598, 256 662 against 686; with 32
+//    besides, 256 experts of about 128, f 2048, k 7168 2733 against 2778.  (256
 //    rows would need twice the accumulators.)
 template <bool GATE_UP>
 hipError_t choose(const ExpertProduct& p, hipStream_t stream)
@@ -885,11 +895,11 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
     if constexpr (EIGHT) {
         if (mean <= 96 || workgroups(p, 256, n_tiles) < 200)
             return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>>(p, stream);
-        return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<128, 256, 2, 4, 3, true, 16, false>>(
-            p, stream);
+        return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<192, 256, 4, 2, 2, true, 16, false>,
+                      Tile<128, 256, 2, 4, 3, true, 16, false>, Tile<64, 256, 1, 8, 3, true, 16, false>>(p, stream);
     } else {
-        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<64, 256, 1, 8, 3, false, 16, false>>(
-            p, stream);
+        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<64, 256, 1, 8, 3, false, 16, false>,
+                      Tile<32, 256, 1, 8, 4, false, 16, false>>(p, stream);
     }
 }
 
