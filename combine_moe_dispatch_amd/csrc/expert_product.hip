@@ -859,20 +859,24 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 //    against 196; against 64 + 32: mean 6 157 against 169, mean 16 162-186
 //    against 170-173, mean 24 186-190 against 174-201; the product alike (mean
 //    6 140 / 142, 24 170-181 / 162-171);
+//  - 64 + 48 + 32 against 64 + 32, gate/up: mean 30 177 against 185-191, 40
+//    187-211 against 206-222;
 //  - 64 + 32 against 32 + 16, mean 32: gate/up 206 against 214, the product
 //    171 against 216; 64 against 128, mean 60 of the product 211 against 204;
 //  - 128 rows nontemporal against 256 + 128 plain: mean 60 193-204 against
 //    201-210, mean 96 208-222 against 216-224, mean 112 228-259 against
-//    222-241, mean 128 277-296 against 254-261;
+//    222-241, mean 128 277-296 against 254-261; with 96 and 64 besides: mean 52
+//    181-185 against 193-204, 70 191 against 200, 96 206-231 against 210-235;
 //  - 256 + 128 against 256 alone: ragged means of 200-512 315-341 against
 //    316-391; with 192 and 64 besides: mean 128 242-245 against 253-260, 160
 //    268-275 against 286-289, 200 290-311 against 299-325, 256 experts of
 //    about 128 930 against 971; against 128 + 32, mean 192 298-302 against
 //    328-334;
 //  - gate/up, 128 + 64 against 128 alone: mean 75 316 against 343, 128
-//    405-452 against 418-469, 200 567 against 598, 256 662 against 686; with 32
-//    besides, 256 experts of about 128, f 2048, k 7168 2733 against 2778.  (256
-//    rows would need twice the accumulators.)
+//    405-452 against 418-469, 200 567 against 598, 256 662 against 686; with 96
+//    besides, mean 90 287-309 against 308-326; with 32 besides,
+//    256 experts of about 128, f 2048, k 7168 2733 against 2778.  (256 rows would
+//    need twice the accumulators.)
 template <bool GATE_UP>
 hipError_t choose(const ExpertProduct& p, hipStream_t stream)
 {
@@ -890,16 +894,17 @@ hipError_t choose(const ExpertProduct& p, hipStream_t stream)
         return launch<GATE_UP, Tile<32, 256, 1, 8, 2, EIGHT, 16, true>, Tile<16, 256, 1, 8, 2, EIGHT, 16, true>>(
             p, stream);
     if (mean <= 48 || workgroups(p, 128, n_tiles) < 200)
-        return launch<GATE_UP, Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, Tile<32, 256, 1, 8, 3, EIGHT, 16, true>>(
-            p, stream);
+        return launch<GATE_UP, Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, Tile<48, 256, 1, 8, 3, EIGHT, 16, true>,
+                      Tile<32, 256, 1, 8, 3, EIGHT, 16, true>>(p, stream);
     if constexpr (EIGHT) {
         if (mean <= 96 || workgroups(p, 256, n_tiles) < 200)
-            return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>>(p, stream);
+            return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>, Tile<96, 256, 2, 4, 3, true, 16, true>,
+                          Tile<64, 256, 1, 8, 3, true, 16, true>>(p, stream);
         return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<192, 256, 4, 2, 2, true, 16, false>,
                       Tile<128, 256, 2, 4, 3, true, 16, false>, Tile<64, 256, 1, 8, 3, true, 16, false>>(p, stream);
     } else {
-        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<64, 256, 1, 8, 3, false, 16, false>,
-                      Tile<32, 256, 1, 8, 4, false, 16, false>>(p, stream);
+        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<96, 256, 1, 8, 3, false, 16, false>,
+                      Tile<64, 256, 1, 8, 3, false, 16, false>, Tile<32, 256, 1, 8, 4, false, 16, false>>(p, stream);
     }
 }
 

@@ -382,7 +382,8 @@ def test_products_odd_values(rows):
 WIDE_PRODUCTS = [
     (64, 300, 1024, 256, "even", 3), (64, 400, 1024, 640, "spread", 0), (16, 500, 4096, 256, "spread", 0),
     (16, 1200, 4096, 128, "spread", 2), (16, 2400, 4096, 384, "spread", 0), (2, 709, 4416, 256, "even", 0),
-    (3, 700, 4600, 128, "first", 1), (1, 64, 7168, 384, "even", 0)]
+    (3, 700, 4600, 128, "first", 1), (1, 64, 7168, 384, "even", 0), (40, 1800, 2048, 128, "spread", 1),
+    (12, 960, 5120, 256, "even", 0), (10, 1900, 5120, 128, "spread", 3)]
 
 
 @pytest.mark.parametrize("E,rows,n,k,kind,spare", WIDE_PRODUCTS)
