@@ -413,6 +413,14 @@ def test_widest_rows(rows):
     check_gate_up(h[:rows].cpu().numpy(), R.f64(hs[:rows]), x, xs, w, ws, offsets)
 
 
+@pytest.mark.parametrize("rows", [3, 150])
+def test_widest_outputs(rows):
+    """The widest outputs that the calls take."""
+    test_matmul(2, rows, 65536, 128, "even", 1)
+    test_matmul(1, rows, 65528, 128, "even", 0)
+    test_gate_up(2, rows, 65536, 128, "even", 1)
+
+
 def test_matmul_long_offsets():
     """Rows and weights past 2^31 bytes."""
     say("[gpu] matmul past 32 bits")
@@ -520,7 +528,8 @@ def check_few(out, ref, noise):
     (1, 1, 1, 128, 128), (1, 8, 3, 384, 256), (2, 8, 8, 256, 640), (3, 300, 8, 128, 128),
     (15, 8, 2, 1152, 128), (16, 3, 3, 256, 256), (17, 4, 2, 384, 128), (32, 2, 2, 256, 128),
     (33, 5, 2, 128, 384), (64, 3, 2, 256, 128), (64, 64, 4, 128, 128), (5, 1024, 64, 128, 128),
-    (64, 70, 64, 128, 128), (40, 2, 64, 128, 128)])
+    (64, 70, 64, 128, 128), (40, 2, 64, 128, 128), (3, 2, 2, 65536, 128), (20, 2, 2, 128, 65536),
+    (6, 2, 1, 128, 65536), (18, 3, 1, 65536, 128)])
 def test_few(T, E, K, H, F):
     say(f"[gpu] few T={T} E={E} K={K} H={H} F={F}")
     ins = few_inputs(rng(9, T, E, K, H, F), T, E, K, H, F)
