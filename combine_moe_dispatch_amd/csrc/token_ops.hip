@@ -260,17 +260,18 @@ __global__ __launch_bounds__(256) void topk_route_kernel(int64_t tokens, int E, 
 
 // Floats as unsigned numbers in the same order; -0 as +0, NaN as -infinity.
 // 0 is below all of them.
-__device__ inline uint32_t order_of(float v)
+__device__ inline uint32_t ordered(float v)          // not for NaN and -0
 {
-    const uint32_t u = __float_as_uint(v == v ? v + 0.0f : -INFINITY);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(v);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ inline uint32_t order_of(float v) { return ordered(v == v ? v + 0.0f : -INFINITY); }
 __device__ inline float value_of(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// The same with a wave per token, for 64 < E <= 64 V: lane l holds experts
+// The same with a wave per token, for E <= 64 V: lane l holds experts
 // l*V .. l*V+V-1, sorted once (largest first, stable).  A pick is then the
 // largest of the lanes' heads, the lowest lane among equals (its experts are
 // the lowest), and one shift of that lane's list; lists end in 0.  The logits
@@ -373,6 +374,128 @@ __global__ __launch_bounds__(256) void topk_route_wave_kernel(int64_t tokens, in
     }
 }
 
+// The same for up to 16 choices, four tokens per wave: a row of 16 lanes per
+// token, LISTS sorted lists of four experts per lane, so that the rounds'
+// instructions serve four tokens (a whole wave's maximum takes six steps and
+// a scalar trip for one).  The vector unit bounds both.
+template <int LISTS, bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void topk_route_rows_kernel(int64_t tokens, int E, int K, const void* logits,
+                                                              int renorm, int32_t* idx, float* w)
+{
+    const int l = threadIdx.x & 15;
+    const int64_t tok = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 16 + threadIdx.x / 16;
+    const int64_t row = (tok < tokens ? tok : tokens - 1) * E;
+    const int e0 = l * 4 * LISTS;                 // this lane's experts: e0 .. e0 + 4*LISTS - 1
+    float z[LISTS][4];
+#pragma unroll
+    for (int j = 0; j < LISTS; ++j) {
+        v4f v{NAN, NAN, NAN, NAN};
+        const int e = e0 + 4 * j;
+        if (VEC) {
+            if (e < E) {
+                if (BF16) {
+                    const v2u b = *(const v2u*)((const uint16_t*)logits + row + e);
+                    v = v4f{bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y)};
+                } else {
+                    v = *(const v4f*)((const float*)logits + row + e);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (e + c < E)
+                    v[c] = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)logits)[row + e + c] << 16)
+                                : ((const float*)logits)[row + e + c];
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            z[j][c] = v[c] == v[c] ? v[c] + 0.0f : -INFINITY;
+    }
+    float top = z[0][0];
+#pragma unroll
+    for (int j = 0; j < LISTS; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            top = fmaxf(top, z[j][c]);
+    across<16>([&](auto trade) { top = fmaxf(top, trade(top)); });
+    // p(z) = exp(z - top); infinite tops share the whole weight (the minimum of
+    // NaN and 0 is 0), and a token with nothing but -infinity has none
+    auto p = [&](float v) { return __expf(fminf(v - top, 0.0f)); };
+    const bool none = top == -INFINITY;
+    float sum = 0.0f;
+    if (!renorm) {
+#pragma unroll
+        for (int j = 0; j < LISTS; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sum += p(z[j][c]);
+        across<16>([&](auto trade) { sum += trade(sum); });
+    }
+    uint32_t key[LISTS][4];
+#pragma unroll
+    for (int j = 0; j < LISTS; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            key[j][c] = ordered(z[j][c]) & (e0 + 4 * j + c < E ? ~0u : 0u);
+    auto row_max = [](uint32_t v) {
+        across<16>([&](auto trade) { v = max(v, (uint32_t)trade((int)v)); });
+        return v;
+    };
+    uint32_t at[LISTS];                           // a list's experts, two bits each
+#pragma unroll
+    for (int j = 0; j < LISTS; ++j) {
+        uint32_t i[4] = {0, 1, 2, 3};
+#pragma unroll
+        for (int n = 3; n > 0; --n)
+#pragma unroll
+            for (int c = 0; c < n; ++c) {
+                const uint32_t a = key[j][c], b = key[j][c + 1], ia = i[c], ib = i[c + 1];
+                key[j][c] = max(a, b);
+                key[j][c + 1] = min(a, b);
+                i[c] = a < b ? ib : ia;
+                i[c + 1] = a < b ? ia : ib;
+            }
+        at[j] = i[0] | i[1] << 2 | i[2] << 4 | i[3] << 6;
+    }
+    const int lane = threadIdx.x & (WAVE - 1);
+    const uint32_t before = (0xFFFFu << (lane & 16)) & ((1u << (lane & 31)) - 1);   // lanes of the row below this one
+    int32_t* out = idx + tok * K;
+    uint32_t mine = 0;
+    for (int k = 0; k < K; ++k) {
+        uint32_t head = key[0][0];
+#pragma unroll
+        for (int j = 1; j < LISTS; ++j)
+            head = max(head, key[j][0]);
+        const uint32_t pick = row_max(head);
+        const uint64_t have = __ballot(head == pick);
+        const uint32_t half = lane < 32 ? (uint32_t)have : (uint32_t)(have >> 32);
+        bool win = head == pick && (half & before) == 0;
+        const bool write = win && tok < tokens;
+        int e = e0;
+#pragma unroll
+        for (int j = 0; j < LISTS; ++j) {
+            const bool here = win && key[j][0] == pick;      // the first list that has it
+            win = win && !here;
+            e = here ? e0 + 4 * j + (int)(at[j] & 3) : e;
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+                key[j][c] = here ? key[j][c + 1] : key[j][c];
+            key[j][3] = here ? 0 : key[j][3];
+            at[j] >>= here ? 2 : 0;
+        }
+        if (write)
+            out[k] = e;
+        mine = l == k ? pick : mine;
+    }
+    const float v = l < K ? p(value_of(mine)) : 0.0f;
+    if (renorm) {
+        sum = v;
+        across<16>([&](auto trade) { sum += trade(sum); });
+    }
+    if (l < K && tok < tokens)
+        w[tok * K + l] = none ? 0.0f : v / sum;
+}
+
 // `blocks` workgroups as a grid whose dimensions times the threads stay below 2^32.
 inline dim3 grid_of(int64_t blocks)
 {
@@ -470,21 +593,48 @@ static hipError_t route_wave(int64_t tokens, int E, int K, const void* logits, i
     return hipGetLastError();
 }
 
+template <int LISTS>
+static hipError_t route_rows(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm,
+                             int32_t* idx, float* w, hipStream_t stream)
+{
+    const dim3 grid = grid_of((tokens + 15) / 16), block(256);
+    if (E % 4 == 0) {
+        if (bf16)
+            topk_route_rows_kernel<LISTS, true, true><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+        else
+            topk_route_rows_kernel<LISTS, false, true><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+    } else {
+        if (bf16)
+            topk_route_rows_kernel<LISTS, true, false><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+        else
+            topk_route_rows_kernel<LISTS, false, false><<<grid, block, 0, stream>>>(tokens, E, K, logits, renorm, idx, w);
+    }
+    return hipGetLastError();
+}
+
 hipError_t launch_topk_route(int64_t tokens, int E, int K, const void* logits, int bf16, int renorm,
                              int32_t* idx, float* w, hipStream_t stream)
 {
     if (tokens == 0)
         return hipSuccess;
-    // Few experts: some lanes per token, whose trades stay inside a row of 16
-    // (131072 tokens, 16 experts, top 4 6.7 us against 20 with 16 lanes, 64, top
-    // 8 24 against 36).  More: a wave per token, unless there are many tokens
-    // of up to 128 experts (131072, top 8 36 against 56; 300 9.4 against 5.4).
+    // Up to 16 experts, four lanes per token (131072 tokens, 16 experts, top 4 6.7
+    // us against 13 with a row of 16 lanes and lists).  Up to 256 and 16 choices,
+    // a row of 16 lanes (131072 tokens, top 8: 64 experts 17 against 24 with 8
+    // lanes and no lists; 128 experts 26 against 56 with a wave per token; 256
+    // experts 48 against 66, top 16 60 against 88; 300 tokens alike).  512 experts
+    // would gain 10% where E is a multiple of 4, and lose half elsewhere.
     if (E <= 16)
         return route<4, 4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+    if (K <= 16) {
+        if (E <= 64)
+            return route_rows<1>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+        if (E <= 128)
+            return route_rows<2>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+        if (E <= 256)
+            return route_rows<4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
+    }
     if (E <= 64)
         return route<8, 8>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
-    if (E <= 128 && tokens > 16384)
-        return route<8, 16>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
     if (E <= 256)
         return route_wave<4>(tokens, E, K, logits, bf16, renorm, idx, w, stream);
     if (E <= 512)

@@ -229,7 +229,8 @@ def test_route_masks(renorm):
 
 
 @pytest.mark.parametrize("T,E,K", [(16385, 100, 8), (16390, 128, 64), (16400, 65, 3), (1003, 16, 16), (77, 12, 5),
-                                   (4099, 33, 12)])
+                                   (4099, 33, 12), (2051, 64, 16), (777, 17, 17), (1030, 256, 16), (515, 255, 8),
+                                   (99, 200, 17), (33, 129, 1), (1, 64, 6)])
 def test_route_many_tokens(T, E, K):
     say(f"[gpu] route T={T} E={E} K={K}")
     g = rng(17, T, E)
