@@ -767,12 +767,13 @@ __global__ __launch_bounds__(CODE_THREADS) void add_parts_kernel(const float* pa
 }
 
 // Whether the product kernels code their columns themselves: when an expert
-// has few of them.  Measured (us, direct against coded): 16 tokens, 64 experts,
-// top 4, hidden 4096, f 2048 194 against 198; 8 tokens, 8 experts, top 2 41
-// against 54; 13 tokens of hidden 6400, f 256, 117 experts, top 2 38 against
-// 46; but 29 tokens, 5 experts, top 5, hidden 1024, f 1536 65 against 44, 32
-// tokens, 8 experts, top 2, hidden 4096 90 against 60, and 64 tokens of the
-// 256-expert layer 2146 against 1874.
+// has few of them.  Measured (us, direct against coded): 5 tokens, 160 experts,
+// top 3, hidden 768, f 384 17.6 against 21.9; 8 tokens, 8 experts, top 2, hidden
+// 4096, f 2048 40 against 45; 13 tokens of hidden 6400, f 256, 117 experts, top 2
+// 34 against 39; 16 tokens, 64 experts, top 4, hidden 4096, f 2048 191 against
+// 187; but, before the weights came in whole lines, 29 tokens, 5 experts, top 5,
+// hidden 1024, f 1536 65 against 44, 32 tokens, 8 experts, top 2, hidden 4096 90
+// against 60, and 64 tokens of the 256-expert layer 2146 against 1874.
 inline bool direct(const FewTokens& p)
 {
     return p.T <= FEW || (p.T <= DIRECT_TOKENS && p.T * p.K <= FEW * p.E);
