@@ -132,6 +132,20 @@ def test_norm_in_place_and_neighbours():
     assert torch.equal(z[:-5], y[:-5]) and bool((z[-5:] == 3.0).all())
 
 
+@pytest.mark.parametrize("rows,hidden", [(300, 24), (300, 128), (100, 384), (9, 1032), (5, 16392), (9000, 4096)])
+def test_norm_in_place(rows, hidden):
+    say(f"[gpu] norm in place rows={rows} hidden={hidden}")
+    g = rng(20, rows, hidden)
+    x, r, w = (R.bf16(g.standard_normal(s, dtype=np.float32)).to(DEV) for s in ((rows, hidden), (rows, hidden), hidden))
+    ro, y = torch.empty_like(x), torch.empty_like(x)
+    mep.moe_add_rmsnorm(rows, hidden, x, r, w, 1e-6, ro, y, None, None)
+    for a, b in ((0, 1), (1, 0)):                   # residual_out and y over x and residual, both ways
+        t = [x.clone(), r.clone()]
+        mep.moe_add_rmsnorm(rows, hidden, t[0], t[1], w, 1e-6, t[a], t[b], None, None)
+        torch.cuda.synchronize()
+        assert torch.equal(t[a], ro) and torch.equal(t[b], y)
+
+
 def test_norm_odd_values():
     """A NaN or an infinity stays in its row; rows and blocks of zeros; tiny blocks."""
     say("[gpu] norm odd values")
