@@ -140,11 +140,6 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
     }
 }
 
-// ---------------------------------------------------------------------------
-// A token's K best experts and their softmax weights.  G lanes share a token,
-// lane l of them holds experts l, l+G, ...; K times: the largest logit left
-// (lowest expert among equals) is taken out.  NaN counts as -infinity.
-// ---------------------------------------------------------------------------
 // What the lanes of a group trade when a reduction joins neighbours, then
 // pairs, fours and so on: the other half's value (mirrored inside a row of 16,
 // whose parts hold one value each by then).
@@ -175,6 +170,11 @@ __device__ inline void across(Step step)
         step(WaveTrade<32>{});
 }
 
+// ---------------------------------------------------------------------------
+// A token's K best experts and their softmax weights.  G lanes share a token,
+// lane l of them holds experts l, l+G, ...; K times: the largest logit left
+// (lowest expert among equals) is taken out.  NaN counts as -infinity.
+// ---------------------------------------------------------------------------
 template <int G, int V, bool BF16>
 __global__ __launch_bounds__(256) void topk_route_kernel(int64_t tokens, int E, int K, const void* logits,
                                                          int renorm, int32_t* idx, float* w)
