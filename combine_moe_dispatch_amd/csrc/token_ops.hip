@@ -31,6 +31,13 @@ __device__ inline void store_row(const v4u& v, v4u* p)
 // lanes of a wave; the norm is of the fp32 sum,
 // not of its bf16 rounding, and the codes are of the fp32 result, not of y's
 // bf16 rounding, so each output is rounded once.
+//
+// Where mean(s^2) + eps is below 2^-100, squares may have left fp32's range
+// (s below 2^-63 in a row with an eps as small): the sum is then that of (2^80
+// s)^2, with 2^160 eps, and y = 2^80 s / its root.  A wave forms it where its
+// own share of the sum is below 2^-80, which holds for every wave of such a
+// row (65536 * 2^-100 at most); its largest square is then below 2^80, its
+// smallest 2^-106 (bf16's smallest number is 2^-133).
 // ---------------------------------------------------------------------------
 struct NormArgs {
     int64_t rows;
@@ -50,7 +57,7 @@ struct NormArgs {
 template <int V, int STREAM, int LANES>
 __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int waves_per_row)
 {
-    __shared__ float part[16];
+    __shared__ float part[2][16];
     const int lane = threadIdx.x % LANES;
     const int wave = threadIdx.x / LANES;
     const int per_block = blockDim.x / LANES / waves_per_row;
@@ -85,16 +92,37 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
 #pragma unroll
     for (int d = LANES / 2; d; d >>= 1)
         sum += __shfl_xor(sum, d, LANES);
-    if (LANES == WAVE && waves_per_row > 1) {
-        if (lane == 0)
-            part[wave] = sum;
-        __syncthreads();
-        sum = 0.0f;
-        const int w0 = wave / waves_per_row * waves_per_row;
-        for (int w = 0; w < waves_per_row; ++w)
-            sum += part[w0 + w];
+    constexpr float UP = 0x1p80f;
+    float small = 0.0f;                  // the sum of (UP s)^2, where sum is below 2^-80
+    if (sum < 0x1p-80f) {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                small = fmaf(s[u][c] * UP, s[u][c] * UP, small);
+#pragma unroll
+        for (int d = LANES / 2; d; d >>= 1)
+            small += __shfl_xor(small, d, LANES);
     }
-    const float r = 1.0f / sqrtf(sum / (float)a.hidden + a.eps);
+    if (LANES == WAVE && waves_per_row > 1) {
+        if (lane == 0) {
+            part[0][wave] = sum;
+            part[1][wave] = small;
+        }
+        __syncthreads();
+        sum = small = 0.0f;
+        const int w0 = wave / waves_per_row * waves_per_row;
+        for (int w = 0; w < waves_per_row; ++w) {
+            sum += part[0][w0 + w];
+            small += part[1][w0 + w];
+        }
+    }
+    float mean = sum / (float)a.hidden + a.eps, up = 1.0f;
+    if (mean < 0x1p-100f) {
+        mean = small / (float)a.hidden + a.eps * UP * UP;
+        up = UP;
+    }
+    const float r = 1.0f / sqrtf(mean);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         const int v = u * nt + t;
@@ -113,6 +141,8 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+            s[u][2 * c] *= up;
+            s[u][2 * c + 1] *= up;
             s[u][2 * c] *= r * bf16_lo(wv[c]);
             s[u][2 * c + 1] *= r * bf16_hi(wv[c]);
             top = fmaxf(top, fmaxf(fabsf(s[u][2 * c]), fabsf(s[u][2 * c + 1])));

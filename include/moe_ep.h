@@ -406,7 +406,9 @@ int moe_hbm_probe(int kind, void* dst, const void* src, size_t bytes, hipStream_
  * rounding, nor the codes y's).  At least one output is given.  hidden a
  * multiple of 8 (of 128 with y_q), <= 65536.  residual_out and y may be x or
  * residual themselves.  The sum of squares is an fp32 sum: elements above
- * about 1e19/sqrt(hidden) overflow it. */
+ * about 1e19/sqrt(hidden) overflow it; small ones keep their norm down to
+ * bf16's smallest number, whatever eps.  A row of zeros gives zeros, but with
+ * eps 0 it is 0/0: NaN, in y and its codes. */
 int moe_add_rmsnorm(int32_t rows, int32_t hidden, const void* x, const void* residual,
                     const void* weight, float eps, void* residual_out, void* y, void* y_q,
                     float* y_scale, hipStream_t stream);
