@@ -85,6 +85,21 @@ __device__ inline float wave_sum(float v)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), WAVE - 1));
 }
 
+// exp(x).  The exponential instruction is of base 2: x log2(e) rounded to fp32
+// would leave an error of |x| 2^-24 in the result, so what that rounding and
+// the constant's lose, r, goes into it as 2^r = 1 + r ln 2.  Off by four
+// roundings of 2^-24, zero below the normal numbers, +infinity above the
+// largest, 2^-288 (zero) and 2^288 (infinity) for the infinities.
+__device__ inline float exp_of(float x)
+{
+    constexpr double LOG2E = 1.4426950408889634074;
+    constexpr float HI = (float)LOG2E, LO = (float)(LOG2E - HI);
+    x = fminf(fmaxf(x, -200.0f), 200.0f);
+    const float t = x * HI;
+    const float r = fmaf(x, LO, fmaf(x, HI, -t));
+    return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718f, 1.0f);
+}
+
 // The dispatch payload's block scale from a block's largest magnitude:
 // scale = amax/448 and inv = 448/amax (correctly rounded divisions), the
 // scale held at the smallest normal number, 1 for a block of zeros.

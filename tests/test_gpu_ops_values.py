@@ -85,3 +85,36 @@ def test_norm_zero_rows():
                     assert bool(torch.isnan(y[t].float()).all()) and bool(((yq[t] & 0x7F) == 0x7F).all())
                 else:
                     assert bool((y[t] == 0).all()) and bool((yq[t] == 0).all())
+
+
+# --- routing --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("E,K", [(8, 8), (16, 12), (50, 16), (128, 16), (256, 16), (64, 40), (200, 64), (512, 64),
+                                 (1024, 64)])
+@pytest.mark.parametrize("bf", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_far_weights(E, K, bf, renorm):
+    """Weights of experts far below the best.  The best logit is 0, so z - best
+    is exact.  In roundings of 2^-24: the exponential of a chosen expert 4 (its
+    argument's and the instruction's last place); the sum of all of them, at
+    most 22 additions in a row, and its terms' 2 + |z|, of which the softmax
+    mean of |z| counts, at most 5 for 1024 experts; the quotient 1: below
+    2^-19."""
+    say(f"[gpu] route far weights E={E} K={K} bf16={bf} renorm={renorm}")
+    g = rng(2, E, K)
+    T = 300
+    z = -85 * g.random((T, E)) ** 0.7
+    z[np.arange(T), g.integers(0, E, T)] = 0
+    z[:20, :] = np.where(z[:20] == 0, 0, -5.5)          # many near the best: the sum's worst
+    t = torch.from_numpy(z.astype(np.float32)).to(torch.bfloat16 if bf else torch.float32).to(DEV)
+    idx = torch.empty((T, K), dtype=torch.int32, device=DEV)
+    w = torch.empty((T, K), device=DEV)
+    mep.moe_topk_route(T, E, K, t, mep.MOE_BF16 if bf else mep.MOE_FP32, renorm, idx, w)
+    torch.cuda.synchronize()
+    v = R.f64(t)
+    order = np.argsort(-v, axis=-1, kind="stable")[:, :K]
+    assert np.array_equal(idx.cpu().numpy(), order)
+    p = np.exp(v)
+    ref = np.take_along_axis(p, order, -1)
+    ref = ref / (ref if renorm else p).sum(-1, keepdims=True)
+    assert np.all(np.abs(R.f64(w) - ref) <= 2.0 ** -19 * ref + 2.0 ** -126)
