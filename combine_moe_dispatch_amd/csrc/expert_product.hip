@@ -623,7 +623,7 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
 #pragma unroll
             for (int c = 0; c < C::OUTS; ++c) {
                 const float g = acc[j][i][c], u = acc[(j + HALF) % C::NT][i][c];
-                const float h = g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+                const float h = silu(g) * u;
                 acc[j][i][c] = h;
                 top = fmaxf(top, fabsf(h));
             }

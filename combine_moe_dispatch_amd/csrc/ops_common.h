@@ -94,11 +94,17 @@ __device__ inline float exp_of(float x)
 {
     constexpr double LOG2E = 1.4426950408889634074;
     constexpr float HI = (float)LOG2E, LO = (float)(LOG2E - HI);
-    x = fminf(fmaxf(x, -200.0f), 200.0f);
+    x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);       // NaN as -200
     const float t = x * HI;
     const float r = fmaf(x, LO, fmaf(x, HI, -t));
     return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718f, 1.0f);
 }
+
+// The experts' activation, the same for every operator that forms it.  The
+// reciprocal is off by one place of 2^-23 at most; a division by the letter
+// cost gate/up 5-10% where k is short (16 experts, 16384 rows, f 4096, k 512
+// 238-242 us against 226-229).  NaN stays NaN.
+__device__ inline float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + exp_of(-v)); }
 
 // The dispatch payload's block scale from a block's largest magnitude:
 // scale = amax/448 and inv = 448/amax (correctly rounded divisions), the

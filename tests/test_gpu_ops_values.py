@@ -118,3 +118,92 @@ def test_route_far_weights(E, K, bf, renorm):
     ref = np.take_along_axis(p, order, -1)
     ref = ref / (ref if renorm else p).sum(-1, keepdims=True)
     assert np.all(np.abs(R.f64(w) - ref) <= 2.0 ** -19 * ref + 2.0 ** -126)
+
+
+# --- the experts' activation ------------------------------------------------------------------------
+
+def one_hot_rows(rows, k):
+    """Rows of a single code 1 at place 0, scale 1."""
+    x = torch.zeros((rows, k), dtype=torch.uint8, device=DEV)
+    x[:, 0] = 0x38
+    return x, torch.ones((rows, k // 128), device=DEV)
+
+
+GATES = np.concatenate([-np.exp2(np.linspace(-6, 6.4, 40)), [0.0, -86.5, 1.0, 17.0, 88.0]])
+
+
+def gate_weights(f, k):
+    """Weights whose gate and up products of a one-hot row are a code times a
+    scale: gate block b has the gates GATES[b] * (1 .. 15)/8, rounded to fp32
+    with the scale; up is 1."""
+    w = torch.zeros((2 * f, k), dtype=torch.uint8)
+    w[:f, 0] = torch.arange(f).remainder(8).to(torch.uint8) + 0x38          # 1, 1.125 .. 1.875
+    w[f:, 0] = 0x38
+    s = torch.ones((2 * f // 128, k // 128))
+    s[: f // 128, 0] = torch.from_numpy(np.resize(GATES, f // 128).astype(np.float32))
+    code = 1 + np.arange(f) % 8 / 8
+    gate = np.repeat(s[: f // 128, 0].double().numpy(), 128) * code
+    return w[None].contiguous().to(DEV), s[None].contiguous().to(DEV), gate
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_gate_up_scales_of_large_gates(rows):
+    """The scale is the block's largest |silu(gate)| / 448 in fp32.  The gate is
+    a code times the scale, rounded once, which the reference rounds alike; in
+    roundings of 2^-24: exponential 4, sum 1, quotient 3 at most, division by
+    448 1: 9."""
+    say(f"[gpu] gate_up scales of large gates rows={rows}")
+    f, k = 128 * len(GATES), 128
+    x, xs = one_hot_rows(rows, k)
+    w, ws, gate = gate_weights(f, k)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    h = torch.empty((rows, f), dtype=torch.uint8, device=DEV)
+    hs = torch.empty((rows, f // 128), device=DEV)
+    mep.moe_expert_gate_up(rows, 1, f, k, x, xs, off, w, ws, h, hs)
+    torch.cuda.synchronize()
+    v = gate.astype(np.float32).astype(np.float64)
+    ref = np.abs(v / (1 + np.exp(-v))).reshape(-1, 128)
+    at = ref.argmax(-1)
+    want = ref.max(-1) / 448
+    g = np.abs(v.reshape(-1, 128)[np.arange(len(at)), at])
+    want = np.where(want == 0, 1.0, np.maximum(want, 2.0 ** -126))
+    got = R.f64(hs)
+    assert np.all(got == got[:1])
+    off_by = np.abs(got[0] - want) / want * 2.0 ** 24
+    normal = want > 2.0 ** -120
+    assert np.all(off_by[normal] <= 9), (g[normal], off_by[normal])
+
+
+def test_silu_alike():
+    """gate_up and the few-token layer form the same h: with one expert, one
+    token and one block of f they give the same bits through the same down product."""
+    say("[gpu] silu alike")
+    H, k = 128, 128
+    for gate in (0.3, -3.0, -21.0, -60.0, 5.0):
+        f = 128
+        w = torch.zeros((1, 2 * f, k), dtype=torch.uint8, device=DEV)
+        w[0, :f, 0] = (torch.arange(f) % 8).to(torch.uint8).to(DEV) + 0x38
+        w[0, f:, 0] = 0x38
+        s13 = torch.ones((1, 2, 1), device=DEV)
+        s13[0, 0, 0] = gate
+        x = torch.zeros((1, k), dtype=torch.bfloat16, device=DEV)
+        x[0, 0] = 1.0                                      # codes as 448, scale 1/448
+        q = torch.zeros((1, k), dtype=torch.uint8, device=DEV)
+        q[0, 0] = 0x7E
+        xs = torch.full((1, 1), 1.0 / 448, device=DEV)
+        off = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+        h = torch.empty((1, f), dtype=torch.uint8, device=DEV)
+        hs = torch.empty((1, 1), device=DEV)
+        mep.moe_expert_gate_up(1, 1, f, k, q, xs, off, w, s13, h, hs)
+        # the down product of the few-token layer picks out h's codes one by one, and adds the
+        # scale's last bits: w2 = 1 at (n, n), s2 = 1, so out[n] = bf16(code * scale)
+        w2 = torch.zeros((1, H, f), dtype=torch.uint8, device=DEV)
+        w2[0, torch.arange(f), torch.arange(f)] = 0x38
+        s2 = torch.ones((1, 1, 1), device=DEV)
+        out = torch.empty((1, H), dtype=torch.bfloat16, device=DEV)
+        ws = torch.empty(mep.moe_few_token_workspace(1, 1, H, f), dtype=torch.uint8, device=DEV)
+        idx = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+        mep.moe_few_token_layer(1, 1, 1, H, f, x, idx, torch.ones((1, 1), device=DEV), w, s13, w2, s2, out, ws)
+        torch.cuda.synchronize()
+        want = (h.view(torch.float8_e4m3fn).float() * hs).to(torch.bfloat16)
+        assert torch.equal(out, want), gate
