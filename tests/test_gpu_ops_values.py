@@ -207,3 +207,65 @@ def test_silu_alike():
         torch.cuda.synchronize()
         want = (h.view(torch.float8_e4m3fn).float() * hs).to(torch.bfloat16)
         assert torch.equal(out, want), gate
+
+
+# --- the product's sums -----------------------------------------------------------------------------
+
+def product_bound(x, w):
+    """Of rows x [r][k] and weights w [n][k] (values, scales 1): the product in
+    64 bits and what the call may add to it.  Of every 8 consecutive products,
+    seven are cut by less than 2^-13 of the largest (a code below 2^-6, the
+    smallest normal one, counts as that); the other sums are fp32, 16 of 8 in a
+    block and then the blocks, each addition off by 2^-23 of the magnitudes at
+    most; and the result is rounded to bf16."""
+    p = x[:, None, :] * w[None]
+    floor = lambda v: np.where(v == 0, 0, np.maximum(np.abs(v), 2.0 ** -6))  # noqa: E731
+    top = (floor(x)[:, None, :] * floor(w)[None]).reshape(*p.shape[:2], -1, 8).max(-1).sum(-1)
+    ref = p.sum(-1)
+    off = 7 * 2.0 ** -13 * top + (16 + x.shape[1] // 128) * 2.0 ** -23 * np.abs(p).sum(-1)
+    return ref, R.BF16_HALF * (np.abs(ref) + off) + off
+
+
+@pytest.mark.parametrize("kind", ["outliers", "cancelling", "subnormal", "random"])
+@pytest.mark.parametrize("rows,n", [(16, 64), (300, 16384)])
+def test_matmul_bound(kind, rows, n):
+    """The documented bound, where one product of every 8 is far above the
+    rest, where such products cancel, and among the format's smallest numbers;
+    in the narrow kernel and in a tile (whose first and last rows are looked at)."""
+    say(f"[gpu] matmul bound {kind} rows={rows} n={n}")
+    g = rng(3, rows, n)
+    k = 1024
+    lut = R.LUT
+    pick = lambda lo, hi, shape: (lambda v: g.choice(v, shape) * g.choice([1.0, 1.0, -1.0], shape))(  # noqa: E731
+        lut[(lut >= lo) & (lut <= hi)])
+    some = 24
+    x, w = pick(0.5, 8, (some, k)), pick(0.5, 4, (64, k))
+    if kind in ("outliers", "cancelling"):
+        x[:, ::8], w[:, ::8] = pick(256, 448, (some, k // 8)), pick(256, 448, (64, k // 8))
+        x[some // 2:], w[32:] = np.abs(x[some // 2:]), np.abs(w[32:])          # cuts that add up
+        # products just below a multiple of what is kept beside 256 * 256
+        x[::3, 1:8], w[::3, 1:8], x[::3, 0], w[::3, 0] = 3.75, 2, 256, 256
+    if kind == "cancelling":
+        x[:, 8::16], w[:, 8::16] = -x[:, ::16], w[:, ::16]
+    if kind == "subnormal":
+        x, w = pick(2.0 ** -9, 2.0 ** -5, (some, k)), pick(2.0 ** -9, 1, (64, k))
+        w[:, ::8] = 256
+    if kind == "random":
+        x, w = pick(2.0 ** -9, 448, (some, k)), pick(2.0 ** -9, 448, (64, k))
+    ref, tol = product_bound(x, w)
+    codes = lambda v: torch.from_numpy(v.astype(np.float32)).to(torch.float8_e4m3fn)  # noqa: E731
+    xr = codes(np.resize(x, (rows, k))).to(DEV)
+    wr = codes(np.resize(w, (n, k)))[None].contiguous().to(DEV)
+    xs = torch.ones((rows, k // 128), device=DEV)
+    ws = torch.ones((1, n // 128 + (n % 128 > 0), k // 128), device=DEV)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    y = torch.empty((rows, n), dtype=torch.bfloat16, device=DEV)
+    mep.moe_expert_matmul(rows, 1, n, k, xr, xs, off, wr, ws, y)
+    torch.cuda.synchronize()
+    got = R.f64(y)
+    m = min(rows, some)
+    assert np.all(np.abs(got[:m, :64] - ref[:m]) <= tol[:m])
+    assert np.all(np.abs(got[:m, n - 64:] - ref[:m]) <= tol[:m])
+    if rows > some:
+        last = rows // some * some - some
+        assert np.all(np.abs(got[last: last + some, :64] - ref) <= tol)
