@@ -356,12 +356,10 @@ def _op_stream(stream, dev: int):
 
 
 def _op_arg(a, call: str, name: str, numel: int, width: int, dtypes, dev: int):
-    if a is None or type(a) is int:
+    if a is None or isinstance(a, int):
         return a
     if a.dtype in dtypes and a.get_device() == dev and a.is_contiguous() and a.numel() >= numel:
         return a.data_ptr()
-    if isinstance(a, int):
-        return a
     if not a.is_cuda:
         bad = "not a device tensor"
     elif a.get_device() != dev:

@@ -104,3 +104,13 @@ def test_tensors_are_checked():
     x = torch.zeros((2, 256), dtype=torch.bfloat16)
     with pytest.raises(mep.MoeError, match="x not a device tensor"):
         mep.moe_add_rmsnorm(2, 256, x, None, A, 1e-6, None, A, None, None, stream=0)
+
+
+def test_addresses_of_any_int_type():
+    """An int subclass is an address, as the four calls take it."""
+    class Address(int):
+        pass
+
+    args = {**NORM, "x": Address(A), "weight": Address(A + 2)}
+    refused(mep.moe_add_rmsnorm, *args.values())                 # by the library: misaligned
+    assert mep._op_arg(Address(A), "call", "x", 1 << 40, 2, (), 0) == A
