@@ -64,10 +64,9 @@ struct Tile {
     static constexpr int FRAGS = NT * ROUNDS;            // weight operands of a block
     static_assert(FRAGS % 2 == 0, "two operands are read ahead in turn");
     static constexpr int OUTS = SUB * SUB / WAVE;        // outputs per lane
-    // vector instructions beside each matrix instruction: a round's share of
-    // the joins and the next operand's conversions, spread evenly
+    // joins of a round, and how many go beside each e4m3 matrix instruction
     static constexpr int JOINS = MT * OUTS / ROUNDS;
-    static constexpr int BESIDE = (JOINS + (EIGHT ? 0 : 8)) / (MT * STEPS);
+    static constexpr int BESIDE = JOINS / MT;
     static_assert(!EIGHT || SUB == 16, "the e4m3 instruction takes a whole block of 16 rows");
 
     static constexpr int W_BYTES = BN * SCALE_BLOCK, X_BYTES = BM * SCALE_BLOCK;
@@ -231,6 +230,7 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
 template <class C, bool GATE_UP>
 __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place& at, uint8_t* lds)
 {
+    static_assert(C::EIGHT == !GATE_UP, "each operator has its arithmetic");
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % C::WM, wn = wave / C::WM;
@@ -398,19 +398,17 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
         wait_loads_and_meet<0>();
     int slot = 0;
     read_scales(0);
-    // One block, with the e4m3 instruction.  `steady`: stage kb+S exists and is
+    // One block of the product, with the e4m3 instruction.  `steady`: stage kb+S exists and is
     // loaded into the slot that this block frees; else (the last S blocks)
     // nothing more is loaded.
     auto step8 = [&](const int kb, auto steady) {
         const uint8_t* st = lds + slot * C::STAGE;
         if (steady && (kb + C::S) % C::SC_STEPS == 0)
             issue_scales(kb + C::S);
-        float sg[C::MT], su[C::MT];
+        float sg[C::MT];
 #pragma unroll
-        for (int i = 0; i < C::MT; ++i) {
+        for (int i = 0; i < C::MT; ++i)
             sg[i] = xsc[i] * gs;
-            su[i] = xsc[i] * us;
-        }
         Operand<C> xf[C::MT][C::ROUNDS], wf;
         wf.from(wraw[0]);
 #pragma unroll
@@ -447,14 +445,12 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
                     read_scales(kb + 1);
                 }
 #pragma unroll
-                for (int s = 0; s < C::STEPS; ++s)
-#pragma unroll
-                    for (int i = 0; i < C::MT; ++i)
-                        t[i] = product_step(wf.f[s], xf[i][r].f[s], t[i]);
+                for (int i = 0; i < C::MT; ++i)
+                    t[i] = product_step(wf.f[0], xf[i][r].f[0], t[i]);
                 join(j > 0 ? j - 1 : C::NT - 1, r);
                 wf = wnext;
 #pragma unroll
-                for (int i = 0; i < C::MT * C::STEPS; ++i) {
+                for (int i = 0; i < C::MT; ++i) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // a matrix instruction,
                     __builtin_amdgcn_sched_group_barrier(0x002, C::BESIDE, 0);  // what goes beside it
                 }
@@ -462,11 +458,11 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
 #pragma unroll
             for (int i = 0; i < C::MT; ++i) {
                 held[i] = t[i];
-                held_s[i] = GATE_UP && j >= C::NT / 2 ? su[i] : sg[i];
+                held_s[i] = sg[i];
             }
         }
     };
-    // The same through fp16, round by round: each round converts the next one's
+    // The same of gate_up through fp16, round by round: each round converts the next one's
     // pieces of both operands while its products run, so that no conversion
     // waits for the block to end.  All of a block's products stay open to its
     // last round; the first half of them joins there, the second half in the
@@ -508,7 +504,7 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
 #pragma unroll
         for (int i = 0; i < C::MT; ++i) {
             sg[i] = xsc[i] * gs;
-            su[i] = xsc[i] * (GATE_UP ? us : gs);
+            su[i] = xsc[i] * us;
         }
 #pragma unroll
         for (int r = 0; r < C::ROUNDS; ++r) {
