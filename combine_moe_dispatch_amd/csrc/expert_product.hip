@@ -833,8 +833,9 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-// The tile.  With few rows per expert the weights are what costs, each read
-// once: low tiles, several workgroups per CU, nontemporal loads.  With many,
+// The form of a call: the narrow kernel, or the launch's tile.  With few rows
+// per expert the weights are what costs, each read once: low tiles, several
+// workgroups per CU, nontemporal loads.  With many,
 // the matrix unit: high tiles, whose loads and LDS reads serve more products,
 // and a lower tile for an expert's last rows.  And a launch of fewer workgroups
 // than CUs waits for memory step by step: lower tiles, narrower ones, a deeper
@@ -879,47 +880,76 @@ hipError_t launch(const ExpertProduct& p, hipStream_t stream)
 //    besides, mean 90 287-309 against 308-326; with 32 besides,
 //    256 experts of about 128, f 2048, k 7168 2733 against 2778.  (256 rows would
 //    need twice the accumulators.)
-template <bool GATE_UP>
-hipError_t choose(const ExpertProduct& p, hipStream_t stream)
+enum class Form { NARROW, ROWS32_DEEP, ROWS32, ROWS64, ROWS128, ROWS256 };
+
+Form form_of(bool gate_up, const ExpertProduct& p)
 {
-    if (p.rows == 0)
-        return hipSuccess;
     const int64_t mean = p.rows / p.E;
-    constexpr bool EIGHT = !GATE_UP;
-    const int n_tiles = GATE_UP ? p.n / 256 : (p.n + 255) / 256;
-    if (EIGHT && workgroups(p, NARROW_ROWS, (p.n + NARROW_COLS - 1) / NARROW_COLS) <= 720)
-        return launch_narrow(p, stream);
+    const int n_tiles = gate_up ? p.n / 256 : (p.n + 255) / 256;
+    if (!gate_up && workgroups(p, NARROW_ROWS, (p.n + NARROW_COLS - 1) / NARROW_COLS) <= 720)
+        return Form::NARROW;
     if (workgroups(p, 32, n_tiles) <= 256)
-        return launch<GATE_UP, Tile<32, 256, 1, 8, 4, EIGHT, 16, true>, Tile<16, 256, 1, 8, 4, EIGHT, 16, true>>(
-            p, stream);
+        return Form::ROWS32_DEEP;
     if (mean <= 20)
-        return launch<GATE_UP, Tile<32, 256, 1, 8, 2, EIGHT, 16, true>, Tile<16, 256, 1, 8, 2, EIGHT, 16, true>>(
-            p, stream);
+        return Form::ROWS32;
     if (mean <= 48 || workgroups(p, 128, n_tiles) < 200)
-        return launch<GATE_UP, Tile<64, 256, 1, 8, 3, EIGHT, 16, true>, Tile<48, 256, 1, 8, 3, EIGHT, 16, true>,
-                      Tile<32, 256, 1, 8, 3, EIGHT, 16, true>>(p, stream);
-    if constexpr (EIGHT) {
-        if (mean <= 96 || workgroups(p, 256, n_tiles) < 200)
-            return launch<GATE_UP, Tile<128, 256, 2, 4, 3, true, 16, true>, Tile<96, 256, 2, 4, 3, true, 16, true>,
-                          Tile<64, 256, 1, 8, 3, true, 16, true>>(p, stream);
-        return launch<GATE_UP, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<192, 256, 4, 2, 2, true, 16, false>,
-                      Tile<128, 256, 2, 4, 3, true, 16, false>, Tile<64, 256, 1, 8, 3, true, 16, false>>(p, stream);
-    } else {
-        return launch<GATE_UP, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<96, 256, 1, 8, 3, false, 16, false>,
-                      Tile<64, 256, 1, 8, 3, false, 16, false>, Tile<32, 256, 1, 8, 4, false, 16, false>>(p, stream);
-    }
+        return Form::ROWS64;
+    return gate_up || mean <= 96 || workgroups(p, 256, n_tiles) < 200 ? Form::ROWS128 : Form::ROWS256;
 }
 
 }  // namespace
 
+const char* product_form(bool gate_up, const ExpertProduct& p)
+{
+    switch (form_of(gate_up, p)) {
+    case Form::NARROW: return "narrow";
+    case Form::ROWS32_DEEP: return "32 deep";
+    case Form::ROWS32: return "32";
+    case Form::ROWS64: return "64";
+    case Form::ROWS128: return "128";
+    default: return "256";
+    }
+}
+
 hipError_t launch_expert_matmul(const ExpertProduct& p, hipStream_t stream)
 {
-    return choose<false>(p, stream);
+    if (p.rows == 0)
+        return hipSuccess;
+    switch (form_of(false, p)) {
+    case Form::NARROW:
+        return launch_narrow(p, stream);
+    case Form::ROWS32_DEEP:
+        return launch<false, Tile<32, 256, 1, 8, 4, true, 16, true>, Tile<16, 256, 1, 8, 4, true, 16, true>>(p, stream);
+    case Form::ROWS32:
+        return launch<false, Tile<32, 256, 1, 8, 2, true, 16, true>, Tile<16, 256, 1, 8, 2, true, 16, true>>(p, stream);
+    case Form::ROWS64:
+        return launch<false, Tile<64, 256, 1, 8, 3, true, 16, true>, Tile<48, 256, 1, 8, 3, true, 16, true>,
+                      Tile<32, 256, 1, 8, 3, true, 16, true>>(p, stream);
+    case Form::ROWS128:
+        return launch<false, Tile<128, 256, 2, 4, 3, true, 16, true>, Tile<96, 256, 2, 4, 3, true, 16, true>,
+                      Tile<64, 256, 1, 8, 3, true, 16, true>>(p, stream);
+    default:
+        return launch<false, Tile<256, 256, 4, 2, 2, true, 16, false>, Tile<192, 256, 4, 2, 2, true, 16, false>,
+                      Tile<128, 256, 2, 4, 3, true, 16, false>, Tile<64, 256, 1, 8, 3, true, 16, false>>(p, stream);
+    }
 }
 
 hipError_t launch_expert_gate_up(const ExpertProduct& p, hipStream_t stream)
 {
-    return choose<true>(p, stream);
+    if (p.rows == 0)
+        return hipSuccess;
+    switch (form_of(true, p)) {
+    case Form::ROWS32_DEEP:
+        return launch<true, Tile<32, 256, 1, 8, 4, false, 16, true>, Tile<16, 256, 1, 8, 4, false, 16, true>>(p, stream);
+    case Form::ROWS32:
+        return launch<true, Tile<32, 256, 1, 8, 2, false, 16, true>, Tile<16, 256, 1, 8, 2, false, 16, true>>(p, stream);
+    case Form::ROWS64:
+        return launch<true, Tile<64, 256, 1, 8, 3, false, 16, true>, Tile<48, 256, 1, 8, 3, false, 16, true>,
+                      Tile<32, 256, 1, 8, 3, false, 16, true>>(p, stream);
+    default:
+        return launch<true, Tile<128, 256, 2, 4, 3, false, 32, false>, Tile<96, 256, 1, 8, 3, false, 16, false>,
+                      Tile<64, 256, 1, 8, 3, false, 16, false>, Tile<32, 256, 1, 8, 4, false, 16, false>>(p, stream);
+    }
 }
 
 }  // namespace ops

@@ -26,6 +26,8 @@ struct ExpertProduct {
 
 hipError_t launch_expert_matmul(const ExpertProduct& p, hipStream_t stream);
 hipError_t launch_expert_gate_up(const ExpertProduct& p, hipStream_t stream);
+// The form that a call of these rows, E and n takes, for the tests.
+const char* product_form(bool gate_up, const ExpertProduct& p);
 
 hipError_t launch_add_rmsnorm(int64_t rows, int hidden, const uint16_t* x, const uint16_t* residual,
                               const uint16_t* weight, float eps, uint16_t* residual_out, uint16_t* y,

@@ -143,6 +143,17 @@ int moe_expert_gate_up(int32_t rows, int32_t num_experts, int32_t f, int32_t k, 
     return from_hip(moe::ops::launch_expert_gate_up(p, stream));
 }
 
+// Not part of the public ABI: which kernel a product takes (n: weight rows per
+// expert, 2f for gate_up), so that tests can say which one they check.
+const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_experts, int32_t n)
+{
+    moe::ops::ExpertProduct p{};
+    p.rows = rows;
+    p.E = num_experts;
+    p.n = n;
+    return moe::ops::product_form(gate_up != 0, p);
+}
+
 size_t moe_few_token_workspace(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t f)
 {
     if (num_tokens < 1 || num_tokens > MOE_FEW_TOKENS_MAX || top_k < 1 || top_k > moe::MAX_TOPK ||

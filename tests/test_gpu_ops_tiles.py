@@ -1,0 +1,242 @@
+"""The experts' products in every kernel form, asked of the library case by
+case: k long enough that the ring of stages and the row scales' buffers turn
+several times, experts whose last rows fall into every lower tile, empty
+experts, rows of zeros and a row with a NaN, rows behind the last; the widest
+rows; the first call of a process captured.  References in 64 bits on the GPU.
+
+Bounds, per output, of sums S with magnitudes M = sum |x w|:
+ * fp32 sums (gate_up): 16 steps inside a block, then its blocks, each off by
+   2^-23 M at most;
+ * the product's groups of 8 besides, 7 * 2^-13 of the largest of 8, held by
+   the product of the largest |x| and |w| (a code below 2^-6 counting as that).
+"""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+from tests import ops_ref as R
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import ctypes  # noqa: E402
+
+import combine_moe_dispatch_amd as mep  # noqa: E402
+
+DEV = "cuda"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+_form = mep._lib.moe_ops_product_form
+_form.argtypes, _form.restype = [ctypes.c_int32] * 4, ctypes.c_char_p
+
+
+def form(gate_up, rows, E, n):
+    return _form(int(gate_up), rows, E, n).decode()
+
+
+def codes(gen, *shape):
+    """Random finite codes."""
+    q = torch.empty(shape, dtype=torch.uint8, device=DEV)
+    for part in q.view(-1).split(1 << 28):
+        part.random_(0, 256, generator=gen)
+        part[(part & 0x7F) == 0x7F] = 0x38
+    return q
+
+
+def value(q):
+    return q.view(torch.float8_e4m3fn).float().double()
+
+
+def make(seed, E, counts, spare, n, k, spread):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    rows = int(sum(counts)) + spare
+    x, w = codes(gen, rows, k), codes(gen, E, n, k)
+    xs = torch.exp(0.5 * torch.randn((rows, k // 128), generator=gen, device=DEV))
+    ws = torch.exp(torch.randn((E, -(-n // 128), k // 128), generator=gen, device=DEV)) * spread
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    return x, xs, w, ws, off
+
+
+def reference(x, xs, w, ws, rows, e):
+    """Of the given rows of x with expert e: S, the fp32 sums' error, and the
+    error of the groups of 8."""
+    k = x.shape[1]
+    S = M = T = 0
+    for a in range(0, k, 8192):                     # k by parts: the widest rows in 64 bits are large
+        b = min(k, a + 8192)
+        s8 = slice(a // 128, b // 128)
+        xv, wv = value(x[rows, a:b]), value(w[e, :, a:b])
+        xf, wf = (torch.where(v == 0, v, v.abs().clamp_min(2.0 ** -6)) for v in (xv, wv))
+        xsc = xs[rows, s8].double()
+        wsc = ws[e, :, s8].double().repeat_interleave(128, 0)[: w.shape[1]]
+        xr, wr = xsc.repeat_interleave(128, 1), wsc.repeat_interleave(128, 1)
+        S = S + (xv * xr) @ (wv * wr).T
+        M = M + (xv * xr).abs() @ (wv * wr).abs().T
+        top = lambda f, sc: f.unflatten(1, (-1, 8)).amax(-1) * sc.repeat_interleave(16, 1)  # noqa: E731
+        T = T + top(xf, xsc) @ top(wf, wsc).T
+    return S, (16 + k // 128) * 2.0 ** -23 * M, 7 * 2.0 ** -13 * T
+
+
+def silu(v):
+    return v / (1 + torch.exp(-v))
+
+
+def plant(x, off):
+    """A row of zeros (+0 and -0) and a row with one NaN code, where an expert
+    has three rows or more: (zero row, NaN row)."""
+    o = off.tolist()
+    e = max(range(len(o) - 1), key=lambda i: o[i + 1] - o[i])
+    zero, nan = o[e] + 1, o[e + 1] - 1
+    x[zero] = 0
+    x[zero, ::2] = 0x80
+    x[nan, x.shape[1] - 5] = 0x7F
+    return zero, nan
+
+
+def check_matmul(want_form, E, counts, n, k, spare=3, plants=True, some=None):
+    rows = int(sum(counts))
+    assert form(False, rows + spare, E, n) == want_form
+    x, xs, w, ws, off = make(hash((n, k, rows)) & 0xFFFF, E, counts, spare, n, k, 2.0 ** -12)
+    zero, nan = plant(x, off) if plants else (-1, -1)
+    y = torch.full((rows + spare, n), 9.0, dtype=torch.bfloat16, device=DEV)
+    mep.moe_expert_matmul(rows + spare, E, n, k, x, xs, off, w, ws, y)
+    torch.cuda.synchronize()
+    assert bool((y[rows:] == 9.0).all())
+    o = off.tolist()
+    for e in range(E):
+        mine = [r for r in range(o[e], o[e + 1]) if r not in (zero, nan)]
+        if some:                                    # the first, the last and some between
+            mine = sorted(set(mine[:3] + mine[-3:] + mine[:: max(1, len(mine) // some)]))
+        if not mine:
+            continue
+        S, fp32, eight = reference(x, xs, w, ws, mine, e)
+        err, off_by = (y[mine].double() - S).abs(), fp32 + eight
+        tol = R.BF16_HALF * (S.abs() + off_by) + off_by
+        assert bool((err <= tol).all()), (e, float((err / tol).max()))
+        # The bound finds faults: one of KB blocks gone wrong moves results by about 1/sqrt(KB) of
+        # their size.  The bound grows with KB, results with its root: 1% of them at 18 blocks,
+        # 11% at the widest rows' 512, where only the place of a whole row's scales is in doubt.
+        assert float(tol.median()) < (0.1 if k <= 8192 else 0.2) * float(S.abs().median())
+    if plants:
+        assert bool((y[zero] == 0).all()) and bool(torch.isnan(y[nan].float()).all())
+
+
+def check_gate_up(want_form, E, counts, f, k, spare=3, plants=True, some=None):
+    rows = int(sum(counts))
+    assert form(True, rows + spare, E, 2 * f) == want_form
+    x, xs, w, ws, off = make(hash((f, k, rows)) & 0xFFFF, E, counts, spare, 2 * f, k, 2.0 ** -16 / (k / 128) ** 0.5)
+    zero, nan = plant(x, off) if plants else (-1, -1)
+    h = torch.full((rows + spare, f), 5, dtype=torch.uint8, device=DEV)
+    hs = torch.full((rows + spare, f // 128), 9.0, device=DEV)
+    mep.moe_expert_gate_up(rows + spare, E, f, k, x, xs, off, w, ws, h, hs)
+    torch.cuda.synchronize()
+    assert bool((h[rows:] == 5).all()) and bool((hs[rows:] == 9.0).all())
+    o = off.tolist()
+    for e in range(E):
+        mine = [r for r in range(o[e], o[e + 1]) if r not in (zero, nan)]
+        if some:
+            mine = sorted(set(mine[:3] + mine[-3:] + mine[:: max(1, len(mine) // some)]))
+        if not mine:
+            continue
+        S, fp32, _ = reference(x, xs, w, ws, mine, e)
+        g, u, dg, du = S[:, :f], S[:, f:], fp32[:, :f], fp32[:, f:]
+        ref = silu(g) * u
+        # silu's slope is below 1.1; 9 roundings of its own and the product's
+        work = 1.1 * dg * (u.abs() + du) + silu(g).abs() * du + 10 * 2.0 ** -24 * ref.abs()
+        top = work.unflatten(1, (-1, 128)).amax(-1) / 448
+        scale = ref.abs().unflatten(1, (-1, 128)).amax(-1) / 448
+        assert bool(((hs[mine].double() - scale).abs() <= top + 2.0 ** -22 * scale).all())
+        got = value(h[mine]) * hs[mine].double().repeat_interleave(128, 1)
+        tol = (R.E4M3_HALF + 2.0 ** -18) * ref.abs() + 2 * work + (2.0 ** -10 * scale + top).repeat_interleave(128, 1)
+        assert bool(((got - ref).abs() <= tol).all()), e
+    if plants:
+        assert bool((hs[zero] == 1).all()) and bool(((h[zero] & 0x7F) == 0).all())
+        assert bool(((h[nan] & 0x7F) == 0x7F).all())
+
+
+# rows per expert: empty, both sides of every tile's height and of every lower tile's for the last rows
+FEW = [1, 16, 17, 32, 33, 0]
+LOW = [0, 3, 16, 17, 32, 33, 1, 20] * 5
+MID = [0, 1, 32, 33, 48, 49, 64, 65, 100, 20] * 2
+HIGH = [0, 64, 65, 96, 97, 128, 129, 30, 200, 110] * 2
+TOP = [0, 64, 65, 128, 129, 192, 193, 256, 257, 300] * 2
+GATED = [0, 32, 33, 64, 65, 96, 97, 128, 129, 200] * 2
+
+
+@pytest.mark.parametrize("k", [2176, 4224])
+@pytest.mark.parametrize("want,counts,n", [
+    ("narrow", [1, 0, 15, 16, 17], 264), ("32 deep", FEW, 4360), ("32", LOW, 1288), ("64", MID, 1544),
+    ("128", HIGH, 1544), ("256", TOP, 1544)])
+def test_matmul_forms(want, counts, n, k):
+    say(f"[gpu] matmul form {want} k={k}")
+    check_matmul(want, len(counts), counts, n, k)
+
+
+@pytest.mark.parametrize("k", [2176, 4224])
+@pytest.mark.parametrize("want,counts,f", [
+    ("32 deep", FEW, 1280), ("32", LOW, 640), ("64", MID, 768), ("128", GATED, 896)])
+def test_gate_up_forms(want, counts, f, k):
+    say(f"[gpu] gate_up form {want} k={k}")
+    check_gate_up(want, len(counts), counts, f, k)
+
+
+@pytest.mark.parametrize("want,counts,n", [
+    ("narrow", [5], 264), ("32 deep", [64], 5824), ("32", [15] * 10, 4864), ("64", [500], 4352),
+    ("128", [1024], 7680), ("256", [2000], 6400)])
+def test_matmul_forms_widest(want, counts, n):
+    """k of 512 blocks: the weight scales behind the ring fill the CU's LDS."""
+    say(f"[gpu] matmul form {want}, widest rows")
+    check_matmul(want, len(counts), counts, n, 65536, plants=False, some=12)
+
+
+@pytest.mark.parametrize("want,counts,f", [
+    ("32 deep", [64], 512), ("32", [15] * 10, 2432), ("64", [500], 2176), ("128", [1024], 3200)])
+def test_gate_up_forms_widest(want, counts, f):
+    say(f"[gpu] gate_up form {want}, widest rows")
+    check_gate_up(want, len(counts), counts, f, 65536, plants=False, some=12)
+
+
+def captured_first(gate_up, E, counts, n, k):
+    """In a process of its own: the first call of a form is a captured one."""
+    rows = int(sum(counts))
+    x, xs, w, ws, off = make(5, E, counts, 0, n, k, 2.0 ** -14)
+    if gate_up:
+        outs = [torch.empty((rows, n // 2), dtype=torch.uint8, device=DEV),
+                torch.empty((rows, n // 256), device=DEV)]
+        call = lambda: mep.moe_expert_gate_up(rows, E, n // 2, k, x, xs, off, w, ws, *outs)  # noqa: E731
+    else:
+        outs = [torch.empty((rows, n), dtype=torch.bfloat16, device=DEV)]
+        call = lambda: mep.moe_expert_matmul(rows, E, n, k, x, xs, off, w, ws, *outs)  # noqa: E731
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    for _ in range(3):
+        for t in outs:
+            t.view(torch.uint8).fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(outs, want))
+    assert not any(bool((t.view(torch.uint8) == 0xFF).all()) for t in outs)
+    print("captured", form(gate_up, rows, E, n), flush=True)
+
+
+@pytest.mark.parametrize("gate_up,want,counts,n", [
+    (0, "32 deep", FEW, 4360), (0, "32", LOW, 1288), (0, "64", MID, 1544), (0, "128", HIGH, 1544), (0, "256", TOP, 1544),
+    (1, "32 deep", FEW, 2560), (1, "32", LOW, 1280), (1, "64", MID, 1536), (1, "128", GATED, 1792)])
+def test_first_call_of_a_form_captured(gate_up, want, counts, n):
+    say(f"[gpu] first call captured gate_up={gate_up} form {want}")
+    run = f"from tests.test_gpu_ops_tiles import captured_first; captured_first({gate_up}, {len(counts)}, {counts}, {n}, 384)"
+    p = subprocess.run([sys.executable, "-c", run], cwd=ROOT, capture_output=True, text=True, timeout=90)
+    assert p.returncode == 0 and f"captured {want}\n" in p.stdout, p.stdout + p.stderr
