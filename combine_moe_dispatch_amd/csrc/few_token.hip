@@ -766,17 +766,32 @@ __global__ __launch_bounds__(CODE_THREADS) void add_parts_kernel(const float* pa
     *(v2u*)(out + at) = v2u{bf16_pack(sum[0], sum[1]), bf16_pack(sum[2], sum[3])};
 }
 
-// Whether the product kernels code their columns themselves: when an expert
-// has few of them.  Measured (us, direct against coded): 5 tokens, 160 experts,
-// top 3, hidden 768, f 384 17.6 against 21.9; 8 tokens, 8 experts, top 2, hidden
-// 4096, f 2048 40 against 45; 13 tokens of hidden 6400, f 256, 117 experts, top 2
-// 34 against 39; 16 tokens, 64 experts, top 4, hidden 4096, f 2048 191 against
-// 187; but, before the weights came in whole lines, 29 tokens, 5 experts, top 5,
-// hidden 1024, f 1536 65 against 44, 32 tokens, 8 experts, top 2, hidden 4096 90
-// against 60, and 64 tokens of the 256-expert layer 2146 against 1874.
+// Whether the product kernels code their columns themselves.  That saves two
+// launches, some 4 us, and costs by the columns: an expert with more than FEW
+// reads its weights again, and each pass keeps more of the vector unit.  So up
+// to FEW tokens; and up to DIRECT_TOKENS where experts have 2.5 columns at most
+// on average and either few weights are read (256 MB) or columns are few (1/3).
+// Measured (us, direct against coded):
+//  - 5 tokens, 160 experts, top 3, hidden 768, f 384 18.1 against 22.3; 16
+//    tokens, top 1 of 200, hidden 1024, f 512 16.4 against 21.3; 13 tokens, top
+//    2 of 117, hidden 6400, f 256 33.6 against 38.5;
+//  - hidden 4096, f 2048 from here on, 8 experts, top 2: 8 tokens 40 against 46,
+//    10 (2.5 columns) 40 against 45, 12 46.5 against 45.5, 16 58 against 48.5; 8
+//    tokens, top 4 59 against 49; 16 experts, top 4: 12 tokens 100 against 93;
+//  - 64 experts, top 4: 6 tokens (0.4 columns) 114 against 114, 8 139 against 135,
+//    12 177 against 170, 16 188 against 180; 16 experts, top 4 (400 MB): 8 tokens
+//    86 against 81;
+//  - hidden 7168, 256 experts, top 8: 8 tokens (0.25) 445 against 450, 16 (0.5)
+//    816 against 817;
+//  - beyond 16 tokens: 29 tokens, 5 experts, top 5, hidden 1024, f 1536 62 against
+//    38, 32 tokens, 8 experts, top 2, hidden 4096 99 against 51, 64 tokens of the
+//    256-expert layer 1751 against 1675.
 inline bool direct(const FewTokens& p)
 {
-    return p.T <= FEW || (p.T <= DIRECT_TOKENS && p.T * p.K <= FEW * p.E);
+    const int columns = p.T * p.K;
+    const int64_t bytes = (int64_t)std::min(columns, p.E) * 3 * p.F * p.H;
+    return p.T <= FEW ||
+           (p.T <= DIRECT_TOKENS && 2 * columns <= 5 * p.E && (bytes <= (int64_t)256 << 20 || 3 * columns <= p.E));
 }
 
 // Shares of the down product: 512 workgroups, two per CU, as long as each wave
@@ -896,6 +911,12 @@ struct Launches {
 size_t few_token_workspace(int T, int K, int H, int F)
 {
     return Workspace(T, K, H, F).bytes;
+}
+
+const char* few_token_form(const FewTokens& p)
+{
+    const bool split = down_shares(p.T, p.K, p.H, p.F) > 1;
+    return direct(p) ? split ? "direct split" : "direct" : split ? "coded split" : "coded";
 }
 
 hipError_t launch_few_token_layer(const FewTokens& p, hipStream_t stream)

@@ -50,6 +50,8 @@ struct FewTokens {
 };
 
 size_t few_token_workspace(int T, int K, int H, int F);
+// The form that a call of these sizes takes, for the tests.
+const char* few_token_form(const FewTokens& p);
 hipError_t launch_few_token_layer(const FewTokens& p, hipStream_t stream);
 
 }  // namespace ops

@@ -143,8 +143,8 @@ int moe_expert_gate_up(int32_t rows, int32_t num_experts, int32_t f, int32_t k, 
     return from_hip(moe::ops::launch_expert_gate_up(p, stream));
 }
 
-// Not part of the public ABI: which kernel a product takes (n: weight rows per
-// expert, 2f for gate_up), so that tests can say which one they check.
+// These two are not part of the public ABI: which kernels a call takes (n: weight
+// rows per expert, 2f for gate_up), so that tests can say what they check.
 const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_experts, int32_t n)
 {
     moe::ops::ExpertProduct p{};
@@ -152,6 +152,17 @@ const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_expe
     p.E = num_experts;
     p.n = n;
     return moe::ops::product_form(gate_up != 0, p);
+}
+
+const char* moe_ops_few_token_form(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden, int32_t f)
+{
+    moe::ops::FewTokens p{};
+    p.T = num_tokens;
+    p.E = num_experts;
+    p.K = top_k;
+    p.H = hidden;
+    p.F = f;
+    return moe::ops::few_token_form(p);
 }
 
 size_t moe_few_token_workspace(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t f)

@@ -1,6 +1,8 @@
 """What the operators' entry points refuse, which needs no GPU: every check
 comes before any HIP call.  Sizes are paired with made-up aligned addresses
 that no call may reach."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -114,3 +116,27 @@ def test_addresses_of_any_int_type():
     args = {**NORM, "x": Address(A), "weight": Address(A + 2)}
     refused(mep.moe_add_rmsnorm, *args.values())                 # by the library: misaligned
     assert mep._op_arg(Address(A), "call", "x", 1 << 40, 2, (), 0) == A
+
+
+def _form(name, *sizes):
+    fn = getattr(mep._lib, name)
+    fn.argtypes, fn.restype = [ctypes.c_int32] * len(sizes), ctypes.c_char_p
+    return fn(*sizes).decode()
+
+
+@pytest.mark.parametrize("want,T,E,K,H,F", [
+    # up to four tokens; up to 2.5 columns per expert with 256 MB of weights; up to a third with more
+    ("direct", 4, 1, 1, 4096, 2048), ("direct", 10, 8, 2, 4096, 2048), ("coded", 11, 8, 2, 4096, 2048),
+    ("coded", 16, 64, 4, 4096, 2048), ("direct", 5, 64, 4, 4096, 2048), ("coded", 6, 64, 4, 4096, 2048),
+    ("direct", 10, 256, 8, 7168, 2048), ("coded", 11, 256, 8, 7168, 2048), ("coded", 17, 1024, 1, 4096, 128),
+    ("direct split", 10, 187, 6, 384, 2432), ("coded split", 61, 177, 5, 384, 1024)])
+def test_few_token_forms(want, T, E, K, H, F):
+    assert _form("moe_ops_few_token_form", T, E, K, H, F) == want
+
+
+@pytest.mark.parametrize("want,gate_up,rows,E,n", [
+    ("narrow", 0, 64, 1, 5760), ("32 deep", 0, 64, 1, 5824), ("32 deep", 1, 1, 1, 256), ("32", 0, 1024, 256, 4096),
+    ("32", 1, 1024, 256, 4096), ("64", 0, 2000, 64, 7168), ("128", 0, 6144, 64, 7168), ("256", 0, 6208, 64, 7168),
+    ("128", 1, 32768, 256, 4096), ("64", 1, 2000, 2, 1536)])
+def test_product_forms(want, gate_up, rows, E, n):
+    assert _form("moe_ops_product_form", gate_up, rows, E, n) == want
