@@ -138,11 +138,13 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
                 store_row<true>(o, (v4u*)(a.residual_out + at) + v);      // not read soon
             }
         }
+        if (up != 1.0f)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                s[u][c] *= up;
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            s[u][2 * c] *= up;
-            s[u][2 * c + 1] *= up;
             s[u][2 * c] *= r * bf16_lo(wv[c]);
             s[u][2 * c + 1] *= r * bf16_hi(wv[c]);
             top = fmaxf(top, fmaxf(fabsf(s[u][2 * c]), fabsf(s[u][2 * c + 1])));
