@@ -145,8 +145,8 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_kernel(const NormArgs a, int
         float top = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            s[u][2 * c] *= r * bf16_lo(wv[c]);
-            s[u][2 * c + 1] *= r * bf16_hi(wv[c]);
+            s[u][2 * c] = s[u][2 * c] * r * bf16_lo(wv[c]);        // |s r| is sqrt(hidden) at most
+            s[u][2 * c + 1] = s[u][2 * c + 1] * r * bf16_hi(wv[c]);
             top = fmaxf(top, fmaxf(fabsf(s[u][2 * c]), fabsf(s[u][2 * c + 1])));
         }
         if (mine && a.y) {

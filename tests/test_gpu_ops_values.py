@@ -64,6 +64,22 @@ def test_norm_small_rows(rows, hidden, eps):
             assert np.all(np.abs(got - ref[live]) <= tol)
 
 
+@pytest.mark.parametrize("size,scale", [(2.0 ** -60, 2.0 ** 90), (2.0 ** -130, 2.0 ** 70), (2.0 ** 40, 2.0 ** -110)])
+def test_norm_far_weights(size, scale):
+    """Rows and weights at opposite ends: 1/rms times the weight leaves fp32's
+    range, the result does not."""
+    say(f"[gpu] norm far weights {size} {scale}")
+    for hidden in (128, 2048):
+        g = rng(4, hidden)
+        x, w = R.bf16(size * g.standard_normal((7, hidden))).to(DEV), R.bf16(scale * g.standard_normal(hidden)).to(DEV)
+        y = torch.empty_like(x)
+        mep.moe_add_rmsnorm(7, hidden, x, None, w, 0.0, None, y, None, None)
+        torch.cuda.synchronize()
+        s = R.f64(x)
+        ref = s / np.sqrt((s * s).mean(-1, keepdims=True)) * R.f64(w)
+        assert np.all(np.abs(R.f64(y) - ref) <= (R.BF16_HALF + 2.0 ** -17) * np.abs(ref) + 2.0 ** -133)
+
+
 def test_norm_zero_rows():
     """A row of zeros is zero with any eps above 0; with eps 0 it is 0/0, NaN,
     and so are its codes; its neighbours are as ever."""
