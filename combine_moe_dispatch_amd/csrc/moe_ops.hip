@@ -144,9 +144,12 @@ int moe_expert_gate_up(int32_t rows, int32_t num_experts, int32_t f, int32_t k, 
 }
 
 // These two are not part of the public ABI: which kernels a call takes (n: weight
-// rows per expert, 2f for gate_up), so that tests can say what they check.
+// rows per expert, 2f for gate_up), so that tests can say what they check; ""
+// for sizes that no call takes.
 const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_experts, int32_t n)
 {
+    if (rows < 1 || num_experts < 1 || num_experts > moe::MAX_EXPERTS || n < 8 || n > 2 * MAX_WIDTH)
+        return "";
     moe::ops::ExpertProduct p{};
     p.rows = rows;
     p.E = num_experts;
@@ -156,6 +159,9 @@ const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_expe
 
 const char* moe_ops_few_token_form(int32_t num_tokens, int32_t num_experts, int32_t top_k, int32_t hidden, int32_t f)
 {
+    if (num_tokens < 1 || num_tokens > MOE_FEW_TOKENS_MAX || num_experts < 1 || num_experts > moe::MAX_EXPERTS ||
+        top_k < 1 || top_k > moe::MAX_TOPK || !width128(hidden) || !width128(f))
+        return "";
     moe::ops::FewTokens p{};
     p.T = num_tokens;
     p.E = num_experts;

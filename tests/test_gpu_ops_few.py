@@ -48,3 +48,35 @@ def test_few_forms(want, T, E, K, H, F):
     ref, noise = few_ref(x[live], idx[live], w[live], *wts)
     check_few(out[live], ref, noise)
     assert T <= 2 or bool((out[-2:] == 0).all())
+
+
+@pytest.mark.parametrize("want,T,E,K,H,F", [("direct", 9, 8, 2, 384, 256), ("direct split", 9, 32, 4, 256, 4096),
+                                            ("coded", 11, 8, 2, 256, 128), ("coded split", 33, 8, 3, 256, 1024)])
+def test_few_forms_at_once(want, T, E, K, H, F):
+    """Each form captured twice, replayed on two streams at once between eager calls."""
+    say(f"[gpu] few at once {want}")
+    assert _form(T, E, K, H, F).decode() == want
+    x, *rest = few_inputs(np.random.default_rng([29, T]), T, E, K, H, F)
+    eager = run_few(x, *rest)
+    idx, w, *wts = (torch.from_numpy(a).to("cuda") for a in rest)
+    nbytes = mep.moe_few_token_workspace(T, K, H, F)
+    outs = [torch.empty_like(x) for _ in range(2)]
+    spaces = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    graphs = []
+    torch.cuda.synchronize()
+    for out, space in zip(outs, spaces):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mep.moe_few_token_layer(T, E, K, H, F, x, idx, w, *wts, out, space)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for t in outs + spaces:
+            t.view(torch.uint8).fill_(0xFF)
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, eager) for out in outs)
+        assert torch.equal(run_few(x, *rest), eager)

@@ -188,6 +188,23 @@ def test_gate_up_forms(want, counts, f, k):
     check_gate_up(want, len(counts), counts, f, k)
 
 
+def many(E, *some):
+    return (list(some) * E)[:E]
+
+
+@pytest.mark.parametrize("E", [257, 600, 1024])
+@pytest.mark.parametrize("want,counts,n,f", [
+    ("32", (0, 3, 16, 17, 0, 33, 1, 20), 264, 256), ("64", (0, 1, 32, 33, 48, 49, 64, 65), 520, 128),
+    ("128", (64, 65, 96, 97, 0, 128, 30, 129), 520, 128), ("256", (0, 64, 193, 65, 128, 129, 256, 257), 520, None)])
+def test_many_experts(E, want, counts, n, f):
+    """More experts than a lane finds its tile with four of (257 and more: up to sixteen)."""
+    say(f"[gpu] products of {E} experts, form {want}")
+    counts = many(E, *counts)
+    check_matmul(want, E, counts, n, 384)
+    if f:
+        check_gate_up(want, E, counts, f, 384)
+
+
 @pytest.mark.parametrize("want,counts,n", [
     ("narrow", [5], 264), ("32 deep", [64], 5824), ("32", [15] * 10, 4864), ("64", [500], 4352),
     ("128", [1024], 7680), ("256", [2000], 6400)])

@@ -285,3 +285,56 @@ def test_matmul_bound(kind, rows, n):
     if rows > some:
         last = rows // some * some - some
         assert np.all(np.abs(got[last: last + some, :64] - ref) <= tol)
+
+
+# --- the stream that is named -------------------------------------------------------------------------
+
+def test_named_stream():
+    """Every operator runs on the stream it is given, behind what that stream
+    does: inputs are written there late, by a copy behind long work."""
+    say("[gpu] named stream")
+    E, K, H, F, rows = 8, 2, 256, 128, 16
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    f8 = lambda *s: (20 * rand(*s)).to(torch.float8_e4m3fn)  # noqa: E731
+    late = {"x": rand(rows, H).to(torch.bfloat16), "z": rand(rows, E), "q": f8(rows, H)}
+    nw, xs, off = rand(H).to(torch.bfloat16), torch.ones((rows, H // 128), device=DEV), torch.tensor(
+        [2 * e for e in range(E + 1)], dtype=torch.int32, device=DEV)
+    w13, s13 = f8(E, 2 * F, H), torch.full((E, 2 * F // 128, H // 128), 2.0 ** -12, device=DEV)
+    w2, s2 = f8(E, H, F), torch.full((E, H // 128, F // 128), 2.0 ** -12, device=DEV)
+    idx0 = torch.arange(rows * K, device=DEV, dtype=torch.int32).remainder(E).view(rows, K).contiguous()
+    space = torch.empty(mep.moe_few_token_workspace(rows, K, H, F), dtype=torch.uint8, device=DEV)
+    big = torch.empty(1 << 28, dtype=torch.float32, device=DEV)
+
+    def run(ins, outs, stream):
+        x, z, q = ins["x"], ins["z"], ins["q"]
+        y, idx, w, h, hs, p, o = outs
+        mep.moe_add_rmsnorm(rows, H, x, None, nw, 1e-6, None, y, None, None, stream=stream)
+        mep.moe_topk_route(rows, E, K, z, mep.MOE_FP32, True, idx, w, stream=stream)
+        mep.moe_expert_gate_up(rows, E, F, H, q, xs, off, w13, s13, h, hs, stream=stream)
+        mep.moe_expert_matmul(rows, E, 2 * F, H, q, xs, off, w13, s13, p, stream=stream)
+        mep.moe_few_token_layer(rows, E, K, H, F, x, idx0, w, w13, s13, w2, s2, o, space, stream=stream)
+
+    def outputs():
+        e = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device=DEV)  # noqa: E731
+        b = torch.bfloat16
+        return (e(rows, H, dt=b), e(rows, K, dt=torch.int32), e(rows, K), e(rows, F, dt=torch.uint8),
+                e(rows, F // 128), e(rows, 2 * F, dt=b), e(rows, H, dt=b))
+
+    want = outputs()
+    run(late, want, None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        ins, got = {k: torch.zeros_like(v) for k, v in late.items()}, outputs()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big.fill_(1.0)
+            for k, v in late.items():
+                ins[k].copy_(v)
+        run(ins, got, handle)                          # the current stream is another one
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((want[4] > 0).any()) and bool((want[6] != 0).any())

@@ -140,3 +140,11 @@ def test_few_token_forms(want, T, E, K, H, F):
     ("128", 1, 32768, 256, 4096), ("64", 1, 2000, 2, 1536)])
 def test_product_forms(want, gate_up, rows, E, n):
     assert _form("moe_ops_product_form", gate_up, rows, E, n) == want
+
+
+def test_forms_of_no_call():
+    for sizes in ((0, 0, 1, 256), (0, 4, 0, 256), (1, 4, 1025, 256), (0, 4, 1, 0), (0, -1, 1, 256)):
+        assert _form("moe_ops_product_form", *sizes) == ""
+    for sizes in ((0, 8, 2, 256, 256), (65, 8, 2, 256, 256), (4, 0, 2, 256, 256), (4, 8, 0, 256, 256),
+                  (4, 8, 2, 0, 256), (4, 8, 2, 256, 64)):
+        assert _form("moe_ops_few_token_form", *sizes) == ""
