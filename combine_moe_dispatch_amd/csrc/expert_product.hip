@@ -376,7 +376,7 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
     };
     auto read_scales = [&](int kb) {
         gs = wsc_mine[kb];
-        us = GATE_UP ? wsc[ws_row + kb] : 0.0f;
+        us = GATE_UP ? 0.25f * wsc[ws_row + kb] : 0.0f;       // up is summed as up/4: silu4 below
         const uint8_t* sc = sc_lds + (kb / C::SC_STEPS & 1) * C::SC_BYTES + (kb % C::SC_STEPS) * 32;
 #pragma unroll
         for (int i = 0; i < C::MT; ++i) {
@@ -625,7 +625,7 @@ __device__ __forceinline__ void product_tile(const ExpertProduct& p, const Place
 #pragma unroll
             for (int c = 0; c < C::OUTS; ++c) {
                 const float g = acc[j][i][c], u = acc[(j + HALF) % C::NT][i][c];
-                const float h = silu(g) * u;
+                const float h = silu4(g) * u;
                 acc[j][i][c] = h;
                 top = fmaxf(top, fabsf(h));
             }

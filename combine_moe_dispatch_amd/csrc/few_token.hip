@@ -402,7 +402,7 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 4) void few_gate_up_kernel(const 
                 a += part[q][0][col][f];
                 b += part[q][1][col][f];
             }
-            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = silu(a) * b;
+            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = silu4(a) * (0.25f * b);
         }
         __syncthreads();
     }
@@ -684,7 +684,7 @@ __global__ __launch_bounds__(GATE_WAVES* WAVE, 3) void coded_gate_up_kernel(cons
                 a += part[q][0][col][f];
                 b += part[q][1][col][f];
             }
-            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = silu(a) * b;
+            hbuf[(int64_t)cols[c0 + col] * p.F + f0 + f] = silu4(a) * (0.25f * b);
         }
         __syncthreads();
     }

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(256) void topk_route_kernel(int64_t tokens, int E, 
         for (int i = 0; i < V; ++i)
             if (i * G + l == be)
                 gone[i] = true;
-        const float v = p(bz, exp_of);
+        const float v = p(bz, [](float d) { return exp_of(d); });
         // lane k % G keeps pick k and writes it when it must
         if (k % G == l) {
             best_sum += v;

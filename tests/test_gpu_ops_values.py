@@ -190,6 +190,32 @@ def test_gate_up_scales_of_large_gates(rows):
     assert np.all(off_by[normal] <= 9), (g[normal], off_by[normal])
 
 
+@pytest.mark.parametrize("rows", [1, 200])
+def test_gate_up_far_gates(rows):
+    """Gates to -88.5, where exp(-gate) nears fp32's largest number and its
+    reciprocal is below the normal ones: silu is still an ordinary number, and
+    counts where up is large.  Roundings as above, and one of h = silu * up."""
+    say(f"[gpu] gate_up far gates rows={rows}")
+    gates = np.float32([-20, -60, -80, -86.5, -87, -87.25, -87.5, -88, -88.25, -88.5])
+    f, k = 128 * len(gates), 128
+    x, xs = one_hot_rows(rows, k)
+    w = torch.zeros((1, 2 * f, k), dtype=torch.uint8, device=DEV)
+    w[:, :, 0] = 0x38
+    ws = torch.full((1, 2 * len(gates), 1), 2.0 ** 60, device=DEV)
+    ws[0, : len(gates), 0] = torch.from_numpy(gates).to(DEV)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    h = torch.empty((rows, f), dtype=torch.uint8, device=DEV)
+    hs = torch.empty((rows, f // 128), device=DEV)
+    mep.moe_expert_gate_up(rows, 1, f, k, x, xs, off, w, ws, h, hs)
+    torch.cuda.synchronize()
+    v = gates.astype(np.float64)
+    want = np.abs(v / (1 + np.exp(-v))) * 2.0 ** 60 / 448
+    got = R.f64(hs)
+    assert np.all(got == got[:1])
+    # silu below the normal numbers is rounded at 2^-149: nothing here is that small
+    assert np.all(np.abs(got[0] - want) <= 10 * 2.0 ** -24 * want), got[0] / want - 1
+
+
 def test_silu_alike():
     """gate_up and the few-token layer form the same h: with one expert, one
     token and one block of f they give the same bits through the same down product."""
