@@ -446,6 +446,8 @@ int moe_topk_route(int32_t tokens, int32_t num_experts, int32_t top_k, const voi
  * large as the sum of these largest products that is below the rounding to
  * bf16; where they cancel it is not, and can be the larger part of what is left.
  * (moe_expert_gate_up and moe_few_token_layer sum all products in fp32.)
+ * In all three the row's and the weights' scale are multiplied first, in fp32:
+ * below 2^-126 that product loses bits.
  * n a multiple of 8, k of 128, both <= 65536; num_experts <= 1024. */
 int moe_expert_matmul(int32_t rows, int32_t num_experts, int32_t n, int32_t k, const void* x,
                       const float* x_scale, const int32_t* expert_offsets, const void* w,
