@@ -39,6 +39,12 @@ MOE_FP32 = 2                # moe_topk_route's logits
 
 MOE_FEW_TOKENS_MAX = 64
 
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_SILU = 3
+MOE_ACT_SWIGLU = 4
+
 MOE_TRANSPORT_STAGED = 0
 MOE_TRANSPORT_DIRECT = 1
 
@@ -119,6 +125,20 @@ def _load():
         "moe_few_token_workspace": ([I32, I32, I32, I32], ctypes.c_size_t),
         "moe_few_token_layer": ([I32, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P,
                                  ctypes.c_size_t, P], I),
+        "moe_sort_workspace": ([I32, I32, I32], ctypes.c_size_t),
+        "moe_sort_plan": ([I32, I32, I32, P, P, P, P, P, ctypes.c_size_t, P], I),
+        "moe_sort_rows": ([I32, I32, I32, I32, I32, P, P, P, P, P, P], I),
+        "moe_unsort_rows": ([I32, I32, I32, I32, I32, P, P, P, P, P], I),
+        "moe_unsort_rows_grad": ([I32, I32, I32, I32, I32, P, P, P, P, P, P, P], I),
+        "moe_topk_route_grad": ([I32, I32, I32, P, I32, I32, P, P, P, I32, P], I),
+        "moe_expert_linear_workspace": ([I32, I32, I32, I32], ctypes.c_size_t),
+        "moe_expert_linear": ([I32, I32, I32, I32, P, P, P, P, I32, P, P, P, I32, P,
+                               ctypes.c_size_t, P], I),
+        "moe_activation_grad": ([I32, I32, I32, I32, P, P, P, P, P], I),
+        "moe_expert_linear_grad_input": ([I32, I32, I32, I32, P, P, P, I32, P, P, P, I32, P,
+                                          ctypes.c_size_t, P], I),
+        "moe_expert_linear_grad_weight": ([I32, I32, I32, I32, P, P, P, P, I32, P, P,
+                                           ctypes.c_size_t, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -449,3 +469,158 @@ def moe_few_token_layer(num_tokens: int, num_experts: int, top_k: int, hidden: i
         _op_arg(out, c, "out", T * H, 2, _BF16, dev),
         _op_arg(workspace, c, "workspace", workspace_bytes, 1, _U8, dev), workspace_bytes,
         _op_stream(stream, dev)), c)
+
+
+# An expert layer on one card, forward and backward.
+
+def _kind(dtype: int):
+    """Tensor types and width of a MOE_* dtype; of no other is a tensor's."""
+    return {MOE_BF16: (_BF16, 2), MOE_FP32: (_F32, 4), MOE_FP8_E4M3: (_E4M3, 1)}.get(dtype, ((), 1))
+
+
+def _space(workspace, workspace_bytes, call: str, dev: int):
+    """(address, bytes) of a workspace; bytes may be left out where it is a tensor."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() if hasattr(workspace, "numel") else 0
+    p = _op_arg(workspace, call, "workspace", workspace_bytes, 1, _U8, dev)
+    return (p or None), workspace_bytes
+
+
+def moe_sort_workspace(tokens: int, num_experts: int, top_k: int) -> int:
+    return _lib.moe_sort_workspace(tokens, num_experts, top_k)
+
+
+def moe_sort_plan(tokens: int, num_experts: int, top_k: int, topk_idx, expert_offsets, slot, source,
+                  workspace=None, workspace_bytes: int = None, stream=None) -> None:
+    """workspace_bytes may be left out where workspace is a tensor."""
+    c = "moe_sort_plan"
+    dev, n = _op_device(), tokens * top_k
+    ws, size = _space(workspace, workspace_bytes, c, dev)
+    _check(_lib.moe_sort_plan(
+        tokens, num_experts, top_k, _op_arg(topk_idx, c, "topk_idx", n, 4, _I32, dev),
+        _op_arg(expert_offsets, c, "expert_offsets", num_experts + 1, 4, _I32, dev),
+        _op_arg(slot, c, "slot", n, 4, _I32, dev), _op_arg(source, c, "source", n, 4, _I32, dev),
+        ws, size, _op_stream(stream, dev)), c)
+
+
+def moe_sort_rows(tokens: int, top_k: int, rows: int, hidden: int, dtype: int, x, x_scale, slot,
+                  sorted, sorted_scale, stream=None) -> None:
+    c = "moe_sort_rows"
+    dev, nb = _op_device(), hidden // 128
+    kind, width = _kind(dtype)
+    _check(_lib.moe_sort_rows(
+        tokens, top_k, rows, hidden, dtype, _op_arg(x, c, "x", tokens * hidden, width, kind, dev),
+        _op_arg(x_scale, c, "x_scale", tokens * nb, 4, _F32, dev),
+        _op_arg(slot, c, "slot", tokens * top_k, 4, _I32, dev),
+        _op_arg(sorted, c, "sorted", rows * hidden, width, kind, dev),
+        _op_arg(sorted_scale, c, "sorted_scale", rows * nb, 4, _F32, dev), _op_stream(stream, dev)), c)
+
+
+def moe_unsort_rows(tokens: int, top_k: int, rows: int, hidden: int, dtype: int, y, slot,
+                    topk_weights, out, stream=None) -> None:
+    c = "moe_unsort_rows"
+    dev, n = _op_device(), tokens * top_k
+    kind, width = _kind(dtype)
+    _check(_lib.moe_unsort_rows(
+        tokens, top_k, rows, hidden, dtype, _op_arg(y, c, "y", rows * hidden, width, kind, dev),
+        _op_arg(slot, c, "slot", n, 4, _I32, dev),
+        _op_arg(topk_weights, c, "topk_weights", n, 4, _F32, dev),
+        _op_arg(out, c, "out", tokens * hidden, width, kind, dev), _op_stream(stream, dev)), c)
+
+
+def moe_unsort_rows_grad(tokens: int, top_k: int, rows: int, hidden: int, dtype: int, dout, y, slot,
+                         topk_weights, dy, dweights, stream=None) -> None:
+    c = "moe_unsort_rows_grad"
+    dev, n = _op_device(), tokens * top_k
+    kind, width = _kind(dtype)
+    _check(_lib.moe_unsort_rows_grad(
+        tokens, top_k, rows, hidden, dtype,
+        _op_arg(dout, c, "dout", tokens * hidden, width, kind, dev),
+        _op_arg(y, c, "y", rows * hidden, width, kind, dev),
+        _op_arg(slot, c, "slot", n, 4, _I32, dev),
+        _op_arg(topk_weights, c, "topk_weights", n, 4, _F32, dev),
+        _op_arg(dy, c, "dy", rows * hidden, width, kind, dev),
+        _op_arg(dweights, c, "dweights", n, 4, _F32, dev), _op_stream(stream, dev)), c)
+
+
+def moe_topk_route_grad(tokens: int, num_experts: int, top_k: int, logits, logits_dtype: int,
+                        renormalise: bool, topk_idx, dweights, dlogits, dlogits_dtype: int,
+                        stream=None) -> None:
+    c = "moe_topk_route_grad"
+    dev, n, m = _op_device(), tokens * top_k, tokens * num_experts
+    (kind, width), (dkind, dwidth) = _kind(logits_dtype), _kind(dlogits_dtype)
+    _check(_lib.moe_topk_route_grad(
+        tokens, num_experts, top_k, _op_arg(logits, c, "logits", m, width, kind, dev), logits_dtype,
+        1 if renormalise else 0, _op_arg(topk_idx, c, "topk_idx", n, 4, _I32, dev),
+        _op_arg(dweights, c, "dweights", n, 4, _F32, dev),
+        _op_arg(dlogits, c, "dlogits", m, dwidth, dkind, dev), dlogits_dtype,
+        _op_stream(stream, dev)), c)
+
+
+def moe_expert_linear_workspace(rows: int, num_experts: int, n: int, k: int) -> int:
+    return _lib.moe_expert_linear_workspace(rows, num_experts, n, k)
+
+
+def moe_expert_linear(rows: int, num_experts: int, n: int, k: int, x, expert_offsets, w, bias,
+                      activation: int, residual, z, y, y_dtype: int, workspace=None,
+                      workspace_bytes: int = None, stream=None) -> None:
+    """workspace_bytes may be left out where workspace is a tensor."""
+    c = "moe_expert_linear"
+    dev, E = _op_device(), num_experts
+    m = n // 2 if activation == MOE_ACT_SWIGLU else n
+    kind, width = _kind(y_dtype)
+    ws, size = _space(workspace, workspace_bytes, c, dev)
+    _check(_lib.moe_expert_linear(
+        rows, E, n, k, _op_arg(x, c, "x", rows * k, 2, _BF16, dev),
+        _op_arg(expert_offsets, c, "expert_offsets", E + 1, 4, _I32, dev),
+        _op_arg(w, c, "w", E * n * k, 2, _BF16, dev), _op_arg(bias, c, "bias", E * n, 2, _BF16, dev),
+        activation, _op_arg(residual, c, "residual", rows * m, 2, _BF16, dev),
+        _op_arg(z, c, "z", rows * n, 2, _BF16, dev), _op_arg(y, c, "y", rows * m, width, kind, dev),
+        y_dtype, ws, size, _op_stream(stream, dev)), c)
+
+
+def moe_activation_grad(rows: int, num_experts: int, n: int, activation: int, expert_offsets, z, dy,
+                        dz, stream=None) -> None:
+    c = "moe_activation_grad"
+    dev = _op_device()
+    m = n // 2 if activation == MOE_ACT_SWIGLU else n
+    _check(_lib.moe_activation_grad(
+        rows, num_experts, n, activation,
+        _op_arg(expert_offsets, c, "expert_offsets", num_experts + 1, 4, _I32, dev),
+        _op_arg(z, c, "z", rows * n, 2, _BF16, dev), _op_arg(dy, c, "dy", rows * m, 2, _BF16, dev),
+        _op_arg(dz, c, "dz", rows * n, 2, _BF16, dev), _op_stream(stream, dev)), c)
+
+
+def moe_expert_linear_grad_input(rows: int, num_experts: int, n: int, k: int, dz, expert_offsets, w,
+                                 activation: int, z, residual, dx, dx_dtype: int, workspace=None,
+                                 workspace_bytes: int = None, stream=None) -> None:
+    """workspace_bytes may be left out where workspace is a tensor."""
+    c = "moe_expert_linear_grad_input"
+    dev, E = _op_device(), num_experts
+    m = 2 * k if activation == MOE_ACT_SWIGLU else k
+    kind, width = _kind(dx_dtype)
+    ws, size = _space(workspace, workspace_bytes, c, dev)
+    _check(_lib.moe_expert_linear_grad_input(
+        rows, E, n, k, _op_arg(dz, c, "dz", rows * n, 2, _BF16, dev),
+        _op_arg(expert_offsets, c, "expert_offsets", E + 1, 4, _I32, dev),
+        _op_arg(w, c, "w", E * n * k, 2, _BF16, dev), activation,
+        _op_arg(z, c, "z", rows * m, 2, _BF16, dev),
+        _op_arg(residual, c, "residual", rows * m, 2, _BF16, dev),
+        _op_arg(dx, c, "dx", rows * m, width, kind, dev), dx_dtype, ws, size,
+        _op_stream(stream, dev)), c)
+
+
+def moe_expert_linear_grad_weight(rows: int, num_experts: int, n: int, k: int, dz, x, expert_offsets,
+                                  dw, dw_dtype: int, dbias, workspace=None,
+                                  workspace_bytes: int = None, stream=None) -> None:
+    """workspace_bytes may be left out where workspace is a tensor."""
+    c = "moe_expert_linear_grad_weight"
+    dev, E = _op_device(), num_experts
+    kind, width = _kind(dw_dtype)
+    ws, size = _space(workspace, workspace_bytes, c, dev)
+    _check(_lib.moe_expert_linear_grad_weight(
+        rows, E, n, k, _op_arg(dz, c, "dz", rows * n, 2, _BF16, dev),
+        _op_arg(x, c, "x", rows * k, 2, _BF16, dev),
+        _op_arg(expert_offsets, c, "expert_offsets", E + 1, 4, _I32, dev),
+        _op_arg(dw, c, "dw", E * n * k, width, kind, dev), dw_dtype,
+        _op_arg(dbias, c, "dbias", E * n, 4, _F32, dev), ws, size, _op_stream(stream, dev)), c)

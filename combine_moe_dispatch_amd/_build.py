@@ -23,7 +23,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_ep.so")
 SOURCES = [os.path.join(CSRC, name) for name in (
     "moe_ep.hip", "moe_kernels.hip", "moe_ops.hip", "token_ops.hip", "expert_product.hip",
-    "few_token.hip")]
+    "few_token.hip", "sort_rows.hip", "route_grad.hip", "expert_linear.hip")]
 ARCH = "gfx950"
 
 

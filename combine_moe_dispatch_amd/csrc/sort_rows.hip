@@ -1,0 +1,490 @@
+// Tokens sorted by expert and back: the plan (a stable counting sort of the
+// (token, k) pairs by expert), the copy of the tokens' rows into that order,
+// the weighted sum of the experts' rows back to the tokens, and its gradient.
+#include <algorithm>
+
+#include "moe_kernels.h"
+#include "moe_ops.h"
+#include "ops_common.h"
+
+namespace moe {
+namespace ops {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The plan.  Pair p = t*K + k of expert e gets row
+//   slot[p] = (pairs of experts below e) + (pairs before p of expert e).
+// A workgroup has a contiguous range of pairs, each of its waves a contiguous
+// part of that, so the ranks need only counts in order: per wave in LDS, per
+// workgroup in the workspace (a launch before this one, none where one
+// workgroup has all pairs).  Inside 64 pairs the rank is the number of lower
+// lanes with the same expert, found bit by bit of its id.
+// ---------------------------------------------------------------------------
+constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_RANGE = 8192;            // pairs of a workgroup, at least
+constexpr int PLAN_GROUPS = 128;            // workgroups, at most
+
+struct Plan {
+    int64_t pairs;
+    int E, groups, bits;
+    int64_t range;            // pairs per workgroup, a multiple of its threads
+    const int32_t* idx;
+    int32_t* counts;          // [groups][E], null with one workgroup
+    int32_t* offsets;
+    int32_t* slot;
+    int32_t* source;
+};
+
+__global__ __launch_bounds__(PLAN_THREADS) void count_pairs_kernel(const Plan p)
+{
+    __shared__ int count[MAX_EXPERTS];
+    for (int e = threadIdx.x; e < p.E; e += PLAN_THREADS)
+        count[e] = 0;
+    __syncthreads();
+    const int64_t end = min(p.range * (blockIdx.x + 1), p.pairs);
+    for (int64_t i = p.range * blockIdx.x + threadIdx.x; i < end; i += PLAN_THREADS) {
+        const int e = p.idx[i];
+        if ((uint32_t)e < (uint32_t)p.E)
+            atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += PLAN_THREADS)
+        p.counts[(int64_t)blockIdx.x * p.E + e] = count[e];
+}
+
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void sort_plan_kernel(const Plan p)
+{
+    constexpr int WAVES = THREADS / WAVE;
+    extern __shared__ int hist[];                  // [WAVES][E], then all[E + 1]
+    int* const all = hist + WAVES * p.E;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    int* const mine = hist + wave * p.E;
+    for (int e = threadIdx.x; e < WAVES * p.E; e += THREADS)
+        hist[e] = 0;
+    __syncthreads();
+    const int64_t part = p.range / WAVES;          // a multiple of 64
+    const int64_t begin = p.range * blockIdx.x + part * wave;
+    const int64_t end = min(begin + part, p.pairs);
+    for (int64_t i = begin + lane; i < end; i += WAVE) {
+        const int e = p.idx[i];
+        if ((uint32_t)e < (uint32_t)p.E)
+            atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    // each wave's pairs start behind those of the waves and workgroups before it
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+        int before = 0, total = 0;
+        for (int g = 0; g < p.groups && p.counts; ++g) {
+            const int c = p.counts[(int64_t)g * p.E + e];
+            before += g < (int)blockIdx.x ? c : 0;
+            total += c;
+        }
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const int c = hist[w * p.E + e];
+            hist[w * p.E + e] = before;
+            before += c;
+        }
+        all[e] = p.counts ? total : before;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const int per = (p.E + WAVE - 1) / WAVE;
+        const int e0 = min(lane * per, p.E), e1 = min(e0 + per, p.E);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e)
+            sum += all[e];
+        const int upto = wave_scan(sum);
+        int at = upto - sum;
+        for (int e = e0; e < e1; ++e) {
+            const int c = all[e];
+            all[e] = at;
+            at += c;
+        }
+        if (lane == WAVE - 1)
+            all[p.E] = upto;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= p.E; e += THREADS)
+            p.offsets[e] = all[e];
+    for (int64_t i0 = begin; i0 < end; i0 += WAVE) {
+        const int64_t i = i0 + lane;
+        const int e = i < end ? p.idx[i] : -1;
+        const bool valid = (uint32_t)e < (uint32_t)p.E;
+        uint64_t same = __ballot(valid);
+        for (int b = 0; b < p.bits; ++b) {
+            const bool one = e >> b & 1;
+            const uint64_t m = __ballot(one);
+            same &= one ? m : ~m;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        int row = 0;
+        if (valid && rank == 0)
+            row = all[e] + atomicAdd(&mine[e], __popcll(same));
+        row = __shfl(row, valid ? __ffsll((unsigned long long)same) - 1 : lane, WAVE) + rank;
+        if (i < end)
+            p.slot[i] = valid ? row : -1;
+        if (valid && p.source)
+            p.source[row] = (int)i;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  A token's row is V vectors of 16 bytes; LANES lanes of a wave (all 64
+// of them, in chunks, where V >= 64) hold one vector each.
+// ---------------------------------------------------------------------------
+struct Rows {
+    int64_t tokens, rows;
+    int K, vecs, chunks;      // chunks of LANES vectors per token
+    int extra;                // 4-byte words per row of the scales
+    const void* x;
+    const float* xs;
+    const int32_t* slot;
+    const float* w;
+    void* out;
+    float* outs;
+    const void* dout;
+    void* dy;
+    float* dw;
+};
+
+// Task of these lanes: a chunk of a token.
+template <int LANES>
+__device__ inline int64_t task_of()
+{
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    int64_t t = block * (blockDim.x / LANES) + threadIdx.x / LANES;
+    if (LANES == WAVE)
+        t = (int64_t)__builtin_amdgcn_readfirstlane((int)(t >> 32)) << 32 |
+            (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
+    return t;
+}
+
+template <int LANES>
+__global__ __launch_bounds__(256) void sort_rows_kernel(const Rows r)
+{
+    const int64_t task = task_of<LANES>();
+    const int64_t t = task / r.chunks;
+    if (t >= r.tokens)
+        return;
+    const int v = (int)(task - t * r.chunks) * LANES + threadIdx.x % LANES;
+    const bool live = v < r.vecs;
+    const v4u x = ((const v4u*)r.x)[t * r.vecs + (live ? v : 0)];
+    const float s = v < r.extra ? r.xs[t * r.extra + v] : 0.0f;
+    for (int k = 0; k < r.K; ++k) {
+        const int64_t row = r.slot[t * r.K + k];
+        if ((uint64_t)row >= (uint64_t)r.rows)
+            continue;
+        if (live)
+            ((v4u*)r.out)[row * r.vecs + v] = x;
+        if (v < r.extra)
+            r.outs[row * r.extra + v] = s;
+    }
+}
+
+// The elements of a vector as fp32, and back, rounded once.
+template <bool F32>
+struct Vec {
+    static constexpr int N = F32 ? 4 : 8;
+    static __device__ inline void open(const v4u& u, float (&f)[N])
+    {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if constexpr (F32) {
+                f[c] = __uint_as_float(u[c]);
+            } else {
+                f[2 * c] = bf16_lo(u[c]);
+                f[2 * c + 1] = bf16_hi(u[c]);
+            }
+    }
+    static __device__ inline v4u close(const float (&f)[N])
+    {
+        v4u u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if constexpr (F32)
+                u[c] = __float_as_uint(f[c]);
+            else
+                u[c] = bf16_pack(f[2 * c], f[2 * c + 1]);
+        return u;
+    }
+};
+
+constexpr int AHEAD = 8;      // rows of a token in flight
+
+// out[t] = sum over k, ascending, of w[t][k] * y[slot[t][k]]: an fp32 chain of
+// multiply-adds from +0, as moe_combine_recv forms it, rounded once.
+template <int LANES, bool F32>
+__global__ __launch_bounds__(256) void unsort_rows_kernel(const Rows r)
+{
+    typedef Vec<F32> V;
+    const int64_t task = task_of<LANES>();
+    const int64_t t = task / r.chunks;
+    if (t >= r.tokens)
+        return;
+    const int v = (int)(task - t * r.chunks) * LANES + threadIdx.x % LANES;
+    if (v >= r.vecs)
+        return;
+    const v4u* y = (const v4u*)r.x + v;
+    float acc[V::N] = {};
+    for (int k0 = 0; k0 < r.K; k0 += AHEAD) {
+        v4u u[AHEAD];
+        float w[AHEAD];
+        bool has[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int64_t at = t * r.K + min(k0 + a, r.K - 1);
+            const int64_t row = r.slot[at];
+            has[a] = k0 + a < r.K && (uint64_t)row < (uint64_t)r.rows;
+            w[a] = r.w ? r.w[at] : 1.0f;
+            if (has[a])
+                u[a] = y[row * r.vecs];
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (has[a]) {
+                float f[V::N];
+                V::open(u[a], f);
+#pragma unroll
+                for (int c = 0; c < V::N; ++c)
+                    acc[c] = fmaf(w[a], f[c], acc[c]);
+            }
+    }
+    ((v4u*)r.out)[t * r.vecs + v] = V::close(acc);
+}
+
+// dy[slot[t][k]] = w[t][k] * dout[t];  dw[t][k] = dout[t] . y[slot[t][k]].
+// A token's row lies in the registers of `waves` waves (U vectors per lane)
+// while its K rows go by; a dot product is summed per lane, over the lanes,
+// then over the waves in their order.
+template <int LANES, int U, bool F32>
+__global__ __launch_bounds__(1024) void unsort_rows_grad_kernel(const Rows r, int waves)
+{
+    typedef Vec<F32> V;
+    __shared__ float part[MAX_TOPK][16];
+    const int lane = threadIdx.x % LANES;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int wave = LANES == WAVE ? __builtin_amdgcn_readfirstlane(threadIdx.x / LANES) : 0;
+    const int64_t t = LANES == WAVE ? block : block * (blockDim.x / LANES) + threadIdx.x / LANES;
+    if (t >= r.tokens)
+        return;
+    float d[U][V::N];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = (u * waves + wave) * LANES + lane;
+        v4u raw{0, 0, 0, 0};
+        if (v < r.vecs)
+            raw = ((const v4u*)r.dout)[t * r.vecs + v];
+        V::open(raw, d[u]);
+    }
+    for (int k = 0; k < r.K; ++k) {
+        const int64_t row = r.slot[t * r.K + k];
+        const bool has = (uint64_t)row < (uint64_t)r.rows;
+        const float w = r.w ? r.w[t * r.K + k] : 1.0f;
+        float dot = 0.0f;
+        if (has) {
+            v4u raw[U];
+            if (r.dw)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int v = (u * waves + wave) * LANES + lane;
+                    raw[u] = v4u{0, 0, 0, 0};
+                    if (v < r.vecs)
+                        raw[u] = ((const v4u*)r.x)[row * r.vecs + v];
+                }
+            if (r.dy)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int v = (u * waves + wave) * LANES + lane;
+                    float g[V::N];
+#pragma unroll
+                    for (int c = 0; c < V::N; ++c)
+                        g[c] = w * d[u][c];
+                    if (v < r.vecs)
+                        ((v4u*)r.dy)[row * r.vecs + v] = V::close(g);
+                }
+            if (r.dw)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[V::N];
+                    V::open(raw[u], f);
+#pragma unroll
+                    for (int c = 0; c < V::N; ++c)
+                        dot = fmaf(d[u][c], f[c], dot);
+                }
+        }
+        if (r.dw) {
+#pragma unroll
+            for (int s = LANES / 2; s; s >>= 1)
+                dot += __shfl_xor(dot, s, LANES);
+            if (LANES < WAVE || waves == 1) {
+                if (lane == 0)
+                    r.dw[t * r.K + k] = dot;
+            } else if (lane == 0) {
+                part[k][wave] = dot;
+            }
+        }
+    }
+    if (LANES == WAVE && waves > 1 && r.dw) {
+        __syncthreads();
+        if ((int)threadIdx.x < r.K) {
+            float sum = 0.0f;
+            for (int w = 0; w < waves; ++w)
+                sum += part[threadIdx.x][w];
+            r.dw[t * r.K + threadIdx.x] = sum;
+        }
+    }
+}
+
+dim3 grid_of(int64_t blocks)
+{
+    constexpr int64_t ROW = 1 << 20;              // a grid dimension times the threads stays below 2^32
+    return dim3((uint32_t)std::min(blocks, ROW), (uint32_t)((blocks + ROW - 1) / ROW));
+}
+
+int lanes_for(int vecs)
+{
+    int lanes = 1;
+    while (lanes < vecs && lanes < WAVE)
+        lanes *= 2;
+    return lanes;
+}
+
+// Calls f with the number of lanes per row as a constant.
+template <class F>
+void with_lanes(int vecs, F f)
+{
+    switch (lanes_for(vecs)) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 8: return f(std::integral_constant<int, 8>{});
+    case 16: return f(std::integral_constant<int, 16>{});
+    case 32: return f(std::integral_constant<int, 32>{});
+    default: return f(std::integral_constant<int, 64>{});
+    }
+}
+
+Rows rows_of(const SortRows& p, int elem_bytes)
+{
+    Rows r{};
+    r.tokens = p.tokens;
+    r.rows = p.rows;
+    r.K = p.K;
+    r.vecs = (int)((int64_t)p.hidden * elem_bytes / 16);
+    r.chunks = (r.vecs + WAVE - 1) / WAVE;
+    r.x = p.x;
+    r.xs = p.xs;
+    r.slot = p.slot;
+    r.w = p.w;
+    r.out = p.out;
+    r.outs = p.outs;
+    r.dout = p.dout;
+    r.dy = p.dy;
+    r.dw = p.dw;
+    return r;
+}
+
+int plan_groups(int64_t pairs)
+{
+    return (int)std::min<int64_t>((pairs + PLAN_RANGE - 1) / PLAN_RANGE, PLAN_GROUPS);
+}
+
+}  // namespace
+
+size_t sort_workspace(int64_t pairs, int E)
+{
+    const int groups = plan_groups(pairs);
+    return groups > 1 ? (size_t)groups * E * sizeof(int32_t) : 0;
+}
+
+hipError_t launch_sort_plan(int64_t pairs, int E, const int32_t* idx, int32_t* offsets, int32_t* slot,
+                            int32_t* source, void* workspace, hipStream_t stream)
+{
+    Plan p{};
+    p.pairs = pairs;
+    p.E = E;
+    p.groups = std::max(plan_groups(pairs), 1);
+    while ((1 << p.bits) < E)
+        ++p.bits;
+    p.idx = idx;
+    p.offsets = offsets;
+    p.slot = slot;
+    p.source = source;
+    const int64_t share = (pairs + p.groups - 1) / p.groups;
+    p.range = std::max<int64_t>((share + PLAN_THREADS - 1) / PLAN_THREADS, 1) * PLAN_THREADS;
+    if (p.groups > 1) {
+        p.counts = (int32_t*)workspace;
+        count_pairs_kernel<<<dim3(p.groups), dim3(PLAN_THREADS), 0, stream>>>(p);
+    }
+    auto launch = [&](auto threads) {                  // at most 36 KB of counts
+        const int bytes = (threads / WAVE * E + E + 1) * 4;
+        sort_plan_kernel<threads><<<dim3(p.groups), dim3(threads), bytes, stream>>>(p);
+    };
+    if (E <= MAX_EXPERTS / 2)
+        launch(std::integral_constant<int, PLAN_THREADS>{});
+    else
+        launch(std::integral_constant<int, PLAN_THREADS / 2>{});
+    return hipGetLastError();
+}
+
+hipError_t launch_sort_rows(const SortRows& p, int elem_bytes, hipStream_t stream)
+{
+    Rows r = rows_of(p, elem_bytes);
+    r.extra = p.xs ? p.hidden / SCALE_BLOCK : 0;
+    with_lanes(r.vecs, [&](auto lanes) {
+        const int64_t blocks = (r.tokens * r.chunks + 256 / lanes - 1) / (256 / lanes);
+        sort_rows_kernel<lanes><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_unsort_rows(const SortRows& p, bool f32, hipStream_t stream)
+{
+    const Rows r = rows_of(p, f32 ? 4 : 2);
+    with_lanes(r.vecs, [&](auto lanes) {
+        const int64_t blocks = (r.tokens * r.chunks + 256 / lanes - 1) / (256 / lanes);
+        if (f32)
+            unsort_rows_kernel<lanes, true><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+        else
+            unsort_rows_kernel<lanes, false><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+    });
+    return hipGetLastError();
+}
+
+template <int LANES, int U>
+static void launch_grad(const Rows& r, bool f32, int waves, hipStream_t stream)
+{
+    const int threads = LANES == WAVE ? waves * WAVE : 256;
+    const int64_t per = LANES == WAVE ? 1 : 256 / LANES;
+    const dim3 grid = grid_of((r.tokens + per - 1) / per);
+    if (f32)
+        unsort_rows_grad_kernel<LANES, U, true><<<grid, dim3(threads), 0, stream>>>(r, waves);
+    else
+        unsort_rows_grad_kernel<LANES, U, false><<<grid, dim3(threads), 0, stream>>>(r, waves);
+}
+
+hipError_t launch_unsort_rows_grad(const SortRows& p, bool f32, hipStream_t stream)
+{
+    const Rows r = rows_of(p, f32 ? 4 : 2);
+    with_lanes(r.vecs, [&](auto lanes) {
+        if constexpr (lanes < WAVE) {
+            launch_grad<lanes, 1>(r, f32, 1, stream);
+        } else {
+            const int units = (r.vecs + WAVE - 1) / WAVE;      // wave-wide vectors of a row: up to 256
+            if (units <= 1)
+                launch_grad<WAVE, 1>(r, f32, 1, stream);
+            else if (units <= 32)
+                launch_grad<WAVE, 2>(r, f32, (units + 1) / 2, stream);
+            else
+                launch_grad<WAVE, 16>(r, f32, (units + 15) / 16, stream);
+        }
+    });
+    return hipGetLastError();
+}
+
+}  // namespace ops
+}  // namespace moe

@@ -488,6 +488,165 @@ int moe_few_token_layer(int32_t num_tokens, int32_t num_experts, int32_t top_k, 
                         const void* w2, const float* w2_scale, void* out, void* workspace,
                         size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * An expert layer on one card, forward and backward.
+ *
+ * Where one card holds all experts of its tokens nothing has to be
+ * dispatched: the tokens' rows are sorted by expert, go through bf16 products
+ * and come back weighted.  These operators are that, with the gradients:
+ * norm, moe_expert_linear (the router's logits), moe_topk_route,
+ * moe_sort_plan, moe_sort_rows, moe_expert_linear twice, moe_unsort_rows; and
+ * backwards moe_unsort_rows_grad, moe_expert_linear_grad_input and
+ * _grad_weight, moe_unsort_rows (the gradient of the sorted rows),
+ * moe_topk_route_grad.  moe_sort_rows also carries e4m3 rows, which
+ * moe_expert_gate_up and moe_expert_matmul read.  Conventions as above.
+ * ------------------------------------------------------------------------- */
+
+/* Where each (token, k) pair's row lies when pairs are sorted by expert.
+ *   topk_idx        int32 [tokens][top_k]; an id outside [0, num_experts) names
+ *                   no expert (padding).  An expert may be named twice.
+ *   expert_offsets  int32 [num_experts+1]: expert e's rows are
+ *                   [expert_offsets[e], expert_offsets[e+1]), ascending from 0
+ *   slot            int32 [tokens][top_k]: the pair's row, -1 where it names no
+ *                   expert; an expert's pairs in the order t*top_k + k
+ *   source          int32 [tokens*top_k] or NULL: t*top_k + k of each row;
+ *                   entries behind the last expert's rows stay as they are
+ *   workspace       device, moe_sort_workspace(...) bytes (NULL if 0), this
+ *                   call's own until its work has run; holds nothing between calls
+ * tokens*top_k < 2^31, num_experts <= 1024, top_k <= 64.  With zero tokens the
+ * offsets are written (zeros) and nothing else. */
+size_t moe_sort_workspace(int32_t tokens, int32_t num_experts, int32_t top_k);
+int moe_sort_plan(int32_t tokens, int32_t num_experts, int32_t top_k, const int32_t* topk_idx,
+                  int32_t* expert_offsets, int32_t* slot, int32_t* source, void* workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/* Tokens' rows copied to their slots: sorted[slot[t][k]] = x[t].
+ *   rows            room of sorted; a slot outside [0, rows) takes nothing, and
+ *                   rows that no slot names stay as they are
+ *   dtype           MOE_BF16, MOE_FP32 or MOE_FP8_E4M3
+ *   x, x_scale      [tokens][hidden]; fp32 [tokens][hidden/128] with e4m3, else NULL
+ *   sorted, sorted_scale   the same for [rows]
+ * hidden a multiple of 8 (of 128 with e4m3), <= 65536.  Slots are distinct, as
+ * moe_sort_plan makes them.  The gradient of this call is moe_unsort_rows
+ * without weights. */
+int moe_sort_rows(int32_t tokens, int32_t top_k, int32_t rows, int32_t hidden, int32_t dtype,
+                  const void* x, const float* x_scale, const int32_t* slot, void* sorted,
+                  float* sorted_scale, hipStream_t stream);
+
+/* The experts' rows back at their tokens, weighted and added up:
+ *   out[t] = sum over k of topk_weights[t][k] * y[slot[t][k]]
+ * as moe_combine_recv forms it: from +0, k ascending, one fp32 multiply-add
+ * each, rounded once.
+ *   dtype           MOE_BF16 or MOE_FP32, of y and out
+ *   y               [rows][hidden]; a slot outside [0, rows) adds nothing, a
+ *                   token without any gets zeros
+ *   topk_weights    fp32 [tokens][top_k], or NULL: all 1
+ *   out             [tokens][hidden]
+ * hidden a multiple of 8, <= 65536. */
+int moe_unsort_rows(int32_t tokens, int32_t top_k, int32_t rows, int32_t hidden, int32_t dtype,
+                    const void* y, const int32_t* slot, const float* topk_weights, void* out,
+                    hipStream_t stream);
+
+/* Gradient of moe_unsort_rows:
+ *   dy[slot[t][k]] = topk_weights[t][k] * dout[t]    (one fp32 product, rounded once)
+ *   dweights[t][k] = dout[t] . y[slot[t][k]]         (summed in fp32; 0 without a slot)
+ * dy and dweights may be NULL, not both; y is needed for dweights only.  Rows
+ * that no slot names stay as they are. */
+int moe_unsort_rows_grad(int32_t tokens, int32_t top_k, int32_t rows, int32_t hidden, int32_t dtype,
+                         const void* dout, const void* y, const int32_t* slot,
+                         const float* topk_weights, void* dy, float* dweights, hipStream_t stream);
+
+/* Gradient of moe_topk_route's weights to the logits.
+ *   logits, logits_dtype, renormalise, topk_idx   as that call had and gave them
+ *   dweights        fp32 [tokens][top_k]
+ *   dlogits         [tokens][num_experts], MOE_BF16 or MOE_FP32 (dlogits_dtype)
+ * With p the softmax over all experts, g_e the sum of dweights over the k with
+ * topk_idx = e: dlogits_e = p_e (g_e - sum over k of p dweights); with
+ * renormalise the same with the softmax over the chosen logits, and 0 for all
+ * others.  A weight of 0 (masked experts and tokens) passes no gradient,
+ * whatever its dweights; an id outside [0, num_experts) has none. */
+int moe_topk_route_grad(int32_t tokens, int32_t num_experts, int32_t top_k, const void* logits,
+                        int32_t logits_dtype, int32_t renormalise, const int32_t* topk_idx,
+                        const float* dweights, void* dlogits, int32_t dlogits_dtype,
+                        hipStream_t stream);
+
+/* What moe_expert_linear applies to its sums.  GELU is z Phi(z), Phi the normal
+ * distribution function; SILU z / (1 + exp(-z)); SWIGLU takes the first half of
+ * the columns as gate and the second as up: silu(gate) * up. */
+typedef enum moe_activation {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_GELU = 2,
+    MOE_ACT_SILU = 3,
+    MOE_ACT_SWIGLU = 4
+} moe_activation;
+
+/* The bf16 product with bias, activation and residual, rows grouped by expert:
+ *   z[r][j] = sum over i of x[r][i] * w[e][j][i] + bias[e][j],  e the row's expert
+ *   y[r][j] = act(z[r][j]) + residual[r][j]
+ *   x               bf16 [rows][k]
+ *   expert_offsets  int32 [num_experts+1] as for moe_expert_matmul, rows behind
+ *                   the last expert's neither read nor written; NULL with one
+ *                   expert: all rows are its rows (a shared expert, the
+ *                   router's logits, any other layer's product)
+ *   w, bias         bf16 [num_experts][n][k]; bf16 [num_experts][n] or NULL
+ *   residual        bf16 [rows][m] or NULL, m = n (n/2 with SWIGLU)
+ *   z               bf16 [rows][n] or NULL: the sums before the activation, which
+ *                   the gradient needs
+ *   y               [rows][m], MOE_BF16 or MOE_FP32 (y_dtype)
+ *   workspace       device, moe_expert_linear_workspace(...) bytes (NULL if 0),
+ *                   this call's own until its work has run; holds nothing
+ *                   between calls
+ * Sums are fp32; z and y are each rounded once from there (y's activation does
+ * not see z's rounding).  y may be residual itself (bf16).  n and k multiples of
+ * 8 (n of 16 with SWIGLU), <= 65536; num_experts <= 1024. */
+int moe_expert_linear(int32_t rows, int32_t num_experts, int32_t n, int32_t k, const void* x,
+                      const int32_t* expert_offsets, const void* w, const void* bias,
+                      int32_t activation, const void* residual, void* z, void* y, int32_t y_dtype,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace that serve moe_expert_linear and both gradients of these
+ * sizes; 0 if none is needed (or they are out of range). */
+size_t moe_expert_linear_workspace(int32_t rows, int32_t num_experts, int32_t n, int32_t k);
+
+/* Gradient of an activation: dz = dy * act'(z) (SWIGLU: of both halves).
+ *   z               bf16 [rows][n]
+ *   dy              bf16 [rows][m], m = n (n/2 with SWIGLU)
+ *   dz              bf16 [rows][n]; may be dy or z itself (with SWIGLU: z)
+ * expert_offsets as above (only the last is read); rows behind it are not
+ * touched.  relu'(0) = 0. */
+int moe_activation_grad(int32_t rows, int32_t num_experts, int32_t n, int32_t activation,
+                        const int32_t* expert_offsets, const void* z, const void* dy, void* dz,
+                        hipStream_t stream);
+
+/* Gradient of moe_expert_linear's sums to its input, through the activation
+ * that made that input:
+ *   dx[r][i] = act'(z[r][i]) * (sum over j of dz[r][j] * w[e][j][i]) + residual[r][i]
+ *   dz              bf16 [rows][n]
+ *   activation, z   of the layer whose output x was; z bf16 [rows][m], m = k (2k
+ *                   with SWIGLU: gate and up).  NULL with MOE_ACT_NONE: dx is then
+ *                   the input's gradient, else that of the layer's sums before it.
+ *   residual        bf16 [rows][m] or NULL: a gradient that comes another way
+ *   dx              [rows][m], MOE_BF16 or MOE_FP32 (dx_dtype); may be residual
+ *                   itself (bf16)
+ * Other arguments as above; k a multiple of 8. */
+int moe_expert_linear_grad_input(int32_t rows, int32_t num_experts, int32_t n, int32_t k,
+                                 const void* dz, const int32_t* expert_offsets, const void* w,
+                                 int32_t activation, const void* z, const void* residual, void* dx,
+                                 int32_t dx_dtype, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/* Gradient to the weights and the bias:
+ *   dw[e][j][i] = sum over the expert's rows of dz[r][j] * x[r][i]
+ *   dbias[e][j] = sum over the expert's rows of dz[r][j]
+ *   dw              [num_experts][n][k], MOE_BF16 or MOE_FP32 (dw_dtype)
+ *   dbias           fp32 [num_experts][n] or NULL
+ * Sums are fp32, in an order that is the same every time; an expert without
+ * rows gets zeros, with zero rows all do. */
+int moe_expert_linear_grad_weight(int32_t rows, int32_t num_experts, int32_t n, int32_t k,
+                                  const void* dz, const void* x, const int32_t* expert_offsets,
+                                  void* dw, int32_t dw_dtype, float* dbias, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
 /* Static description of a status code; never NULL. */
 const char* moe_strerror(int status);
 
