@@ -14,6 +14,7 @@
 // LDS read.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "expert_tiles.h"
 #include "moe_ep.h"
@@ -335,12 +336,12 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % C::WM, wn = wave / C::WM;
     const int steps = (int)((t1 - t0 + STEP - 1) / STEP);
-    auto issue = [&](int step) {
-        uint8_t* st = lds + step % C::S * C::STAGE;
+    auto issue_to = [&](int step, uint8_t* st) {
         const int64_t t = t0 + (int64_t)step * STEP;
         load_side<C, C::BN, C::V_ALL, C::V_LOADS, V_CONTIG, GATED>(vs, t, t1 - t, st, wave, lane);
         load_side<C, C::BM, C::U_ALL, C::U_LOADS, U_CONTIG, false>(us, t, t1 - t, st + C::V_BYTES, wave, lane);
     };
+    auto issue = [&](int step) { issue_to(step, lds + step * C::STAGE); };
     // LDS row of V's subtile j: gated tiles keep the gate's rows in their first half
     auto vrow = [&](int j) {
         if (GATED) {
@@ -369,38 +370,66 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
             sums[i] = zero;
     }
 #pragma unroll
-    for (int s = 0; s < C::S - 1; ++s)
+    for (int s = 0; s < C::S; ++s)
         if (s < steps)
             issue(s);
-    for (int step = 0; step < steps; ++step) {
-        if (step + C::S - 1 <= steps)
-            wait_loads_and_meet<(C::S - 2) * C::LOADS>();
-        else
-            wait_loads_and_meet<0>();
-        if (step + C::S - 1 < steps)
-            issue(step + C::S - 1);
-        const uint8_t* st = lds + step % C::S * C::STAGE;
+    // A stage is summed in two halves of 32.  Each half's operands are read
+    // while the half before it is multiplied; in the middle of a stage all its
+    // reads are done, its slot is free once every wave is there, and the next
+    // stage has arrived.
+    v8b vf[2][C::NT], uf[2][C::MT];
+    auto read = [&](const uint8_t* st, int h) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v8b vf[C::NT], uf[C::MT];
+        for (int j = 0; j < C::NT; ++j)
+            vf[h][j] = read_side<C::BN, V_CONTIG>(st, vrow(j), h, lane);
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            uf[h][i] = read_side<C::BM, U_CONTIG>(st + C::V_BYTES, wm * C::TM + i * 16, h, lane);
+    };
+    auto multiply = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
 #pragma unroll
             for (int j = 0; j < C::NT; ++j)
-                vf[j] = read_side<C::BN, V_CONTIG>(st, vrow(j), h, lane);
+                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[h][j], uf[h][i], acc[j][i], 0, 0, 0);
+        if constexpr (BIAS)
 #pragma unroll
             for (int i = 0; i < C::MT; ++i)
-                uf[i] = read_side<C::BM, U_CONTIG>(st + C::V_BYTES, wm * C::TM + i * 16, h, lane);
+                if (i / SUMS == wn)
+                    sums[i % SUMS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf[h][i], sums[i % SUMS], 0, 0, 0);
+        // a read beside every few products
+        constexpr int READS = C::NT * (V_CONTIG ? 1 : 2) + C::MT * (U_CONTIG ? 1 : 2);
+        constexpr int EACH = C::NT * C::MT / READS > 0 ? C::NT * C::MT / READS : 1;
 #pragma unroll
-            for (int j = 0; j < C::NT; ++j)
-#pragma unroll
-                for (int i = 0; i < C::MT; ++i)
-                    acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], uf[i], acc[j][i], 0, 0, 0);
-            if constexpr (BIAS)
-#pragma unroll
-                for (int i = 0; i < C::MT; ++i)
-                    if (i / SUMS == wn)
-                        sums[i % SUMS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf[i], sums[i % SUMS], 0, 0, 0);
+        for (int q = 0; q < READS; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, EACH, 0);
         }
+    };
+    if (steps > 0) {
+        if (steps >= C::S)
+            wait_loads_and_meet<(C::S - 1) * C::LOADS>();
+        else
+            wait_loads_and_meet<0>();
+        read(lds, 0);
     }
+    int slot = 0;
+    auto step_of = [&](int step, auto steady) {
+        uint8_t* st = lds + slot * C::STAGE;
+        read(st, 1);
+        multiply(0);
+        wait_loads_and_meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
+        if constexpr (decltype(steady)::value)
+            issue_to(step + C::S, st);
+        slot = slot + 1 == C::S ? 0 : slot + 1;
+        read(lds + slot * C::STAGE, 0);              // (past the last stage: stale, never used)
+        multiply(1);
+    };
+    int step = 0;
+    for (; step + C::S < steps; ++step)
+        step_of(step, std::true_type{});
+    for (; step < steps; ++step)
+        step_of(step, std::false_type{});
 
     // Lane (r, g) holds column r of a subtile and rows 4g .. 4g+3; lanes of two
     // subtiles trade so that each holds eight consecutive outputs.
@@ -667,9 +696,9 @@ int splits_of(int64_t groups, int64_t total)
     return (int)std::max<int64_t>(std::min<int64_t>({256 / groups, steps / 4, 32}), 1);
 }
 
-typedef Block<128, 256, 2, 4, 3> Rows128;
+typedef Block<256, 256, 2, 4, 2> Rows256;
 typedef Block<32, 256, 2, 4, 2> Rows32;
-typedef Block<128, 128, 2, 4, 3> Weights128;
+typedef Block<256, 256, 2, 4, 2> Weights256;
 
 struct Shape {
     bool low;                 // the lower tile
@@ -682,13 +711,13 @@ Shape rows_shape(Kind kind, bool gated, int64_t rows, int E, int n, int k)
     const int width = kind == Kind::FORWARD ? n : k;
     s.n_tiles = gated ? (width / 2 + 127) / 128 : (width + 255) / 256;
     s.low = rows / E <= 48;
-    s.splits = splits_of(workgroups(rows, E, s.low ? Rows32::BM : Rows128::BM, s.n_tiles), kind == Kind::FORWARD ? k : n);
+    s.splits = splits_of(workgroups(rows, E, s.low ? Rows32::BM : Rows256::BM, s.n_tiles), kind == Kind::FORWARD ? k : n);
     return s;
 }
 
 int weight_splits(int64_t rows, int E, int n, int k)
 {
-    return splits_of((int64_t)E * ((n + 127) / 128) * ((k + 127) / 128), rows / E);
+    return splits_of((int64_t)E * ((n + 255) / 256) * ((k + 255) / 256), rows / E);
 }
 
 template <Kind KIND, bool GATED, class C>
@@ -709,7 +738,7 @@ hipError_t launch_rows(const Linear& p, hipStream_t stream)
 {
     const Shape s = rows_shape(KIND, GATED, p.rows, p.E, p.n, p.k);
     const hipError_t e = s.low ? launch_rows<KIND, GATED, Rows32>(p, s, stream)
-                               : launch_rows<KIND, GATED, Rows128>(p, s, stream);
+                               : launch_rows<KIND, GATED, Rows256>(p, s, stream);
     if (e != hipSuccess || s.splits == 1)
         return e;
     const int width = KIND == Kind::FORWARD ? p.n : p.k;
@@ -746,7 +775,7 @@ hipError_t launch_linear_grad_input(const Linear& p, hipStream_t stream)
 
 hipError_t launch_linear_grad_weight(const Linear& p, hipStream_t stream)
 {
-    typedef Weights128 C;
+    typedef Weights256 C;
     const int m_tiles = (p.n + C::BM - 1) / C::BM, n_tiles = (p.k + C::BN - 1) / C::BN;
     const int splits = weight_splits(p.rows, p.E, p.n, p.k);
     static std::atomic<uint64_t> allowed{0};
