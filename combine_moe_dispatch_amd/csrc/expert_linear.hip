@@ -42,6 +42,8 @@ struct Block {
     static constexpr int MT = TM / 16, NT = TN / 16;
     static constexpr int V_BYTES = BN * STEP * 2, U_BYTES = BM * STEP * 2;
     static constexpr int STAGE = V_BYTES + U_BYTES;
+    static constexpr bool DEEP = BM == 256;                 // S does not count there
+    static constexpr int LDS = DEEP ? 3 * V_BYTES + 2 * U_BYTES : S * STAGE;
     // 1 KB loads of a stage, and how many of them each wave issues
     static constexpr int V_ALL = V_BYTES / 1024, U_ALL = U_BYTES / 1024;
     static constexpr int V_LOADS = V_ALL / WAVES, U_LOADS = (U_ALL + WAVES - 1) / WAVES;
@@ -49,6 +51,38 @@ struct Block {
     static_assert(V_ALL % WAVES == 0 && U_ALL % 2 == 0 && WAVES % 2 == 0, "a wave's parts share the swizzle");
     static_assert(NT % 2 == 0, "the epilogue pairs subtiles");
 };
+
+// 16 bytes per lane from memory to LDS, 1 KB from `lds` on: at a uniform base
+// and 32-bit offsets, or at 64-bit addresses.  The compiler does not see these
+// as memory accesses: told of them, it would wait for all of them ahead of
+// every transposing LDS read.  They are waited for by meet() alone, and stay
+// between the two that enclose them (volatile statements keep their order).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"      // m0, a reserved register, is named as overwritten
+__device__ inline void load_to_lds(const uint8_t* base, uint32_t offset, const uint8_t* lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
+                 "s"((uint32_t)(uintptr_t)(lvoid*)lds)
+                 : "m0");
+}
+__device__ inline void load_to_lds(const uint8_t* address, const uint8_t* lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(address),
+                 "s"((uint32_t)(uintptr_t)(lvoid*)lds)
+                 : "m0");
+}
+
+#pragma clang diagnostic pop
+
+// Everything this wave loaded but its last N loads has arrived in LDS, its own
+// LDS reads are done, and so it is with every wave of the workgroup.
+template <int N>
+__device__ inline void meet()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), in a form that the compiler counts
+    asm volatile("s_barrier" ::: "memory");
+}
 
 // What is loaded in place of indices behind the end of the sum.
 __device__ const uint4 zeros = {0, 0, 0, 0};
@@ -71,39 +105,43 @@ __device__ inline int turn(int t)
     return ((t & 3) | (t >> 3 & 1) << 2) << 1 & (PIECES - 1);
 }
 
-// Loads the operand's indices t0 .. t0+63 of the sum into LDS, `left` of them
-// before the sum's end.
-template <class C, int ROWS, int ALL, int LOADS, bool CONTIG, bool GATED>
-__device__ __forceinline__ void load_side(const Side& s, int64_t t0, int64_t left, uint8_t* lds, int wave, int lane)
+// Loads the operand's indices t0 .. t0+63 of the sum, of ROWS of its rows from
+// `first` on, into LDS.  TAIL: only `left` of them lie before the sum's end.
+// Addresses are a uniform base and 32-bit offsets in bytes, at most 256 rows of
+// 65536 elements.
+template <class C, int ROWS, bool CONTIG, bool GATED, bool TAIL>
+__device__ __forceinline__ void load_side(const Side& s, int first, int64_t t0, int left, uint8_t* lds, int wave,
+                                          int lane)
 {
+    constexpr int ALL = ROWS / 8, LOADS = (ALL + C::WAVES - 1) / C::WAVES;
     if constexpr (CONTIG) {
-        const int row0 = wave * 8 + (lane >> 3);
-        const uint32_t piece = (lane & 7) ^ swizzle(row0);
-        const uint16_t* base = s.base + t0;
-        const uint16_t* upper = s.upper + t0;
+        const uint32_t piece = (lane & 7) ^ swizzle(wave * 8 + (lane >> 3));
+        const uint8_t* base = (const uint8_t*)(s.base + t0);
+        const uint8_t* upper = (const uint8_t*)(s.upper + t0);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int part = (i * C::WAVES + wave) % ALL;
-            const int row = part * 8 + (lane >> 3);
+            const int row = first + part * 8 + (lane >> 3);
             const bool up = GATED && part * 8 >= ROWS / 2;
-            const uint32_t at = (uint32_t)min(up ? row - ROWS / 2 : row, s.last) * (uint32_t)s.ld + piece * 8;
-            const uint16_t* src = (up ? upper : base) + at;
-            if (left < STEP && (int)(piece * 8) >= left)
-                src = (const uint16_t*)&zeros;
-            load_lds16<false>((const uint8_t*)src, lds + part * 1024);
+            const uint32_t at = (uint32_t)min(up ? row - ROWS / 2 : row, s.last) * (uint32_t)(s.ld * 2) + piece * 16;
+            if constexpr (TAIL)
+                load_to_lds((int)(piece * 8) >= left ? (const uint8_t*)&zeros : (up ? upper : base) + at, lds + part * 1024);
+            else
+                load_to_lds(up ? upper : base, at, lds + part * 1024);
         }
     } else {
         constexpr int PIECES = ROWS / 8;
-        const uint16_t* base = s.base + t0 * s.ld;
+        const uint8_t* base = (const uint8_t*)(s.base + t0 * s.ld);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int part = (i * C::WAVES + wave) % ALL;
             const int t = part * (WAVE / PIECES) + lane / PIECES;
-            const int piece = min((lane % PIECES) ^ turn<PIECES>(t), s.last >> 3);
-            const uint16_t* src = base + ((uint32_t)t * (uint32_t)s.ld + piece * 8);
-            if (left < STEP && t >= left)
-                src = (const uint16_t*)&zeros;
-            load_lds16<false>((const uint8_t*)src, lds + part * 1024);
+            const int piece = min(first / 8 + ((lane % PIECES) ^ turn<PIECES>(t)), s.last >> 3);
+            const uint32_t at = (uint32_t)t * (uint32_t)(s.ld * 2) + piece * 16;
+            if constexpr (TAIL)
+                load_to_lds(t >= left ? (const uint8_t*)&zeros : base + at, lds + part * 1024);
+            else
+                load_to_lds(base, at, lds + part * 1024);
         }
     }
 }
@@ -326,6 +364,49 @@ __device__ inline void expert_rows(const Linear& p, int e, int64_t& a, int64_t& 
     }
 }
 
+// Hands a wave's sums to `finish`, eight consecutive outputs at a time; subtile
+// (j, i) starts at LDS row vrow(j) of V and urow(i) of U.
+template <class C, bool GATED, bool BIAS, int SUMS, class URow, class VRow, class Finish, class FinishBias>
+__device__ __forceinline__ void hand_over(v4f (&acc)[C::NT][C::MT], v4f (&sums)[SUMS], URow urow, VRow vrow, int wn,
+                                          int u_rows, int v_rows, int lane, Finish finish, FinishBias finish_bias)
+{
+    // Lane (r, g) holds column r of a subtile and rows 4g .. 4g+3; lanes of two
+    // subtiles trade so that each holds eight consecutive outputs.
+    const int r = lane & 15, g = lane >> 4;
+    auto eight = [&](int j, int i, float (&v)[8]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const auto two = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[j][i][c]),
+                                                              __float_as_uint(acc[j + 1][i][c]), false, false);
+            v[c] = __uint_as_float(two[0]);
+            v[4 + c] = __uint_as_float(two[1]);
+        }
+    };
+    constexpr int PAIRED = GATED ? C::NT / 2 : C::NT;
+    static_assert(PAIRED % 2 == 0, "whole pairs of subtiles");
+#pragma unroll
+    for (int i = 0; i < C::MT; ++i) {
+        const int u = urow(i) + r;
+#pragma unroll
+        for (int j = 0; j < PAIRED; j += 2) {
+            const int v = vrow(j) + (g & 1) * 16 + (g >> 1) * 8;
+            float a[8], b[8];
+            eight(j, i, a);
+            if constexpr (GATED)
+                eight(j + C::NT / 2, i, b);
+            if (u < u_rows && v < v_rows)
+                finish(u, v, a, b);
+        }
+    }
+    if constexpr (BIAS)
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i) {
+            const int u = urow(wn * SUMS + i) + r;
+            if (wn * SUMS + i < C::MT && g == 0 && u < u_rows)
+                finish_bias(u, sums[i][0]);
+        }
+}
+
 // Sums U(u,t) V(v,t) over t in [t0, t1) for one tile and hands every eight
 // consecutive outputs to `finish(u, v, out[, up])`.
 template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
@@ -336,12 +417,12 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int wm = wave % C::WM, wn = wave / C::WM;
     const int steps = (int)((t1 - t0 + STEP - 1) / STEP);
-    auto issue_to = [&](int step, uint8_t* st) {
+    const int last_left = (int)(t1 - t0) - (steps - 1) * STEP;      // terms of the last stage
+    auto issue = [&](int step, uint8_t* st, auto tail) {
         const int64_t t = t0 + (int64_t)step * STEP;
-        load_side<C, C::BN, C::V_ALL, C::V_LOADS, V_CONTIG, GATED>(vs, t, t1 - t, st, wave, lane);
-        load_side<C, C::BM, C::U_ALL, C::U_LOADS, U_CONTIG, false>(us, t, t1 - t, st + C::V_BYTES, wave, lane);
+        load_side<C, C::BN, V_CONTIG, GATED, tail>(vs, 0, t, last_left, st, wave, lane);
+        load_side<C, C::BM, U_CONTIG, false, tail>(us, 0, t, last_left, st + C::V_BYTES, wave, lane);
     };
-    auto issue = [&](int step) { issue_to(step, lds + step * C::STAGE); };
     // LDS row of V's subtile j: gated tiles keep the gate's rows in their first half
     auto vrow = [&](int j) {
         if (GATED) {
@@ -371,8 +452,10 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
     }
 #pragma unroll
     for (int s = 0; s < C::S; ++s)
-        if (s < steps)
-            issue(s);
+        if (s < steps - 1)
+            issue(s, lds + s * C::STAGE, std::false_type{});
+        else if (s == steps - 1)
+            issue(s, lds + s * C::STAGE, std::true_type{});
     // A stage is summed in two halves of 32.  Each half's operands are read
     // while the half before it is multiplied; in the middle of a stage all its
     // reads are done, its slot is free once every wave is there, and the next
@@ -408,64 +491,202 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
     };
     if (steps > 0) {
         if (steps >= C::S)
-            wait_loads_and_meet<(C::S - 1) * C::LOADS>();
+            meet<(C::S - 1) * C::LOADS>();
         else
-            wait_loads_and_meet<0>();
+            meet<0>();
         read(lds, 0);
     }
     int slot = 0;
-    auto step_of = [&](int step, auto steady) {
+    auto step_of = [&](int step, auto steady, auto tail) {
         uint8_t* st = lds + slot * C::STAGE;
         read(st, 1);
         multiply(0);
-        wait_loads_and_meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
+        meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
         if constexpr (decltype(steady)::value)
-            issue_to(step + C::S, st);
+            issue(step + C::S, st, tail);
         slot = slot + 1 == C::S ? 0 : slot + 1;
         read(lds + slot * C::STAGE, 0);              // (past the last stage: stale, never used)
         multiply(1);
     };
     int step = 0;
-    for (; step + C::S < steps; ++step)
+    for (; step + C::S < steps - 1; ++step)
+        step_of(step, std::true_type{}, std::false_type{});
+    if (step + C::S < steps)
+        step_of(step++, std::true_type{}, std::true_type{});
+    for (; step < steps; ++step)
+        step_of(step, std::false_type{}, std::false_type{});
+
+    hand_over<C, GATED, BIAS>(acc, sums, [&](int i) { return wm * C::TM + i * 16; }, vrow, wn, u_rows, v_rows, lane,
+                              finish, finish_bias);
+}
+
+// The same for the 256 x 256 tile, U in two halves of 128 rows, with V's
+// stages in three slots of LDS and each half of U's in two: 160 KB.  A step is
+// two phases, one for each half of U; a phase's operands are read while the
+// phase before it is multiplied, and what has been read by every wave is
+// loaded anew at once, so that a load has one and a half to two steps to
+// arrive (with two slots for everything, one step).
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
+__device__ __forceinline__ void product_tile_deep(const Side& us, const Side& vs, int64_t t0, int64_t t1, int u_rows,
+                                                  int v_rows, uint8_t* lds, Finish finish, FinishBias finish_bias)
+{
+    static_assert(C::BM == 256 && C::BN == 256 && C::WM == 2 && C::WN == 4, "eight waves of 128 x 64");
+    constexpr int HALF = 128, HALF_BYTES = HALF * STEP * 2;
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    const int steps = (int)((t1 - t0 + STEP - 1) / STEP);
+    const int last_left = (int)(t1 - t0) - (steps - 1) * STEP;
+    uint8_t* const u_lds = lds + 3 * C::V_BYTES;
+    auto v_slot = [&](int s) { return lds + s * C::V_BYTES; };
+    auto u_slot = [&](int half, int s) { return u_lds + (half * 2 + s) * HALF_BYTES; };
+    auto load_v = [&](int step, int slot, auto tail) {
+        load_side<C, C::BN, V_CONTIG, GATED, tail>(vs, 0, t0 + (int64_t)step * STEP, last_left, v_slot(slot), wave, lane);
+    };
+    auto load_u = [&](int half, int step, auto tail) {
+        load_side<C, HALF, U_CONTIG, false, tail>(us, half * HALF, t0 + (int64_t)step * STEP, last_left,
+                                                  u_slot(half, step & 1), wave, lane);
+    };
+    // near the end of the sum: nothing behind the last stage, whose tail is zeros
+    auto load_v_any = [&](int step, int slot) {
+        if (step < steps - 1)
+            load_v(step, slot, std::false_type{});
+        else if (step == steps - 1)
+            load_v(step, slot, std::true_type{});
+    };
+    auto load_u_any = [&](int half, int step) {
+        if (step < steps - 1)
+            load_u(half, step, std::false_type{});
+        else if (step == steps - 1)
+            load_u(half, step, std::true_type{});
+    };
+    auto vrow = [&](int j) {
+        if (GATED) {
+            constexpr int GH = C::NT / 2;
+            return (j < GH ? 0 : C::BN / 2) + wn * (C::TN / 2) + j % GH * 16;
+        }
+        return wn * C::TN + j * 16;
+    };
+    constexpr int UT = C::MT / 2;                    // subtiles of a half
+    const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc[C::NT][C::MT];
+#pragma unroll
+    for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+            acc[j][i] = zero;
+    constexpr int SUMS = C::MT / C::WN;
+    v4f sums[SUMS];
+    v8b ones;
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            ones[c] = (__bf16)1.0f;
+#pragma unroll
+        for (int i = 0; i < SUMS; ++i)
+            sums[i] = zero;
+    }
+    v8b vf[2][C::NT], uf[2][2][UT];                  // V: [k half]; U: [row half][k half]
+    auto read_v = [&](int slot, int h, int j) {
+        vf[h][j] = read_side<C::BN, V_CONTIG>(v_slot(slot), vrow(j), h, lane);
+    };
+    auto read_u = [&](int half, int slot, int h, int i) {
+        uf[half][h][i] = read_side<HALF, U_CONTIG>(u_slot(half, slot), wm * 64 + i * 16, h, lane);
+    };
+    // Four products, and the reads beside them, in this order.
+    auto products = [&](int half, int h, int i) {
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j)
+            acc[j][half * UT + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[h][j], uf[half][h][i],
+                                                                           acc[j][half * UT + i], 0, 0, 0);
+        if constexpr (BIAS)
+            if ((half * UT + i) / SUMS == wn)
+                sums[i % SUMS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf[half][h][i], sums[i % SUMS], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(C::NT == 4 && UT == 4, "the order of reads below");
+    constexpr int V_LOADS = C::V_LOADS, U_LOADS = HALF / 8 / C::WAVES, AHEAD = V_LOADS + 2 * U_LOADS;
+
+    load_v_any(0, 0);
+    load_u_any(0, 0);
+    load_v_any(1, 1);
+    load_u_any(1, 0);
+    load_u_any(0, 1);
+    load_v_any(2, 2);
+    load_u_any(1, 1);
+    if (steps >= 3)
+        meet<AHEAD + V_LOADS + U_LOADS>();
+    else
+        meet<0>();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        read_v(0, 0, q);
+        read_u(0, 0, 0, q);
+        read_u(0, 0, 1, q);
+    }
+    if (steps >= 3)
+        meet<AHEAD>();
+    else
+        meet<0>();
+    int vs_now = 0;
+    auto step_of = [&](int step, auto steady) {
+        // every wave has read the first half of U and V's first indices of this step
+        if constexpr (steady)
+            load_u(0, step + 2, std::false_type{});
+        else
+            load_u_any(0, step + 2);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q < 2) {
+                read_v(vs_now, 1, 2 * q);
+                read_v(vs_now, 1, 2 * q + 1);
+            } else if (q < 6) {
+                read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2);
+                read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2 + 1);
+            }
+            products(0, q / 4, q % 4);
+        }
+        meet<steady ? AHEAD : 0>();
+        // ... and V and the second half of U
+        if constexpr (steady) {
+            load_v(step + 3, vs_now, std::false_type{});
+            load_u(1, step + 2, std::false_type{});
+        } else {
+            load_v_any(step + 3, vs_now);
+            load_u_any(1, step + 2);
+        }
+        vs_now = vs_now == 2 ? 0 : vs_now + 1;
+        // (past the last stage: stale, never used)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q < 4) {
+                read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2);
+                read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2 + 1);
+            } else if (q < 6) {
+                read_v(vs_now, 0, (q & 1) * 2);
+                read_v(vs_now, 0, (q & 1) * 2 + 1);
+            }
+            products(1, q / 4, q % 4);
+        }
+        meet<steady ? AHEAD : 0>();
+    };
+    int step = 0;
+    for (; step + 3 < steps - 1; ++step)
         step_of(step, std::true_type{});
     for (; step < steps; ++step)
         step_of(step, std::false_type{});
+    hand_over<C, GATED, BIAS>(acc, sums, [&](int i) { return i / UT * HALF + wm * 64 + i % UT * 16; }, vrow, wn, u_rows,
+                              v_rows, lane, finish, finish_bias);
+}
 
-    // Lane (r, g) holds column r of a subtile and rows 4g .. 4g+3; lanes of two
-    // subtiles trade so that each holds eight consecutive outputs.
-    const int r = lane & 15, g = lane >> 4;
-    auto eight = [&](int j, int i, float (&v)[8]) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const auto two = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[j][i][c]),
-                                                              __float_as_uint(acc[j + 1][i][c]), false, false);
-            v[c] = __uint_as_float(two[0]);
-            v[4 + c] = __uint_as_float(two[1]);
-        }
-    };
-    constexpr int PAIRED = GATED ? C::NT / 2 : C::NT;
-    static_assert(PAIRED % 2 == 0, "whole pairs of subtiles");
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i) {
-        const int u = wm * C::TM + i * 16 + r;
-#pragma unroll
-        for (int j = 0; j < PAIRED; j += 2) {
-            const int v = vrow(j) + (g & 1) * 16 + (g >> 1) * 8;
-            float a[8], b[8];
-            eight(j, i, a);
-            if constexpr (GATED)
-                eight(j + C::NT / 2, i, b);
-            if (u < u_rows && v < v_rows)
-                finish(u, v, a, b);
-        }
-    }
-    if constexpr (BIAS)
-#pragma unroll
-        for (int i = 0; i < SUMS; ++i) {
-            const int u = wm * C::TM + (wn * SUMS + i) * 16 + r;
-            if (wn * SUMS + i < C::MT && g == 0 && u < u_rows)
-                finish_bias(u, sums[i][0]);
-        }
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
+__device__ __forceinline__ void run_tile(const Side& us, const Side& vs, int64_t t0, int64_t t1, int u_rows,
+                                         int v_rows, uint8_t* lds, Finish finish, FinishBias finish_bias)
+{
+    if constexpr (C::DEEP)
+        product_tile_deep<C, U_CONTIG, V_CONTIG, GATED, BIAS>(us, vs, t0, t1, u_rows, v_rows, lds, finish, finish_bias);
+    else
+        product_tile<C, U_CONTIG, V_CONTIG, GATED, BIAS>(us, vs, t0, t1, u_rows, v_rows, lds, finish, finish_bias);
 }
 
 // The part of [0, steps * STEP) that split `s` of `splits` sums.
@@ -485,6 +706,10 @@ __global__ __launch_bounds__(C::THREADS) void linear_kernel(const Linear p, int 
     Place at;
     if (!find_rows<C::BM>(p, n_tiles, at))
         return;
+    at.e = __builtin_amdgcn_readfirstlane(at.e);             // (uniform already, which the compiler cannot tell)
+    at.m0 = __builtin_amdgcn_readfirstlane(at.m0);
+    at.rows = __builtin_amdgcn_readfirstlane(at.rows);
+    at.n_tile = __builtin_amdgcn_readfirstlane(at.n_tile);
     const int width = FWD ? p.n : p.k;                       // output columns
     const int f = GATED ? p.n / 2 : width;                   // columns that tiles divide
     const int v0 = at.n_tile * (GATED ? C::BN / 2 : C::BN);
@@ -502,10 +727,8 @@ __global__ __launch_bounds__(C::THREADS) void linear_kernel(const Linear p, int 
     int64_t t0, t1;
     split_range(total, splits, blockIdx.z, t0, t1);
     float* part = (float*)p.workspace + (int64_t)blockIdx.z * p.rows * width;
-    product_tile<C, true, FWD, GATED, false>(
-        us, vs, t0, t1, at.rows, vs.last + 1, lds,
-        [&](int u, int v, float(&a)[8], float(&b)[8]) {
-            const int64_t row = at.m0 + u;
+    auto finish = [&](int u, int v, float(&a)[8], float(&b)[8]) {
+        const int64_t row = at.m0 + u;
             const int col = v0 + v;
             if (splits > 1) {
                 store8(part + row * width + col, a);
@@ -518,8 +741,8 @@ __global__ __launch_bounds__(C::THREADS) void linear_kernel(const Linear p, int 
             } else {
                 finish_input(p, row, col, a);
             }
-        },
-        [](int, float) {});
+        };
+    run_tile<C, true, FWD, GATED, false>(us, vs, t0, t1, at.rows, vs.last + 1, lds, finish, [](int, float) {});
 }
 
 // grad_weight: out rows are an expert's weight rows
@@ -535,6 +758,8 @@ __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear 
     tile_in_group(t - (int64_t)e * m_tiles * n_tiles, m_tiles, n_tiles, m, n);
     int64_t a, b;
     expert_rows(p, e, a, b);
+    a = __builtin_amdgcn_readfirstlane((int)a);              // (uniform already, which the compiler cannot tell)
+    b = __builtin_amdgcn_readfirstlane((int)b);
     const int u0 = m * C::BM, v0 = n * C::BN;
     Side us, vs;
     us.ld = p.n;
@@ -557,9 +782,9 @@ __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear 
     };
     auto finish_bias = [&](int u, float s) { (splits > 1 ? part_b : p.dbias)[(int64_t)e * p.n + u0 + u] = s; };
     if (p.dbias && n == 0)
-        product_tile<C, false, false, false, true>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
+        run_tile<C, false, false, false, true>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
     else
-        product_tile<C, false, false, false, false>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
+        run_tile<C, false, false, false, false>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
 }
 
 // --- joins of split sums -----------------------------------------------------------------------
@@ -729,7 +954,7 @@ hipError_t launch_rows(const Linear& p, const Shape& s, hipStream_t stream)
         return e;
     dim3 grid = grid_of(workgroups(p.rows, p.E, C::BM, s.n_tiles));
     grid.z = s.splits;
-    linear_kernel<KIND, C, GATED><<<grid, dim3(C::THREADS), C::S * C::STAGE, stream>>>(p, s.n_tiles, s.splits);
+    linear_kernel<KIND, C, GATED><<<grid, dim3(C::THREADS), C::LDS, stream>>>(p, s.n_tiles, s.splits);
     return hipGetLastError();
 }
 
@@ -784,7 +1009,7 @@ hipError_t launch_linear_grad_weight(const Linear& p, hipStream_t stream)
         return e;
     dim3 grid = grid_of(((int64_t)p.E * m_tiles * n_tiles + 7) / 8 * 8);
     grid.z = splits;
-    linear_weight_kernel<C><<<grid, dim3(C::THREADS), C::S * C::STAGE, stream>>>(p, m_tiles, n_tiles, splits);
+    linear_weight_kernel<C><<<grid, dim3(C::THREADS), C::LDS, stream>>>(p, m_tiles, n_tiles, splits);
     if (splits > 1)
         join_weight_kernel<<<blocks_of(((int64_t)p.E * p.n * p.k + 7) / 8), dim3(256), 0, stream>>>(p, splits);
     return hipGetLastError();
