@@ -105,21 +105,28 @@ __device__ inline int turn(int t)
     return ((t & 3) | (t >> 3 & 1) << 2) << 1 & (PIECES - 1);
 }
 
+// Loads of 1 KB that each wave issues for 64 summed indices of this many rows.
+template <class C>
+__host__ __device__ constexpr int loads_of(int rows)
+{
+    return (rows / 8 + C::WAVES - 1) / C::WAVES;
+}
+
 // Loads the operand's indices t0 .. t0+63 of the sum, of ROWS of its rows from
 // `first` on, into LDS.  TAIL: only `left` of them lie before the sum's end.
 // Addresses are a uniform base and 32-bit offsets in bytes, at most 256 rows of
-// 65536 elements.
+// 65536 elements.  (from, to: some of the wave's loads only.)
 template <class C, int ROWS, bool CONTIG, bool GATED, bool TAIL>
 __device__ __forceinline__ void load_side(const Side& s, int first, int64_t t0, int left, uint8_t* lds, int wave,
-                                          int lane)
+                                          int lane, int from = 0, int to = loads_of<C>(ROWS))
 {
-    constexpr int ALL = ROWS / 8, LOADS = (ALL + C::WAVES - 1) / C::WAVES;
+    constexpr int ALL = ROWS / 8;
     if constexpr (CONTIG) {
         const uint32_t piece = (lane & 7) ^ swizzle(wave * 8 + (lane >> 3));
         const uint8_t* base = (const uint8_t*)(s.base + t0);
         const uint8_t* upper = (const uint8_t*)(s.upper + t0);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
+        for (int i = from; i < to; ++i) {
             const int part = (i * C::WAVES + wave) % ALL;
             const int row = first + part * 8 + (lane >> 3);
             const bool up = GATED && part * 8 >= ROWS / 2;
@@ -133,7 +140,7 @@ __device__ __forceinline__ void load_side(const Side& s, int first, int64_t t0, 
         constexpr int PIECES = ROWS / 8;
         const uint8_t* base = (const uint8_t*)(s.base + t0 * s.ld);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
+        for (int i = from; i < to; ++i) {
             const int part = (i * C::WAVES + wave) % ALL;
             const int t = part * (WAVE / PIECES) + lane / PIECES;
             const int piece = min(first / 8 + ((lane % PIECES) ^ turn<PIECES>(t)), s.last >> 3);
@@ -540,25 +547,21 @@ __device__ __forceinline__ void product_tile_deep(const Side& us, const Side& vs
     uint8_t* const u_lds = lds + 3 * C::V_BYTES;
     auto v_slot = [&](int s) { return lds + s * C::V_BYTES; };
     auto u_slot = [&](int half, int s) { return u_lds + (half * 2 + s) * HALF_BYTES; };
-    auto load_v = [&](int step, int slot, auto tail) {
-        load_side<C, C::BN, V_CONTIG, GATED, tail>(vs, 0, t0 + (int64_t)step * STEP, last_left, v_slot(slot), wave, lane);
-    };
-    auto load_u = [&](int half, int step, auto tail) {
-        load_side<C, HALF, U_CONTIG, false, tail>(us, half * HALF, t0 + (int64_t)step * STEP, last_left,
-                                                  u_slot(half, step & 1), wave, lane);
-    };
-    // near the end of the sum: nothing behind the last stage, whose tail is zeros
-    auto load_v_any = [&](int step, int slot) {
-        if (step < steps - 1)
-            load_v(step, slot, std::false_type{});
+    // Nothing is loaded behind the last stage, whose tail is zeros; `inner`: it is not the last.
+    auto load_v = [&](int step, int slot, auto inner, int from, int to) {
+        const int64_t t = t0 + (int64_t)step * STEP;
+        if (inner || step < steps - 1)
+            load_side<C, C::BN, V_CONTIG, GATED, false>(vs, 0, t, 0, v_slot(slot), wave, lane, from, to);
         else if (step == steps - 1)
-            load_v(step, slot, std::true_type{});
+            load_side<C, C::BN, V_CONTIG, GATED, true>(vs, 0, t, last_left, v_slot(slot), wave, lane, from, to);
     };
-    auto load_u_any = [&](int half, int step) {
-        if (step < steps - 1)
-            load_u(half, step, std::false_type{});
+    auto load_u = [&](int half, int step, auto inner, int from, int to) {
+        const int64_t t = t0 + (int64_t)step * STEP;
+        uint8_t* const slot = u_slot(half, step & 1);
+        if (inner || step < steps - 1)
+            load_side<C, HALF, U_CONTIG, false, false>(us, half * HALF, t, 0, slot, wave, lane, from, to);
         else if (step == steps - 1)
-            load_u(half, step, std::true_type{});
+            load_side<C, HALF, U_CONTIG, false, true>(us, half * HALF, t, last_left, slot, wave, lane, from, to);
     };
     auto vrow = [&](int j) {
         if (GATED) {
@@ -605,17 +608,21 @@ __device__ __forceinline__ void product_tile_deep(const Side& us, const Side& vs
         __builtin_amdgcn_sched_barrier(0);
     };
     static_assert(C::NT == 4 && UT == 4, "the order of reads below");
-    constexpr int V_LOADS = C::V_LOADS, U_LOADS = HALF / 8 / C::WAVES, AHEAD = V_LOADS + 2 * U_LOADS;
-
-    load_v_any(0, 0);
-    load_u_any(0, 0);
-    load_v_any(1, 1);
-    load_u_any(1, 0);
-    load_u_any(0, 1);
-    load_v_any(2, 2);
-    load_u_any(1, 1);
+    // A phase issues four loads, one beside every eight products: two of the half of U that the
+    // phase before it was the last to read, and half of V's, whose slot was free before.
+    constexpr int V_LOADS = loads_of<C>(C::BN), U_LOADS = loads_of<C>(HALF), PHASE = V_LOADS / 2 + U_LOADS;
+    static_assert(V_LOADS == 4 && U_LOADS == 2, "four loads per phase");
+    constexpr std::false_type any{};
+    load_u(0, 0, any, 0, 2);
+    load_v(0, 0, any, 0, 4);
+    load_u(1, 0, any, 0, 2);
+    load_v(1, 1, any, 0, 2);
+    load_u(0, 1, any, 0, 2);
+    load_v(1, 1, any, 2, 4);
+    load_u(1, 1, any, 0, 2);
+    load_v(2, 2, any, 0, 2);
     if (steps >= 3)
-        meet<AHEAD + V_LOADS + U_LOADS>();
+        meet<3 * PHASE>();
     else
         meet<0>();
 #pragma unroll
@@ -625,56 +632,53 @@ __device__ __forceinline__ void product_tile_deep(const Side& us, const Side& vs
         read_u(0, 0, 1, q);
     }
     if (steps >= 3)
-        meet<AHEAD>();
+        meet<2 * PHASE>();
     else
         meet<0>();
-    int vs_now = 0;
+    int now = 0, last = 2;                           // V's slots of this step and the one before it
     auto step_of = [&](int step, auto steady) {
         // every wave has read the first half of U and V's first indices of this step
-        if constexpr (steady)
-            load_u(0, step + 2, std::false_type{});
-        else
-            load_u_any(0, step + 2);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (q < 2) {
-                read_v(vs_now, 1, 2 * q);
-                read_v(vs_now, 1, 2 * q + 1);
+                read_v(now, 1, 2 * q);
+                read_v(now, 1, 2 * q + 1);
             } else if (q < 6) {
                 read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2);
                 read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2 + 1);
             }
+            if (q == 0 || q == 2)
+                load_u(0, step + 2, steady, q / 2, q / 2 + 1);
+            if (q == 4 || q == 6)
+                load_v(step + 2, last, steady, q / 2, q / 2 + 1);
             products(0, q / 4, q % 4);
         }
-        meet<steady ? AHEAD : 0>();
-        // ... and V and the second half of U
-        if constexpr (steady) {
-            load_v(step + 3, vs_now, std::false_type{});
-            load_u(1, step + 2, std::false_type{});
-        } else {
-            load_v_any(step + 3, vs_now);
-            load_u_any(1, step + 2);
-        }
-        vs_now = vs_now == 2 ? 0 : vs_now + 1;
-        // (past the last stage: stale, never used)
+        meet<steady ? 2 * PHASE : 0>();
+        // ... and V and the second half of U; what is read past the last stage is stale, and not used
+        last = now;
+        now = now == 2 ? 0 : now + 1;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (q < 4) {
                 read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2);
                 read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2 + 1);
             } else if (q < 6) {
-                read_v(vs_now, 0, (q & 1) * 2);
-                read_v(vs_now, 0, (q & 1) * 2 + 1);
+                read_v(now, 0, (q & 1) * 2);
+                read_v(now, 0, (q & 1) * 2 + 1);
             }
+            if (q == 0 || q == 2)
+                load_u(1, step + 2, steady, q / 2, q / 2 + 1);
+            if (q == 4 || q == 6)
+                load_v(step + 3, last, steady, q / 2 - 2, q / 2 - 1);
             products(1, q / 4, q % 4);
         }
-        meet<steady ? AHEAD : 0>();
+        meet<steady ? 2 * PHASE : 0>();
     };
     int step = 0;
     for (; step + 3 < steps - 1; ++step)
         step_of(step, std::true_type{});
     for (; step < steps; ++step)
-        step_of(step, std::false_type{});
+        step_of(step, any);
     hand_over<C, GATED, BIAS>(acc, sums, [&](int i) { return i / UT * HALF + wm * 64 + i % UT * 16; }, vrow, wn, u_rows,
                               v_rows, lane, finish, finish_bias);
 }
