@@ -25,6 +25,24 @@ namespace moe {
 namespace ops {
 namespace {
 
+// The same number, which the compiler takes for a new one: what is formed from
+// it is not formed ahead of a loop and held in registers that the loop needs.
+__device__ inline int anew(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// The kernel's arguments, read again from where the launch left them (its first
+// argument is a Linear): held through a main loop they would take the scalar
+// registers that it needs.
+__device__ inline const Linear& arguments()
+{
+    auto p = (const __attribute__((address_space(4))) Linear*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const Linear*)p;
+}
+
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lv4s;
@@ -50,28 +68,42 @@ struct Block {
     static constexpr int LOADS = V_LOADS + U_LOADS;
     static_assert(V_ALL % WAVES == 0 && U_ALL % 2 == 0 && WAVES % 2 == 0, "a wave's parts share the swizzle");
     static_assert(NT % 2 == 0, "the epilogue pairs subtiles");
+    // first row of U's subtile i; the deep tile takes U in halves of 128 rows
+    static __device__ inline int u_row_of(int i, int wm)
+    {
+        if constexpr (DEEP)
+            return i / (MT / 2) * (BM / 2) + wm * (TM / 2) + i % (MT / 2) * 16;
+        else
+            return wm * TM + i * 16;
+    }
 };
 
-// 16 bytes per lane from memory to LDS, 1 KB from `lds` on: at a uniform base
-// and 32-bit offsets, or at 64-bit addresses.  The compiler does not see these
-// as memory accesses: told of them, it would wait for all of them ahead of
-// every transposing LDS read.  They are waited for by meet() alone, and stay
-// between the two that enclose them (volatile statements keep their order).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"      // m0, a reserved register, is named as overwritten
-__device__ inline void load_to_lds(const uint8_t* base, uint32_t offset, const uint8_t* lds)
+// A buffer of memory as the buffer instructions address it: what lies outside
+// [base, base + bytes) reads as zero.
+typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
+__device__ inline Buffer buffer_of(const void* base, uint32_t bytes)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(offset), "s"(base),
-                 "s"((uint32_t)(uintptr_t)(lvoid*)lds)
-                 : "m0");
-}
-__device__ inline void load_to_lds(const uint8_t* address, const uint8_t* lds)
-{
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(address),
-                 "s"((uint32_t)(uintptr_t)(lvoid*)lds)
-                 : "m0");
+    constexpr uint32_t RAW32 = 0x00020000;               // 32-bit elements, no stride
+    const uint64_t at = (uint64_t)base;
+    // (uniform already, which the compiler cannot always tell)
+    return Buffer{(uint32_t)__builtin_amdgcn_readfirstlane((int)at),
+                  (uint32_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), RAW32};
 }
 
+// 16 bytes per lane from a buffer, at `offset` of the lane and `more` of all, to
+// LDS, 1 KB from `lds` on.  The compiler does not see this as a memory access:
+// told of it, it would wait for all such loads ahead of every transposing LDS
+// read.  They are waited for by meet() alone, and stay between the two that
+// enclose them (volatile statements keep their order).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"      // m0, a reserved register, is named as overwritten
+__device__ inline void load_to_lds(Buffer b, uint32_t offset, uint32_t more, const uint8_t* lds)
+{
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(b),
+                 "s"(more), "s"((uint32_t)(uintptr_t)(lvoid*)lds)
+                 : "m0");
+}
 #pragma clang diagnostic pop
 
 // Everything this wave loaded but its last N loads has arrived in LDS, its own
@@ -84,16 +116,14 @@ __device__ inline void meet()
     asm volatile("s_barrier" ::: "memory");
 }
 
-// What is loaded in place of indices behind the end of the sum.
-__device__ const uint4 zeros = {0, 0, 0, 0};
-
-// One operand of a tile: element (i, t) lies at base[i * ld + t] (CONTIG) or
-// base[t * ld + i]; i <= last.
+// One operand of a tile, from the tile's first index and the sum's first term
+// on: element (i, t) lies at base[i * ld + t] (CONTIG) or base[t * ld + i].
 struct Side {
     const uint16_t* base;
     const uint16_t* upper;    // CONTIG, gated: where rows from half the tile on start
-    int ld;
-    int last;
+    int ld;                   // elements
+    int valid;                // indices i that exist (gated: of each half)
+    int terms;                // t that exist
 };
 
 // 16-byte piece c of row t of a transposed operand lies at place c ^ turn(t):
@@ -112,80 +142,104 @@ __host__ __device__ constexpr int loads_of(int rows)
     return (rows / 8 + C::WAVES - 1) / C::WAVES;
 }
 
-// Loads the operand's indices t0 .. t0+63 of the sum, of ROWS of its rows from
-// `first` on, into LDS.  TAIL: only `left` of them lie before the sum's end.
-// Addresses are a uniform base and 32-bit offsets in bytes, at most 256 rows of
-// 65536 elements.  (from, to: some of the wave's loads only.)
+// Loads stage `step` of the operand's sum, ROWS of its rows from `first` on,
+// into LDS: the wave's loads from .. to-1.  What does not exist is zero: rows
+// lie outside the buffer, and so do a transposed operand's last terms; a
+// contiguous one's (TAIL: the last stage) are sent there.  A lane's offset is
+// the same in all loads of all stages, so that it takes one register.
 template <class C, int ROWS, bool CONTIG, bool GATED, bool TAIL>
-__device__ __forceinline__ void load_side(const Side& s, int first, int64_t t0, int left, uint8_t* lds, int wave,
-                                          int lane, int from = 0, int to = loads_of<C>(ROWS))
+__device__ __forceinline__ void load_side(const Side& s, int first, int step, uint8_t* lds, int wave, int lane,
+                                          int from = 0, int to = loads_of<C>(ROWS))
 {
     constexpr int ALL = ROWS / 8;
+    const int part0 = wave % ALL;                        // load i brings part i * WAVES + part0
+    const uint32_t ld = (uint32_t)s.ld * 2;
     if constexpr (CONTIG) {
-        const uint32_t piece = (lane & 7) ^ swizzle(wave * 8 + (lane >> 3));
-        const uint8_t* base = (const uint8_t*)(s.base + t0);
-        const uint8_t* upper = (const uint8_t*)(s.upper + t0);
+        constexpr int EACH = C::WAVES * 8;               // rows that the waves bring at a time
+        constexpr int HALF = GATED ? ROWS / 2 : ROWS;
+        static_assert(EACH >= ROWS || HALF % EACH == 0, "a load is of one half");
+        const int piece = (lane & 7) ^ swizzle(part0 * 8 + (lane >> 3));
+        uint32_t offset = (uint32_t)(part0 * 8 + (lane >> 3)) * ld + piece * 16;
+        if (TAIL && piece * 8 >= s.terms - step * STEP)
+            offset = 0x40000000;
+        const uint32_t bytes = (uint32_t)(s.valid - 1) * ld + (uint32_t)s.terms * 2;
 #pragma unroll
         for (int i = from; i < to; ++i) {
-            const int part = (i * C::WAVES + wave) % ALL;
-            const int row = first + part * 8 + (lane >> 3);
-            const bool up = GATED && part * 8 >= ROWS / 2;
-            const uint32_t at = (uint32_t)min(up ? row - ROWS / 2 : row, s.last) * (uint32_t)(s.ld * 2) + piece * 16;
-            if constexpr (TAIL)
-                load_to_lds((int)(piece * 8) >= left ? (const uint8_t*)&zeros : (up ? upper : base) + at, lds + part * 1024);
-            else
-                load_to_lds(up ? upper : base, at, lds + part * 1024);
+            const bool up = GATED && i * EACH >= HALF;
+            load_to_lds(buffer_of(up ? s.upper : s.base, bytes), offset,
+                        (uint32_t)(first + i * EACH - (up ? HALF : 0)) * ld + step * STEP * 2,
+                        lds + (i * C::WAVES + part0) * 1024);
         }
     } else {
-        constexpr int PIECES = ROWS / 8;
-        const uint8_t* base = (const uint8_t*)(s.base + t0 * s.ld);
+        constexpr int PIECES = ROWS / 8, TERMS = WAVE / PIECES;      // terms per load
+        constexpr int EACH = C::WAVES * TERMS;
+        static_assert(EACH >= STEP || EACH % 16 == 0, "one swizzle per lane");
+        const int t = part0 * TERMS + lane / PIECES;
+        const uint32_t offset = (uint32_t)t * ld + ((lane % PIECES) ^ turn<PIECES>(t)) * 16;
+        const uint32_t terms = TAIL ? s.terms - step * STEP : STEP;
+        const Buffer b = buffer_of(s.base + (int64_t)step * STEP * s.ld, (terms - 1) * ld + (uint32_t)s.valid * 2);
 #pragma unroll
-        for (int i = from; i < to; ++i) {
-            const int part = (i * C::WAVES + wave) % ALL;
-            const int t = part * (WAVE / PIECES) + lane / PIECES;
-            const int piece = min(first / 8 + ((lane % PIECES) ^ turn<PIECES>(t)), s.last >> 3);
-            const uint32_t at = (uint32_t)t * (uint32_t)(s.ld * 2) + piece * 16;
-            if constexpr (TAIL)
-                load_to_lds(t >= left ? (const uint8_t*)&zeros : base + at, lds + part * 1024);
-            else
-                load_to_lds(base, at, lds + part * 1024);
-        }
+        for (int i = from; i < to; ++i)
+            load_to_lds(b, offset, i * EACH * ld + first * 2, lds + (i * C::WAVES + part0) * 1024);
     }
 }
 
-// The operand's 16 rows from `row` on, summed indices 32*half .. +31, as the matrix instruction
-// takes them: lane (r, g) holds row r, indices 8g .. 8g+7.
-template <int ROWS, bool CONTIG>
-__device__ __forceinline__ v8b read_side(const uint8_t* lds, int row, int half, int lane)
-{
-    const int r = lane & 15, g = lane >> 4;
-    if constexpr (CONTIG) {
-        const int at = row + r;
-        return *(const v8b*)(lds + at * 128 + (((half * 4 + g) ^ swizzle(r)) << 4));
-    } else {
-        constexpr int PIECES = ROWS / 8;
-        const int t = half * 32 + g * 8 + (r >> 2);
-        const int piece = row / 8 + (r >> 1 & 1);
-        const int at = t * ROWS * 2 + ((piece ^ turn<PIECES>(t)) << 4) + ((r & 1) << 3);
-        const int at4 = (t + 4) * ROWS * 2 + ((piece ^ turn<PIECES>(t + 4)) << 4) + ((r & 1) << 3);
-        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lv4s*)(lds + at));
-        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lv4s*)(lds + at4));
-        typedef short v8s __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(v8b, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+// Reads an operand of a stage in LDS, as the matrix instruction takes it: lane
+// (r, g) holds row r of 16, summed indices 32*half + 8g .. +7.  Where those of
+// the wave's first subtile lie is held in registers (N subtiles of a transposed
+// operand, whose places are an exclusive or apart); other rows, halves and slots
+// are a constant away.
+template <int ROWS, bool CONTIG, int N>
+struct Reader {
+    static constexpr int COUNT = CONTIG ? 2 : N;
+    uint32_t at[COUNT];
+    __device__ inline Reader(const uint8_t* lds, int row0, int lane)
+    {
+        const int r = lane & 15, g = lane >> 4;
+        const uint32_t base = (uint32_t)(uintptr_t)(lvoid*)lds;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i)
+            if constexpr (CONTIG) {
+                at[i] = base + (row0 + r) * 128 + (((i * 4 + g) ^ swizzle(r)) << 4);
+            } else {
+                constexpr int PIECES = ROWS / 8;
+                const int t = g * 8 + (r >> 2);
+                at[i] = base + t * ROWS * 2 + (((row0 / 8 + 2 * i + (r >> 1 & 1)) ^ turn<PIECES>(t)) << 4) + ((r & 1) << 3);
+            }
     }
-}
+    __device__ inline void move(uint32_t by)
+    {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i)
+            at[i] += by;
+    }
+    // The subtile `down` rows (CONTIG) below the first, or number i; `off` bytes further on.
+    __device__ __forceinline__ v8b read(int half, int i, int down, int off) const
+    {
+        if constexpr (CONTIG) {
+            typedef __attribute__((address_space(3))) const v8b lv8b;
+            return *(lv8b*)(at[half] + down * 128 + off);
+        } else {
+            const uint32_t p = at[i] + half * 32 * ROWS * 2 + off;       // (terms 4 apart share the turn)
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lv4s*)p);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lv4s*)(p + 4 * ROWS * 2));
+            typedef short v8s __attribute__((ext_vector_type(8)));
+            return __builtin_bit_cast(v8b, (v8s)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+};
 
 // --- epilogues: eight consecutive outputs of a row ---------------------------------------------
 
-__device__ inline void open8(const uint16_t* p, float (&f)[8])
+__device__ inline void open8(const v4u& u, float (&f)[8])
 {
-    const v4u u = *(const v4u*)p;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         f[2 * c] = bf16_lo(u[c]);
         f[2 * c + 1] = bf16_hi(u[c]);
     }
 }
+__device__ inline v4u load8(const uint16_t* p) { return *(const v4u*)p; }
 __device__ inline void store8(uint16_t* p, const float (&f)[8])
 {
     *(v4u*)p = v4u{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7])};
@@ -195,10 +249,10 @@ __device__ inline void store8(float* p, const float (&f)[8])
     ((v4f*)p)[0] = v4f{f[0], f[1], f[2], f[3]};
     ((v4f*)p)[1] = v4f{f[4], f[5], f[6], f[7]};
 }
-__device__ inline void add8(const uint16_t* p, float (&f)[8])
+__device__ inline void add8(const v4u& u, float (&f)[8])
 {
     float r[8];
-    open8(p, r);
+    open8(u, r);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         f[c] += r[c];
@@ -250,111 +304,146 @@ __device__ inline float normal_cdf(float z, float e)
     return z < 0.0f ? tail : 1.0f - tail;
 }
 
-__device__ inline float activate(int act, float z)
+__device__ inline void activate8(int act, float (&z)[8])
 {
-    switch (act) {
-    case MOE_ACT_RELU: return z <= 0.0f ? 0.0f : z;
-    case MOE_ACT_GELU: return z * normal_cdf(z, bell(z));
-    case MOE_ACT_SILU: return silu(z);
-    default: return z;
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            z[c] = z[c] <= 0.0f ? 0.0f : z[c];
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            z[c] *= normal_cdf(z[c], bell(z[c]));
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            z[c] = silu(z[c]);
     }
 }
-__device__ inline float slope(int act, float z)
+// z to the activation's slopes there.
+__device__ inline void slopes8(int act, float (&z)[8])
 {
-    switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case MOE_ACT_GELU: {
-        const float e = bell(z);
-        return fmaf(z * INV_SQRT_2PI, e, normal_cdf(z, e));
-    }
-    case MOE_ACT_SILU: return silu_slope(z);
-    default: return 1.0f;
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            z[c] = z[c] > 0.0f ? 1.0f : 0.0f;
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float e = bell(z[c]);
+            z[c] = fmaf(z[c] * INV_SQRT_2PI, e, normal_cdf(z[c], e));
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            z[c] = silu_slope(z[c]);
     }
 }
 
-// z in fp32 to y; z, bias and residual as the call has them.
-__device__ inline void finish_forward(const Linear& p, int e, int64_t row, int col, float (&v)[8])
-{
-    if (p.bias)
-        add8(p.bias + (int64_t)e * p.n + col, v);
-    if (p.z_out)
-        store8(p.z_out + row * p.n + col, v);
-    if (p.act != MOE_ACT_NONE)
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] = activate(p.act, v[c]);
-    const int64_t at = row * p.n + col;
-    if (p.residual)
-        add8(p.residual + at, v);
-    store_out(p, at, v);
-}
-__device__ inline void finish_gated(const Linear& p, int e, int64_t row, int col, float (&g)[8], float (&u)[8])
-{
-    const int f = p.n / 2;
-    if (p.bias) {
-        add8(p.bias + (int64_t)e * p.n + col, g);
-        add8(p.bias + (int64_t)e * p.n + f + col, u);
-    }
-    if (p.z_out) {
-        store8(p.z_out + row * p.n + col, g);
-        store8(p.z_out + row * p.n + f + col, u);
-    }
-    float v[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        v[c] = silu(g[c]) * u[c];
-    const int64_t at = row * f + col;
-    if (p.residual)
-        add8(p.residual + at, v);
-    store_out(p, at, v);
-}
-// d of silu(gate) * up to the gradients of gate and up.
-__device__ inline void gated_slopes(const float (&d)[8], float (&g)[8], float (&u)[8])
-{
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const float z = g[c];
-        g[c] = d[c] * u[c] * silu_slope(z);
-        u[c] = d[c] * silu(z);
-    }
-}
-__device__ inline void finish_input(const Linear& p, int64_t row, int col, float (&v)[8])
-{
-    if (p.act == MOE_ACT_SWIGLU) {
-        const int64_t at = row * 2 * p.k + col;
-        float g[8], u[8];
-        open8(p.z_in + at, g);
-        open8(p.z_in + at + p.k, u);
-        gated_slopes(v, g, u);
-        if (p.residual) {
-            add8(p.residual + at, g);
-            add8(p.residual + at + p.k, u);
+// What a call reads for eight outputs: bias, pre-activations, residual (with
+// SWIGLU of both halves).
+struct Extra {
+    v4u z[2], residual[2];
+};
+
+template <Kind KIND, bool GATED>
+struct Finish {
+    static constexpr bool FWD = KIND == Kind::FORWARD;
+    const Linear& p;
+    __device__ inline explicit Finish(const Linear& p_) : p(p_) {}
+
+    __device__ inline Extra fetch(int64_t row, int col) const
+    {
+        Extra e{};
+        const bool two = !FWD && p.act == MOE_ACT_SWIGLU;
+        const int width = FWD ? (GATED ? p.n / 2 : p.n) : two ? 2 * p.k : p.k;
+        const int64_t at = row * width + col;
+        if (!FWD && p.z_in) {
+            e.z[0] = load8(p.z_in + at);
+            if (two)
+                e.z[1] = load8(p.z_in + at + p.k);
         }
-        store_out(p, at, g);
-        store_out(p, at + p.k, u);
-        return;
+        if (p.residual) {
+            e.residual[0] = load8(p.residual + at);
+            if (two)
+                e.residual[1] = load8(p.residual + at + p.k);
+        }
+        return e;
     }
-    const int64_t at = row * p.k + col;
-    if (p.act != MOE_ACT_NONE) {
-        float z[8];
-        open8(p.z_in + at, z);
+    __device__ inline void fetch_bias(int expert, int col, v4u (&bias)[2]) const
+    {
+        bias[0] = bias[1] = v4u{0, 0, 0, 0};
+        if (FWD && p.bias) {
+            bias[0] = load8(p.bias + (int64_t)expert * p.n + col);
+            if (GATED)
+                bias[1] = load8(p.bias + (int64_t)expert * p.n + p.n / 2 + col);
+        }
+    }
+    // a: the sums (GATED: of the gate; b: of up)
+    __device__ inline void operator()(int64_t row, int col, float (&a)[8], float (&b)[8], const Extra& e,
+                                      const v4u (&bias)[2]) const
+    {
+        if constexpr (FWD) {
+            if (p.bias) {
+                add8(bias[0], a);
+                if (GATED)
+                    add8(bias[1], b);
+            }
+            if (p.z_out) {
+                store8(p.z_out + row * p.n + col, a);
+                if (GATED)
+                    store8(p.z_out + row * p.n + p.n / 2 + col, b);
+            }
+            if constexpr (GATED) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] *= slope(p.act, z[c]);
+                for (int c = 0; c < 8; ++c)
+                    a[c] = silu(a[c]) * b[c];
+            } else if (p.act != MOE_ACT_NONE) {
+                activate8(p.act, a);
+            }
+            if (p.residual)
+                add8(e.residual[0], a);
+            store_out(p, row * (GATED ? p.n / 2 : p.n) + col, a);
+        } else if (p.act == MOE_ACT_SWIGLU) {
+            float g[8], u[8];
+            open8(e.z[0], g);
+            open8(e.z[1], u);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float z = g[c];
+                g[c] = a[c] * u[c] * silu_slope(z);
+                u[c] = a[c] * silu(z);
+            }
+            if (p.residual) {
+                add8(e.residual[0], g);
+                add8(e.residual[1], u);
+            }
+            const int64_t at = row * 2 * p.k + col;
+            store_out(p, at, g);
+            store_out(p, at + p.k, u);
+        } else {
+            if (p.act != MOE_ACT_NONE) {
+                float z[8];
+                open8(e.z[0], z);
+                slopes8(p.act, z);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    a[c] *= z[c];
+            }
+            if (p.residual)
+                add8(e.residual[0], a);
+            store_out(p, row * p.k + col, a);
+        }
     }
-    if (p.residual)
-        add8(p.residual + at, v);
-    store_out(p, at, v);
-}
+};
 
 // --- tiles -------------------------------------------------------------------------------------
 
 // Tile t of T: consecutive workgroups go to the 8 XCDs in turn, each XCD takes
 // one contiguous run of tiles.
-__device__ inline bool tile_of_workgroup(int64_t tiles, int64_t& t)
+__device__ inline bool tile_of_workgroup(int64_t id, int64_t tiles, int64_t& t)
 {
     const int64_t per_xcd = (tiles + 7) / 8;
-    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     t = (id & 7) * per_xcd + (id >> 3);
     return id >> 3 < per_xcd && t < tiles;
 }
@@ -372,14 +461,21 @@ __device__ inline void tile_in_group(int64_t v, int m_tiles, int n_tiles, int& m
 }
 
 template <int BM>
-__device__ inline bool find_rows(const Linear& p, int n_tiles, Place& at)
+__device__ inline bool find_rows(const Linear& p, int n_tiles, int64_t id, Place& at)
 {
-    if (p.offsets)
-        return p.E <= 4 * WAVE ? find_tile<BM, 4>(p.offsets, p.E, p.rows, n_tiles, at)
-                               : find_tile<BM, 16>(p.offsets, p.E, p.rows, n_tiles, at);
+    if (p.offsets) {
+        const int lane = anew(threadIdx.x & (WAVE - 1));
+        const bool found = p.E <= 4 * WAVE ? find_tile<BM, 4>(p.offsets, p.E, p.rows, n_tiles, at, id, lane)
+                                           : find_tile<BM, 16>(p.offsets, p.E, p.rows, n_tiles, at, id, lane);
+        at.e = __builtin_amdgcn_readfirstlane(at.e);         // (uniform already, which the compiler cannot tell)
+        at.m0 = __builtin_amdgcn_readfirstlane(at.m0);
+        at.rows = __builtin_amdgcn_readfirstlane(at.rows);
+        at.n_tile = __builtin_amdgcn_readfirstlane(at.n_tile);
+        return found;
+    }
     const int m_tiles = (int)((p.rows + BM - 1) / BM);
     int64_t t;
-    if (!tile_of_workgroup((int64_t)m_tiles * n_tiles, t))
+    if (!tile_of_workgroup(id, (int64_t)m_tiles * n_tiles, t))
         return false;
     int m;
     tile_in_group(t, m_tiles, n_tiles, m, at.n_tile);
@@ -400,92 +496,148 @@ __device__ inline void expert_rows(const Linear& p, int e, int64_t& a, int64_t& 
     }
 }
 
-// Hands a wave's sums to `finish`, eight consecutive outputs at a time; subtile
-// (j, i) starts at LDS row vrow(j) of V and urow(i) of U.
-template <class C, bool GATED, bool BIAS, int SUMS, class URow, class VRow, class Finish, class FinishBias>
-__device__ __forceinline__ void hand_over(v4f (&acc)[C::NT][C::MT], v4f (&sums)[SUMS], URow urow, VRow vrow, int wn,
-                                          int u_rows, int v_rows, int lane, Finish finish, FinishBias finish_bias)
+// One tile's product.
+struct Work {
+    Side us, vs;              // of as many terms
+    __device__ inline int steps() const { return (us.terms + (STEP - 1)) / STEP; }
+};
+
+// LDS rows of V's subtiles: the wave's first, and how far below it subtile j is; gated tiles
+// keep the gate's rows in their first half.
+template <class C, bool GATED>
+__device__ inline int v_row_of(int wn)
 {
-    // Lane (r, g) holds column r of a subtile and rows 4g .. 4g+3; lanes of two
-    // subtiles trade so that each holds eight consecutive outputs.
-    const int r = lane & 15, g = lane >> 4;
-    auto eight = [&](int j, int i, float (&v)[8]) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const auto two = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[j][i][c]),
-                                                              __float_as_uint(acc[j + 1][i][c]), false, false);
-            v[c] = __uint_as_float(two[0]);
-            v[4 + c] = __uint_as_float(two[1]);
-        }
-    };
-    constexpr int PAIRED = GATED ? C::NT / 2 : C::NT;
-    static_assert(PAIRED % 2 == 0, "whole pairs of subtiles");
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i) {
-        const int u = urow(i) + r;
-#pragma unroll
-        for (int j = 0; j < PAIRED; j += 2) {
-            const int v = vrow(j) + (g & 1) * 16 + (g >> 1) * 8;
-            float a[8], b[8];
-            eight(j, i, a);
-            if constexpr (GATED)
-                eight(j + C::NT / 2, i, b);
-            if (u < u_rows && v < v_rows)
-                finish(u, v, a, b);
-        }
-    }
-    if constexpr (BIAS)
-#pragma unroll
-        for (int i = 0; i < SUMS; ++i) {
-            const int u = urow(wn * SUMS + i) + r;
-            if (wn * SUMS + i < C::MT && g == 0 && u < u_rows)
-                finish_bias(u, sums[i][0]);
-        }
+    return wn * (GATED ? C::TN / 2 : C::TN);
+}
+template <class C, bool GATED>
+__device__ constexpr int v_down(int j)
+{
+    return GATED ? (j < C::NT / 2 ? 0 : C::BN / 2) + j % (C::NT / 2) * 16 : j * 16;
 }
 
-// Sums U(u,t) V(v,t) over t in [t0, t1) for one tile and hands every eight
-// consecutive outputs to `finish(u, v, out[, up])`.
-template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
-__device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int64_t t0, int64_t t1, int u_rows,
-                                             int v_rows, uint8_t* lds, Finish finish, FinishBias finish_bias)
-{
-    const int lane = threadIdx.x & (WAVE - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int wm = wave % C::WM, wn = wave / C::WM;
-    const int steps = (int)((t1 - t0 + STEP - 1) / STEP);
-    const int last_left = (int)(t1 - t0) - (steps - 1) * STEP;      // terms of the last stage
-    auto issue = [&](int step, uint8_t* st, auto tail) {
-        const int64_t t = t0 + (int64_t)step * STEP;
-        load_side<C, C::BN, V_CONTIG, GATED, tail>(vs, 0, t, last_left, st, wave, lane);
-        load_side<C, C::BM, U_CONTIG, false, tail>(us, 0, t, last_left, st + C::V_BYTES, wave, lane);
-    };
-    // LDS row of V's subtile j: gated tiles keep the gate's rows in their first half
-    auto vrow = [&](int j) {
-        if (GATED) {
-            constexpr int HALF = C::NT / 2;
-            return (j < HALF ? 0 : C::BN / 2) + wn * (C::TN / 2) + j % HALF * 16;
-        }
-        return wn * C::TN + j * 16;
-    };
-    const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
+template <class C>
+struct Sums {
     v4f acc[C::NT][C::MT];
-#pragma unroll
-    for (int j = 0; j < C::NT; ++j)
-#pragma unroll
-        for (int i = 0; i < C::MT; ++i)
-            acc[j][i] = zero;
     // sums of U alone (the bias' gradient): the waves that share U's rows share its subtiles
-    constexpr int SUMS = (C::MT + C::WN - 1) / C::WN;
-    v4f sums[SUMS];
-    v8b ones;
-    if constexpr (BIAS) {
+    static constexpr int ALONE = (C::MT + C::WN - 1) / C::WN;
+    v4f alone[ALONE];
+    __device__ inline void clear()
+    {
+        const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            ones[c] = (__bf16)1.0f;
+        for (int j = 0; j < C::NT; ++j)
 #pragma unroll
-        for (int i = 0; i < SUMS; ++i)
-            sums[i] = zero;
+            for (int i = 0; i < C::MT; ++i)
+                acc[j][i] = zero;
+#pragma unroll
+        for (int i = 0; i < ALONE; ++i)
+            alone[i] = zero;
     }
+    template <bool BIAS>
+    __device__ inline void add(int i, int wn, const v8b (&vf)[C::NT], v8b uf)
+    {
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j)
+            acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[j], uf, acc[j][i], 0, 0, 0);
+        if constexpr (BIAS)
+            if (i / ALONE == wn) {
+                v8b ones;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    ones[c] = (__bf16)1.0f;
+                alone[i % ALONE] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf, alone[i % ALONE], 0, 0, 0);
+            }
+    }
+};
+
+// Hands a wave's sums to the tiles' finish, eight consecutive outputs at a time:
+// 16 rows of U by the wave's 64 of V go through 4 KB of LDS of its own, so that
+// its stores are whole lines (four lanes of 16 bytes from the sums' own layout
+// are half lines), its code is that of one such part, and what the next part
+// reads from memory is on its way meanwhile.
+template <class C, bool GATED, bool BIAS, class Tiles>
+__device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows, uint8_t* lds, int wave, int lane,
+                                          Tiles& tiles)
+{
+    static_assert(C::NT == 4, "a wave has 64 rows of V");
+    constexpr int PASSES = GATED ? 1 : 2;            // by 8 (GATED: 16) rows of U
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    float* const part = (float*)(lds + wave * 4096);
+    // 16-byte piece q of row r lies at place q ^ r: rows apart in the banks both ways
+    auto place = [&](int row, int q) { return part + row * 64 + ((q ^ row) << 2); };
+    const int row0 = GATED ? lane >> 2 : lane >> 3, col = GATED ? lane & 3 : lane & 7;
+    const int v = (GATED ? wn * 32 : wn * 64) + col * 8;
+    const bool live_v = v < v_rows;
+    v4u bias[2];
+    tiles.fetch_bias(live_v ? v : 0, bias);
+    auto fetch = [&](int i, Extra (&e)[PASSES]) {
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+            const int u = C::u_row_of(i, wm) + q * 8 + row0;
+            if (u < u_rows && live_v)
+                e[q] = tiles.fetch(u, v);
+        }
+    };
+    Extra now[PASSES], next[PASSES];
+    fetch(0, next);
+#pragma unroll 1
+    for (int i = 0; i < C::MT; ++i) {
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q)
+            now[q] = next[q];
+        if (i + 1 < C::MT)
+            fetch(i + 1, next);
+        // lane (r, g) holds row r of U and rows 4g .. 4g+3 of each subtile of V
+#pragma unroll
+        for (int s = 0; s < C::MT; ++s)
+            if (s == i)
+#pragma unroll
+                for (int j = 0; j < C::NT; ++j)
+                    *(v4f*)place(lane & 15, j * 4 + (lane >> 4)) = sums.acc[j][s];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q) {
+            const int row = q * 8 + row0, u = C::u_row_of(i, wm) + row;
+            float a[8], b[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const v4f x = *(const v4f*)place(row, col * 2 + h);
+                v4f y;
+                if (GATED)
+                    y = *(const v4f*)place(row, 8 + col * 2 + h);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    a[4 * h + c] = x[c];
+                    if (GATED)
+                        b[4 * h + c] = y[c];
+                }
+            }
+            if (u < u_rows && live_v)
+                tiles.finish(u, v, a, b, now[q], bias);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if constexpr (BIAS) {
+        constexpr int ALONE = Sums<C>::ALONE;
+#pragma unroll
+        for (int i = 0; i < ALONE; ++i) {
+            const int u = C::u_row_of(wn * ALONE + i, wm) + (lane & 15);
+            if (wn * ALONE + i < C::MT && lane < 16 && u < u_rows)
+                tiles.finish_bias(u, sums.alone[i][0]);
+        }
+    }
+}
+
+// The product of one tile, with S stages of both operands in LDS.
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS>
+__device__ __forceinline__ void sum_tile(const Work& w, uint8_t* lds, int wave, int lane, Sums<C>& sums)
+{
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    const int steps = w.steps();
+    auto issue = [&](int step, uint8_t* st, auto tail) {
+        load_side<C, C::BN, V_CONTIG, GATED, tail>(w.vs, 0, step, st, wave, lane);
+        load_side<C, C::BM, U_CONTIG, false, tail>(w.us, 0, step, st + C::V_BYTES, wave, lane);
+    };
 #pragma unroll
     for (int s = 0; s < C::S; ++s)
         if (s < steps - 1)
@@ -497,25 +649,20 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
     // reads are done, its slot is free once every wave is there, and the next
     // stage has arrived.
     v8b vf[2][C::NT], uf[2][C::MT];
-    auto read = [&](const uint8_t* st, int h) {
+    const Reader<C::BN, V_CONTIG, C::NT> v_reader(lds, v_row_of<C, GATED>(wn), lane);
+    const Reader<C::BM, U_CONTIG, C::MT> u_reader(lds + C::V_BYTES, wm * C::TM, lane);
+    auto read = [&](int slot, int h) {
 #pragma unroll
         for (int j = 0; j < C::NT; ++j)
-            vf[h][j] = read_side<C::BN, V_CONTIG>(st, vrow(j), h, lane);
+            vf[h][j] = v_reader.read(h, j, v_down<C, GATED>(j), slot * C::STAGE);
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
-            uf[h][i] = read_side<C::BM, U_CONTIG>(st + C::V_BYTES, wm * C::TM + i * 16, h, lane);
+            uf[h][i] = u_reader.read(h, i, i * 16, slot * C::STAGE);
     };
     auto multiply = [&](int h) {
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-            for (int j = 0; j < C::NT; ++j)
-                acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[h][j], uf[h][i], acc[j][i], 0, 0, 0);
-        if constexpr (BIAS)
-#pragma unroll
-            for (int i = 0; i < C::MT; ++i)
-                if (i / SUMS == wn)
-                    sums[i % SUMS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf[h][i], sums[i % SUMS], 0, 0, 0);
+            sums.template add<BIAS>(i, wn, vf[h], uf[h][i]);
         // a read beside every few products
         constexpr int READS = C::NT * (V_CONTIG ? 1 : 2) + C::MT * (U_CONTIG ? 1 : 2);
         constexpr int EACH = C::NT * C::MT / READS > 0 ? C::NT * C::MT / READS : 1;
@@ -530,18 +677,18 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
             meet<(C::S - 1) * C::LOADS>();
         else
             meet<0>();
-        read(lds, 0);
+        read(0, 0);
     }
     int slot = 0;
     auto step_of = [&](int step, auto steady, auto tail) {
         uint8_t* st = lds + slot * C::STAGE;
-        read(st, 1);
+        read(slot, 1);
         multiply(0);
         meet<decltype(steady)::value ? (C::S - 2) * C::LOADS : 0>();
         if constexpr (decltype(steady)::value)
             issue(step + C::S, st, tail);
         slot = slot + 1 == C::S ? 0 : slot + 1;
-        read(lds + slot * C::STAGE, 0);              // (past the last stage: stale, never used)
+        read(slot, 0);                               // (past the last stage: stale, never used)
         multiply(1);
     };
     int step = 0;
@@ -551,175 +698,168 @@ __device__ __forceinline__ void product_tile(const Side& us, const Side& vs, int
         step_of(step++, std::true_type{}, std::true_type{});
     for (; step < steps; ++step)
         step_of(step, std::false_type{}, std::false_type{});
-
-    hand_over<C, GATED, BIAS>(acc, sums, [&](int i) { return wm * C::TM + i * 16; }, vrow, wn, u_rows, v_rows, lane,
-                              finish, finish_bias);
 }
 
-// The same for the 256 x 256 tile, U in two halves of 128 rows, with V's
-// stages in three slots of LDS and each half of U's in two: 160 KB.  A step is
-// two phases, one for each half of U; a phase's operands are read while the
-// phase before it is multiplied, and what has been read by every wave is
-// loaded anew at once, so that a load has one and a half to two steps to
-// arrive (with two slots for everything, one step).
-template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
-__device__ __forceinline__ void product_tile_deep(const Side& us, const Side& vs, int64_t t0, int64_t t1, int u_rows,
-                                                  int v_rows, uint8_t* lds, Finish finish, FinishBias finish_bias)
-{
+// The 256 x 256 tile: U in two halves of 128 rows, V's stages in three slots of
+// LDS and each half of U's in two, 160 KB.  A step is two phases, one for each
+// half of U; a phase's operands are read while the phase before it is
+// multiplied, and what has been read by every wave is loaded anew at once, so
+// that a load has one and a half to two steps to arrive (with two slots for
+// everything, one step).  A phase issues four loads, one beside every eight
+// products: two of the half of U that the phase before it was the last to read,
+// and half of V's, whose slot was free before.
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED>
+struct DeepTile {
     static_assert(C::BM == 256 && C::BN == 256 && C::WM == 2 && C::WN == 4, "eight waves of 128 x 64");
-    constexpr int HALF = 128, HALF_BYTES = HALF * STEP * 2;
+    static constexpr int HALF = 128, HALF_BYTES = HALF * STEP * 2, UT = C::MT / 2;
+    static constexpr int V_LOADS = loads_of<C>(C::BN), U_LOADS = loads_of<C>(HALF), PHASE = V_LOADS / 2 + U_LOADS;
+    static_assert(V_LOADS == 4 && U_LOADS == 2 && C::NT == 4 && UT == 4, "the orders below");
+
+    uint8_t* lds;
+    int wave, lane, wm, wn;
+    __device__ inline DeepTile(uint8_t* l, int wave_, int lane_)
+        : lds(l), wave(wave_), lane(lane_), wm(wave_ % C::WM), wn(wave_ / C::WM)
+    {
+    }
+    __device__ inline uint8_t* v_slot(int s) const { return lds + s * C::V_BYTES; }
+    __device__ inline uint8_t* u_slot(int half, int step) const
+    {
+        return lds + 3 * C::V_BYTES + (half * 2 + (step & 1)) * HALF_BYTES;
+    }
+    // Nothing is loaded behind the last stage, whose tail is zeros; `inner`: it is not the last.
+    template <class Inner>
+    __device__ __forceinline__ void load_v(const Work& w, int steps, int step, int slot, Inner inner, int from, int to) const
+    {
+        if (inner || step < steps - 1)
+            load_side<C, C::BN, V_CONTIG, GATED, false>(w.vs, 0, step, v_slot(slot), wave, lane, from, to);
+        else if (step == steps - 1)
+            load_side<C, C::BN, V_CONTIG, GATED, true>(w.vs, 0, step, v_slot(slot), wave, lane, from, to);
+    }
+    template <class Inner>
+    __device__ __forceinline__ void load_u(const Work& w, int steps, int half, int step, Inner inner, int from, int to) const
+    {
+        uint8_t* const slot = u_slot(half, step);
+        if (inner || step < steps - 1)
+            load_side<C, HALF, U_CONTIG, false, false>(w.us, half * HALF, step, slot, wave, lane, from, to);
+        else if (step == steps - 1)
+            load_side<C, HALF, U_CONTIG, false, true>(w.us, half * HALF, step, slot, wave, lane, from, to);
+    }
+    // The first loads of a tile, in the order in which the phases issue theirs.
+    __device__ __forceinline__ void start(const Work& w) const
+    {
+        constexpr std::false_type any{};
+        const int steps = w.steps();
+        load_u(w, steps, 0, 0, any, 0, 2);
+        load_v(w, steps, 0, 0, any, 0, 4);
+        load_u(w, steps, 1, 0, any, 0, 2);
+        load_v(w, steps, 1, 1, any, 0, 2);
+        load_u(w, steps, 0, 1, any, 0, 2);
+        load_v(w, steps, 1, 1, any, 2, 4);
+        load_u(w, steps, 1, 1, any, 0, 2);
+        load_v(w, steps, 2, 2, any, 0, 2);
+    }
+    template <bool BIAS>
+    __device__ __forceinline__ void sum(const Work& w, Sums<C>& sums) const
+    {
+        constexpr std::false_type any{};
+        const int steps = w.steps();
+        v8b vf[2][C::NT], uf[2][2][UT];              // V: [k half]; U: [row half][k half]
+        Reader<C::BN, V_CONTIG, C::NT> v_reader(lds, v_row_of<C, GATED>(wn), lane);      // of this step's slot
+        Reader<HALF, U_CONTIG, UT> u_reader(u_slot(0, 0), wm * 64, lane);
+        auto read_v = [&](int h, int j) { vf[h][j] = v_reader.read(h, j, v_down<C, GATED>(j), 0); };
+        auto read_u = [&](int half, int h, int i) {
+            uf[half][h][i] = u_reader.read(h, i, i * 16, half * 2 * HALF_BYTES);
+        };
+        // Four products, behind the reads and loads before them.
+        auto products = [&](int half, int h, int i) {
+            sums.template add<BIAS>(half * UT + i, wn, vf[h], uf[half][h][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (steps >= 3)
+            meet<3 * PHASE>();
+        else
+            meet<0>();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            read_v(0, q);
+            read_u(0, 0, q);
+            read_u(0, 1, q);
+        }
+        if (steps >= 3)
+            meet<2 * PHASE>();
+        else
+            meet<0>();
+        int now = 0, last = 2;                       // V's slots of this step and the one before it
+        auto step_of = [&](int step, auto steady) {
+            // every wave has read the first half of U and V's first indices of this step
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q < 2) {
+                    read_v(1, 2 * q);
+                    read_v(1, 2 * q + 1);
+                } else if (q < 6) {
+                    read_u(1, (q - 2) / 2, (q & 1) * 2);
+                    read_u(1, (q - 2) / 2, (q & 1) * 2 + 1);
+                }
+                if (q == 0 || q == 2)
+                    load_u(w, steps, 0, step + 2, steady, q / 2, q / 2 + 1);
+                if (q == 4 || q == 6)
+                    load_v(w, steps, step + 2, last, steady, q / 2, q / 2 + 1);
+                products(0, q / 4, q % 4);
+            }
+            meet<steady ? 2 * PHASE : 0>();
+            // ... and V and the second half of U; what is read past the last stage is stale, and not used
+            last = now;
+            now = now == 2 ? 0 : now + 1;
+            v_reader.move(now ? C::V_BYTES : -2 * C::V_BYTES);
+            u_reader.move(step & 1 ? -HALF_BYTES : HALF_BYTES);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (q < 4) {
+                    read_u(0, q / 2, (q & 1) * 2);
+                    read_u(0, q / 2, (q & 1) * 2 + 1);
+                } else if (q < 6) {
+                    read_v(0, (q & 1) * 2);
+                    read_v(0, (q & 1) * 2 + 1);
+                }
+                if (q == 0 || q == 2)
+                    load_u(w, steps, 1, step + 2, steady, q / 2, q / 2 + 1);
+                if (q == 4 || q == 6)
+                    load_v(w, steps, step + 3, last, steady, q / 2 - 2, q / 2 - 1);
+                products(1, q / 4, q % 4);
+            }
+            meet<steady ? 2 * PHASE : 0>();
+        };
+        int step = 0;
+        for (; step + 3 < steps - 1; ++step)
+            step_of(step, std::true_type{});
+        for (; step < steps; ++step)
+            step_of(step, any);
+    }
+};
+
+// A workgroup's tile: tiles.next() describes it (false: there is none), and its
+// outputs go to tiles.finish().
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Tiles>
+__device__ __forceinline__ void run_tile(uint8_t* lds, Tiles& tiles)
+{
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    const int wm = wave % C::WM, wn = wave / C::WM;
-    const int steps = (int)((t1 - t0 + STEP - 1) / STEP);
-    const int last_left = (int)(t1 - t0) - (steps - 1) * STEP;
-    uint8_t* const u_lds = lds + 3 * C::V_BYTES;
-    auto v_slot = [&](int s) { return lds + s * C::V_BYTES; };
-    auto u_slot = [&](int half, int s) { return u_lds + (half * 2 + s) * HALF_BYTES; };
-    // Nothing is loaded behind the last stage, whose tail is zeros; `inner`: it is not the last.
-    auto load_v = [&](int step, int slot, auto inner, int from, int to) {
-        const int64_t t = t0 + (int64_t)step * STEP;
-        if (inner || step < steps - 1)
-            load_side<C, C::BN, V_CONTIG, GATED, false>(vs, 0, t, 0, v_slot(slot), wave, lane, from, to);
-        else if (step == steps - 1)
-            load_side<C, C::BN, V_CONTIG, GATED, true>(vs, 0, t, last_left, v_slot(slot), wave, lane, from, to);
-    };
-    auto load_u = [&](int half, int step, auto inner, int from, int to) {
-        const int64_t t = t0 + (int64_t)step * STEP;
-        uint8_t* const slot = u_slot(half, step & 1);
-        if (inner || step < steps - 1)
-            load_side<C, HALF, U_CONTIG, false, false>(us, half * HALF, t, 0, slot, wave, lane, from, to);
-        else if (step == steps - 1)
-            load_side<C, HALF, U_CONTIG, false, true>(us, half * HALF, t, last_left, slot, wave, lane, from, to);
-    };
-    auto vrow = [&](int j) {
-        if (GATED) {
-            constexpr int GH = C::NT / 2;
-            return (j < GH ? 0 : C::BN / 2) + wn * (C::TN / 2) + j % GH * 16;
-        }
-        return wn * C::TN + j * 16;
-    };
-    constexpr int UT = C::MT / 2;                    // subtiles of a half
-    const v4f zero{0.0f, 0.0f, 0.0f, 0.0f};
-    v4f acc[C::NT][C::MT];
-#pragma unroll
-    for (int j = 0; j < C::NT; ++j)
-#pragma unroll
-        for (int i = 0; i < C::MT; ++i)
-            acc[j][i] = zero;
-    constexpr int SUMS = C::MT / C::WN;
-    v4f sums[SUMS];
-    v8b ones;
-    if constexpr (BIAS) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            ones[c] = (__bf16)1.0f;
-#pragma unroll
-        for (int i = 0; i < SUMS; ++i)
-            sums[i] = zero;
+    Work w;
+    if (!tiles.next(workgroup_id(), w))
+        return;
+    Sums<C> sums;
+    sums.clear();
+    if constexpr (C::DEEP) {
+        const DeepTile<C, U_CONTIG, V_CONTIG, GATED> tile(lds, wave, lane);
+        tile.start(w);
+        tile.template sum<BIAS>(w, sums);
+    } else {
+        sum_tile<C, U_CONTIG, V_CONTIG, GATED, BIAS>(w, lds, wave, lane, sums);
+        meet<0>();                                   // the last reads, before LDS is written again
     }
-    v8b vf[2][C::NT], uf[2][2][UT];                  // V: [k half]; U: [row half][k half]
-    auto read_v = [&](int slot, int h, int j) {
-        vf[h][j] = read_side<C::BN, V_CONTIG>(v_slot(slot), vrow(j), h, lane);
-    };
-    auto read_u = [&](int half, int slot, int h, int i) {
-        uf[half][h][i] = read_side<HALF, U_CONTIG>(u_slot(half, slot), wm * 64 + i * 16, h, lane);
-    };
-    // Four products, and the reads beside them, in this order.
-    auto products = [&](int half, int h, int i) {
-#pragma unroll
-        for (int j = 0; j < C::NT; ++j)
-            acc[j][half * UT + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[h][j], uf[half][h][i],
-                                                                           acc[j][half * UT + i], 0, 0, 0);
-        if constexpr (BIAS)
-            if ((half * UT + i) / SUMS == wn)
-                sums[i % SUMS] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, uf[half][h][i], sums[i % SUMS], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    static_assert(C::NT == 4 && UT == 4, "the order of reads below");
-    // A phase issues four loads, one beside every eight products: two of the half of U that the
-    // phase before it was the last to read, and half of V's, whose slot was free before.
-    constexpr int V_LOADS = loads_of<C>(C::BN), U_LOADS = loads_of<C>(HALF), PHASE = V_LOADS / 2 + U_LOADS;
-    static_assert(V_LOADS == 4 && U_LOADS == 2, "four loads per phase");
-    constexpr std::false_type any{};
-    load_u(0, 0, any, 0, 2);
-    load_v(0, 0, any, 0, 4);
-    load_u(1, 0, any, 0, 2);
-    load_v(1, 1, any, 0, 2);
-    load_u(0, 1, any, 0, 2);
-    load_v(1, 1, any, 2, 4);
-    load_u(1, 1, any, 0, 2);
-    load_v(2, 2, any, 0, 2);
-    if (steps >= 3)
-        meet<3 * PHASE>();
-    else
-        meet<0>();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        read_v(0, 0, q);
-        read_u(0, 0, 0, q);
-        read_u(0, 0, 1, q);
-    }
-    if (steps >= 3)
-        meet<2 * PHASE>();
-    else
-        meet<0>();
-    int now = 0, last = 2;                           // V's slots of this step and the one before it
-    auto step_of = [&](int step, auto steady) {
-        // every wave has read the first half of U and V's first indices of this step
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (q < 2) {
-                read_v(now, 1, 2 * q);
-                read_v(now, 1, 2 * q + 1);
-            } else if (q < 6) {
-                read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2);
-                read_u(1, step & 1, (q - 2) / 2, (q & 1) * 2 + 1);
-            }
-            if (q == 0 || q == 2)
-                load_u(0, step + 2, steady, q / 2, q / 2 + 1);
-            if (q == 4 || q == 6)
-                load_v(step + 2, last, steady, q / 2, q / 2 + 1);
-            products(0, q / 4, q % 4);
-        }
-        meet<steady ? 2 * PHASE : 0>();
-        // ... and V and the second half of U; what is read past the last stage is stale, and not used
-        last = now;
-        now = now == 2 ? 0 : now + 1;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (q < 4) {
-                read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2);
-                read_u(0, (step + 1) & 1, q / 2, (q & 1) * 2 + 1);
-            } else if (q < 6) {
-                read_v(now, 0, (q & 1) * 2);
-                read_v(now, 0, (q & 1) * 2 + 1);
-            }
-            if (q == 0 || q == 2)
-                load_u(1, step + 2, steady, q / 2, q / 2 + 1);
-            if (q == 4 || q == 6)
-                load_v(step + 3, last, steady, q / 2 - 2, q / 2 - 1);
-            products(1, q / 4, q % 4);
-        }
-        meet<steady ? 2 * PHASE : 0>();
-    };
-    int step = 0;
-    for (; step + 3 < steps - 1; ++step)
-        step_of(step, std::true_type{});
-    for (; step < steps; ++step)
-        step_of(step, any);
-    hand_over<C, GATED, BIAS>(acc, sums, [&](int i) { return i / UT * HALF + wm * 64 + i % UT * 16; }, vrow, wn, u_rows,
-                              v_rows, lane, finish, finish_bias);
-}
-
-template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Finish, class FinishBias>
-__device__ __forceinline__ void run_tile(const Side& us, const Side& vs, int64_t t0, int64_t t1, int u_rows,
-                                         int v_rows, uint8_t* lds, Finish finish, FinishBias finish_bias)
-{
-    if constexpr (C::DEEP)
-        product_tile_deep<C, U_CONTIG, V_CONTIG, GATED, BIAS>(us, vs, t0, t1, u_rows, v_rows, lds, finish, finish_bias);
-    else
-        product_tile<C, U_CONTIG, V_CONTIG, GATED, BIAS>(us, vs, t0, t1, u_rows, v_rows, lds, finish, finish_bias);
+    tiles.begin_finish();
+    hand_over<C, GATED, BIAS>(sums, w.us.valid, w.vs.valid, lds, wave, anew(lane), tiles);
 }
 
 // The part of [0, steps * STEP) that split `s` of `splits` sums.
@@ -732,108 +872,161 @@ __device__ inline void split_range(int64_t total, int splits, int s, int64_t& t0
 
 // forward and grad_input: out rows are the token rows
 template <Kind KIND, class C, bool GATED>
+struct RowTiles {
+    static constexpr bool FWD = KIND == Kind::FORWARD;
+    int n_tiles, splits;
+    Place at;
+    const Linear* args;
+
+    // columns of an output row's sums, and those that tiles divide
+    static __device__ inline int width(const Linear& p) { return FWD ? p.n : p.k; }
+    static __device__ inline int f(const Linear& p) { return GATED ? p.n / 2 : width(p); }
+    static __device__ inline int first_col(const Place& a) { return a.n_tile * (GATED ? C::BN / 2 : C::BN); }
+    __device__ inline bool next(int64_t id, Work& w)
+    {
+        const Linear& p = arguments();
+        if (!find_rows<C::BM>(p, n_tiles, id, at))
+            return false;
+        const int v0 = first_col(at);
+        const int64_t total = FWD ? p.k : p.n;
+        w.us.ld = (int)total;
+        int64_t t0, t1;
+        split_range(total, splits, blockIdx.z, t0, t1);
+        w.us.base = w.us.upper = (FWD ? p.x : p.dz) + (int64_t)at.m0 * total + t0;
+        w.us.valid = at.rows;
+        const uint16_t* weights = p.w + (int64_t)at.e * p.n * p.k;
+        w.vs.ld = p.k;
+        w.vs.base = FWD ? weights + (int64_t)v0 * p.k + t0 : weights + t0 * p.k + v0;
+        w.vs.upper = GATED ? w.vs.base + (int64_t)f(p) * p.k : w.vs.base;
+        w.vs.valid = min(GATED ? C::BN / 2 : C::BN, f(p) - v0);
+        w.us.terms = w.vs.terms = (int)(t1 - t0);
+        return true;
+    }
+    __device__ inline void begin_finish() { args = &arguments(); }
+    __device__ inline Extra fetch(int u, int v) const
+    {
+        return splits > 1 ? Extra{} : Finish<KIND, GATED>(*args).fetch(at.m0 + u, first_col(at) + v);
+    }
+    __device__ inline void fetch_bias(int v, v4u (&bias)[2]) const
+    {
+        Finish<KIND, GATED>(*args).fetch_bias(at.e, first_col(at) + v, bias);
+    }
+    __device__ inline void finish(int u, int v, float (&a)[8], float (&b)[8], const Extra& e, const v4u (&bias)[2]) const
+    {
+        const Linear& p = *args;
+        const int64_t row = at.m0 + u;
+        const int col = first_col(at) + v;
+        if (splits > 1) {
+            float* part = (float*)p.workspace + ((int64_t)blockIdx.z * p.rows + row) * width(p) + col;
+            store8(part, a);
+            if (GATED)
+                store8(part + f(p), b);
+            return;
+        }
+        const Finish<KIND, GATED> whole(p);
+        whole(row, col, a, b, e, bias);
+    }
+    __device__ inline void finish_bias(int, float) const {}
+};
+
+template <Kind KIND, class C, bool GATED>
 __global__ __launch_bounds__(C::THREADS) void linear_kernel(const Linear p, int n_tiles, int splits)
 {
     extern __shared__ __align__(1024) uint8_t lds[];
-    constexpr bool FWD = KIND == Kind::FORWARD;
-    Place at;
-    if (!find_rows<C::BM>(p, n_tiles, at))
-        return;
-    at.e = __builtin_amdgcn_readfirstlane(at.e);             // (uniform already, which the compiler cannot tell)
-    at.m0 = __builtin_amdgcn_readfirstlane(at.m0);
-    at.rows = __builtin_amdgcn_readfirstlane(at.rows);
-    at.n_tile = __builtin_amdgcn_readfirstlane(at.n_tile);
-    const int width = FWD ? p.n : p.k;                       // output columns
-    const int f = GATED ? p.n / 2 : width;                   // columns that tiles divide
-    const int v0 = at.n_tile * (GATED ? C::BN / 2 : C::BN);
-    const int64_t total = FWD ? p.k : p.n;
-    Side us, vs;
-    us.ld = (int)total;
-    us.base = (FWD ? p.x : p.dz) + (int64_t)at.m0 * total;
-    us.upper = us.base;
-    us.last = at.rows - 1;
-    const uint16_t* w = p.w + (int64_t)at.e * p.n * p.k;
-    vs.ld = p.k;
-    vs.base = FWD ? w + (int64_t)v0 * p.k : w + v0;
-    vs.upper = GATED ? vs.base + (int64_t)f * p.k : vs.base;
-    vs.last = min(GATED ? C::BN / 2 : C::BN, f - v0) - 1;
-    int64_t t0, t1;
-    split_range(total, splits, blockIdx.z, t0, t1);
-    float* part = (float*)p.workspace + (int64_t)blockIdx.z * p.rows * width;
-    auto finish = [&](int u, int v, float(&a)[8], float(&b)[8]) {
-        const int64_t row = at.m0 + u;
-            const int col = v0 + v;
-            if (splits > 1) {
-                store8(part + row * width + col, a);
-                if (GATED)
-                    store8(part + row * width + f + col, b);
-            } else if (GATED) {
-                finish_gated(p, at.e, row, col, a, b);
-            } else if (FWD) {
-                finish_forward(p, at.e, row, col, a);
-            } else {
-                finish_input(p, row, col, a);
-            }
-        };
-    run_tile<C, true, FWD, GATED, false>(us, vs, t0, t1, at.rows, vs.last + 1, lds, finish, [](int, float) {});
+    RowTiles<KIND, C, GATED> tiles{n_tiles, splits};
+    run_tile<C, true, KIND == Kind::FORWARD, GATED, false>(lds, tiles);
 }
 
 // grad_weight: out rows are an expert's weight rows
 template <class C>
+struct WeightTiles {
+    int m_tiles, n_tiles, splits;
+    struct Spot {
+        int e, m, n;
+    } at;
+    const Linear* args;
+
+    __device__ inline bool next(int64_t id, Work& w)
+    {
+        const Linear& p = arguments();
+        int64_t t;
+        if (!tile_of_workgroup(id, (int64_t)p.E * m_tiles * n_tiles, t))
+            return false;
+        const int per = m_tiles * n_tiles;                   // 2^16 at most
+        at.e = (int)(t / per);
+        tile_in_group(t - (int64_t)at.e * per, m_tiles, n_tiles, at.m, at.n);
+        int64_t a, b;
+        expert_rows(p, at.e, a, b);
+        a = __builtin_amdgcn_readfirstlane((int)a);          // (uniform already, which the compiler cannot tell)
+        b = __builtin_amdgcn_readfirstlane((int)b);
+        const int u0 = at.m * C::BM, v0 = at.n * C::BN;
+        int64_t t0, t1;
+        split_range(b - a, splits, blockIdx.z, t0, t1);
+        w.us.ld = p.n;
+        w.us.base = w.us.upper = p.dz + (a + t0) * p.n + u0;
+        w.us.valid = min(C::BM, p.n - u0);
+        w.vs.ld = p.k;
+        w.vs.base = w.vs.upper = p.x + (a + t0) * p.k + v0;
+        w.vs.valid = min(C::BN, p.k - v0);
+        w.us.terms = w.vs.terms = (int)(t1 - t0);
+        return true;
+    }
+    __device__ inline void begin_finish() { args = &arguments(); }
+    __device__ inline Extra fetch(int, int) const { return Extra{}; }
+    __device__ inline void fetch_bias(int, v4u (&)[2]) const {}
+    __device__ inline void finish(int u, int v, float (&o)[8], float (&)[8], const Extra&, const v4u (&)[2]) const
+    {
+        const Linear& p = *args;
+        const int64_t i = ((int64_t)at.e * p.n + at.m * C::BM + u) * p.k + at.n * C::BN + v;
+        if (splits > 1)
+            store8((float*)p.workspace + (int64_t)blockIdx.z * p.E * p.n * p.k + i, o);
+        else
+            store_out(p, i, o);
+    }
+    __device__ inline void finish_bias(int u, float s) const
+    {
+        if (at.n > 0)                                        // every tile has the sums, the first one hands them on
+            return;
+        const Linear& p = *args;
+        const int64_t biases = (int64_t)p.E * p.n;
+        float* out = p.dbias;
+        if (splits > 1)
+            out = (float*)p.workspace + splits * biases * p.k + blockIdx.z * biases;
+        out[(int64_t)at.e * p.n + at.m * C::BM + u] = s;
+    }
+};
+
+template <class C, bool BIAS>
 __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear p, int m_tiles, int n_tiles, int splits)
 {
     extern __shared__ __align__(1024) uint8_t lds[];
-    int64_t t;
-    if (!tile_of_workgroup((int64_t)p.E * m_tiles * n_tiles, t))
-        return;
-    const int e = (int)(t / ((int64_t)m_tiles * n_tiles));
-    int m, n;
-    tile_in_group(t - (int64_t)e * m_tiles * n_tiles, m_tiles, n_tiles, m, n);
-    int64_t a, b;
-    expert_rows(p, e, a, b);
-    a = __builtin_amdgcn_readfirstlane((int)a);              // (uniform already, which the compiler cannot tell)
-    b = __builtin_amdgcn_readfirstlane((int)b);
-    const int u0 = m * C::BM, v0 = n * C::BN;
-    Side us, vs;
-    us.ld = p.n;
-    us.base = us.upper = p.dz + a * p.n + u0;
-    us.last = min(C::BM, p.n - u0) - 1;
-    vs.ld = p.k;
-    vs.base = vs.upper = p.x + a * p.k + v0;
-    vs.last = min(C::BN, p.k - v0) - 1;
-    int64_t t0, t1;
-    split_range(b - a, splits, blockIdx.z, t0, t1);
-    const int64_t weights = (int64_t)p.E * p.n * p.k;
-    float* part = (float*)p.workspace + (int64_t)blockIdx.z * weights;
-    float* part_b = (float*)p.workspace + (int64_t)splits * weights + (int64_t)blockIdx.z * p.E * p.n;
-    auto finish = [&](int u, int v, float(&o)[8], float(&)[8]) {
-        const int64_t at = ((int64_t)e * p.n + u0 + u) * p.k + v0 + v;
-        if (splits > 1)
-            store8(part + at, o);
-        else
-            store_out(p, at, o);
-    };
-    auto finish_bias = [&](int u, float s) { (splits > 1 ? part_b : p.dbias)[(int64_t)e * p.n + u0 + u] = s; };
-    if (p.dbias && n == 0)
-        run_tile<C, false, false, false, true>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
-    else
-        run_tile<C, false, false, false, false>(us, vs, t0, t1, us.last + 1, vs.last + 1, lds, finish, finish_bias);
+    WeightTiles<C> tiles{m_tiles, n_tiles, splits};
+    run_tile<C, false, false, false, BIAS>(lds, tiles);
 }
 
 // --- joins of split sums -----------------------------------------------------------------------
 
+// The sum of eight neighbours over the splits, in their order, four splits in flight.
 __device__ inline void add_parts(const float* part, int64_t stride, int splits, float (&v)[8])
 {
+    constexpr int AHEAD = 4;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
         v[c] = 0.0f;
-    for (int s = 0; s < splits; ++s, part += stride) {
-        const v4f a = ((const v4f*)part)[0], b = ((const v4f*)part)[1];
+    for (int s = 0; s < splits; s += AHEAD) {
+        v4f a[AHEAD][2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            v[c] += a[c];
-            v[4 + c] += b[c];
+        for (int q = 0; q < AHEAD; ++q) {
+            const v4f* at = (const v4f*)(part + min(s + q, splits - 1) * stride);
+            a[q][0] = at[0];
+            a[q][1] = at[1];
         }
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+            if (s + q < splits)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    v[c] += a[q][c / 4][c % 4];
     }
 }
 
@@ -879,19 +1072,17 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const Linear p, int spli
     place_of_eight(p.rows, f, row, col);
     if (row >= p.rows || !expert_of(p, row, e))
         return;
+    const Finish<KIND, GATED> finish(p);
+    const Extra extra = finish.fetch(row, col);
+    v4u bias[2];
+    finish.fetch_bias(e, col, bias);
     const int64_t stride = p.rows * width;
     const float* part = (const float*)p.workspace + row * width + col;
-    float a[8];
+    float a[8], b[8];
     add_parts(part, stride, splits, a);
-    if constexpr (GATED) {
-        float b[8];
+    if (GATED)
         add_parts(part + f, stride, splits, b);
-        finish_gated(p, e, row, col, a, b);
-    } else if constexpr (KIND == Kind::FORWARD) {
-        finish_forward(p, e, row, col, a);
-    } else {
-        finish_input(p, row, col, a);
-    }
+    finish(row, col, a, b, extra, bias);
 }
 
 __global__ __launch_bounds__(256) void join_weight_kernel(const Linear p, int splits)
@@ -942,12 +1133,12 @@ __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, co
         return;
     constexpr float ERR = 0x1p-21f;
     float d[8], z[8], v[8];
-    open8(dy + row * f + col, d);
+    open8(load8(dy + row * f + col), d);
     uint16_t* out = (uint16_t*)p.out + row * p.n + col;
-    open8(p.z_in + row * p.n + col, z);
+    open8(load8(p.z_in + row * p.n + col), z);
     if (p.act == MOE_ACT_SWIGLU) {
         float u[8], w[8];
-        open8(p.z_in + row * p.n + f + col, u);
+        open8(load8(p.z_in + row * p.n + f + col), u);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const float g = d[c] * u[c];
@@ -963,8 +1154,12 @@ __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, co
         return;
     }
 #pragma unroll
+    for (int c = 0; c < 8; ++c)
+        v[c] = z[c];
+    slopes8(p.act, v);
+#pragma unroll
     for (int c = 0; c < 8; ++c) {
-        v[c] = d[c] * slope(p.act, z[c]);
+        v[c] *= d[c];
         if (p.act != MOE_ACT_RELU && near_border(v[c], ERR * fabsf(d[c])))
             v[c] = (float)(d[c] * slope64(p.act, z[c]));
     }
@@ -992,47 +1187,80 @@ hipError_t allow_lds(K kernel, std::atomic<uint64_t>& allowed)
 
 dim3 blocks_of(int64_t threads) { return grid_of((threads + 255) / 256); }
 
-// Splits of a sum of `total` terms where a launch has `groups` workgroups.
-int splits_of(int64_t groups, int64_t total)
+// The tiles of a launch, from high to low.
+enum class Form { T256, T128W, T128, T64, T32W, T32, COUNT };
+
+template <Form F>
+struct Tile;
+template <>
+struct Tile<Form::T256> : Block<256, 256, 2, 4, 2> {};
+template <>
+struct Tile<Form::T128W> : Block<128, 256, 2, 4, 3> {};
+template <>
+struct Tile<Form::T128> : Block<128, 128, 2, 2, 2> {};
+template <>
+struct Tile<Form::T64> : Block<64, 128, 2, 2, 3> {};
+template <>
+struct Tile<Form::T32W> : Block<32, 256, 2, 4, 2> {};
+template <>
+struct Tile<Form::T32> : Block<32, 128, 2, 2, 4> {};
+
+template <class F>
+auto with_tile(Form form, F f)
 {
-    const int64_t steps = (total + STEP - 1) / STEP;
-    if (groups > 128 || steps < 8)
-        return 1;
-    return (int)std::max<int64_t>(std::min<int64_t>({256 / groups, steps / 4, 32}), 1);
+    switch (form) {
+    case Form::T256: return f(Tile<Form::T256>{});
+    case Form::T128W: return f(Tile<Form::T128W>{});
+    case Form::T128: return f(Tile<Form::T128>{});
+    case Form::T64: return f(Tile<Form::T64>{});
+    case Form::T32W: return f(Tile<Form::T32W>{});
+    default: return f(Tile<Form::T32>{});
+    }
 }
 
-typedef Block<256, 256, 2, 4, 2> Rows256;
-typedef Block<32, 256, 2, 4, 2> Rows32;
-typedef Block<256, 256, 2, 4, 2> Weights256;
-
-struct Shape {
-    bool low;                 // the lower tile
-    int n_tiles, splits;
+struct Plan {
+    Form form;
+    int m_tiles, n_tiles;     // m_tiles: of grad_weight
+    int64_t groups;
+    int splits;
 };
 
-Shape rows_shape(Kind kind, bool gated, int64_t rows, int E, int n, int k)
+void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, int n, int k)
 {
-    Shape s;
-    const int width = kind == Kind::FORWARD ? n : k;
-    s.n_tiles = gated ? (width / 2 + 127) / 128 : (width + 255) / 256;
-    s.low = rows / E <= 48;
-    s.splits = splits_of(workgroups(rows, E, s.low ? Rows32::BM : Rows256::BM, s.n_tiles), kind == Kind::FORWARD ? k : n);
+    s.form = form;
+    with_tile(form, [&](auto c) {
+        typedef decltype(c) C;
+        const int width = kind == Kind::FORWARD ? n : k, bn = gated ? C::BN / 2 : C::BN;
+        s.n_tiles = ((gated ? width / 2 : width) + bn - 1) / bn;
+        s.m_tiles = (n + C::BM - 1) / C::BM;
+        s.groups = kind == Kind::WEIGHT ? ((int64_t)E * s.m_tiles * s.n_tiles + 7) / 8 * 8
+                                        : workgroups(rows, E, C::BM, s.n_tiles);
+    });
+}
+
+Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
+{
+    Plan s{};
+    const int64_t total = kind == Kind::FORWARD ? k : kind == Kind::INPUT ? n : rows / E;
+    const int64_t steps = (total + STEP - 1) / STEP;
+    set_tiles(s, kind == Kind::WEIGHT || rows / E > 48 ? Form::T256 : Form::T32W, kind, gated, rows, E, n, k);
+    s.splits = 1;
+    if (s.groups <= 128 && steps >= 8)
+        s.splits = (int)std::max<int64_t>(std::min<int64_t>({256 / s.groups, steps / 4, 32}), 1);
     return s;
 }
 
-int weight_splits(int64_t rows, int E, int n, int k)
-{
-    return splits_of((int64_t)E * ((n + 255) / 256) * ((k + 255) / 256), rows / E);
-}
+// Fp32 partial sums of a call whose sums are split.
+size_t parts(const Plan& s, int64_t outputs) { return s.splits > 1 ? (size_t)s.splits * outputs * 4 : 0; }
 
 template <Kind KIND, bool GATED, class C>
-hipError_t launch_rows(const Linear& p, const Shape& s, hipStream_t stream)
+hipError_t launch_rows(const Linear& p, const Plan& s, hipStream_t stream)
 {
     static std::atomic<uint64_t> allowed{0};
     const hipError_t e = allow_lds(linear_kernel<KIND, C, GATED>, allowed);
     if (e != hipSuccess)
         return e;
-    dim3 grid = grid_of(workgroups(p.rows, p.E, C::BM, s.n_tiles));
+    dim3 grid = grid_of(s.groups);
     grid.z = s.splits;
     linear_kernel<KIND, C, GATED><<<grid, dim3(C::THREADS), C::LDS, stream>>>(p, s.n_tiles, s.splits);
     return hipGetLastError();
@@ -1041,9 +1269,9 @@ hipError_t launch_rows(const Linear& p, const Shape& s, hipStream_t stream)
 template <Kind KIND, bool GATED>
 hipError_t launch_rows(const Linear& p, hipStream_t stream)
 {
-    const Shape s = rows_shape(KIND, GATED, p.rows, p.E, p.n, p.k);
-    const hipError_t e = s.low ? launch_rows<KIND, GATED, Rows32>(p, s, stream)
-                               : launch_rows<KIND, GATED, Rows256>(p, s, stream);
+    const Plan s = plan_of(KIND, GATED, p.rows, p.E, p.n, p.k);
+    const hipError_t e =
+        with_tile(s.form, [&](auto c) { return launch_rows<KIND, GATED, decltype(c)>(p, s, stream); });
     if (e != hipSuccess || s.splits == 1)
         return e;
     const int width = KIND == Kind::FORWARD ? p.n : p.k;
@@ -1052,19 +1280,30 @@ hipError_t launch_rows(const Linear& p, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <class C, bool BIAS>
+hipError_t launch_weight(const Linear& p, const Plan& s, hipStream_t stream)
+{
+    static std::atomic<uint64_t> allowed{0};
+    const hipError_t e = allow_lds(linear_weight_kernel<C, BIAS>, allowed);
+    if (e != hipSuccess)
+        return e;
+    dim3 grid = grid_of(s.groups);
+    grid.z = s.splits;
+    linear_weight_kernel<C, BIAS><<<grid, dim3(C::THREADS), C::LDS, stream>>>(p, s.m_tiles, s.n_tiles, s.splits);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t linear_workspace(int64_t rows, int E, int n, int k)
 {
-    size_t most = 0;
-    for (int gated = 0; gated < 2; ++gated) {
-        const int s = rows_shape(Kind::FORWARD, gated, rows, E, n, k).splits;
-        most = std::max(most, s > 1 ? (size_t)s * rows * n * 4 : 0);
-    }
-    const int si = rows_shape(Kind::INPUT, false, rows, E, n, k).splits;
-    most = std::max(most, si > 1 ? (size_t)si * rows * k * 4 : 0);
-    const int sw = weight_splits(rows, E, n, k);
-    return std::max(most, sw > 1 ? (size_t)sw * E * n * (k + 1) * 4 : 0);
+    const int64_t weights = (int64_t)E * n * (k + 1);
+    size_t most = parts(plan_of(Kind::WEIGHT, false, rows, E, n, k), weights);
+    most = std::max(most, parts(plan_of(Kind::INPUT, false, rows, E, n, k), rows * k));
+    most = std::max(most, parts(plan_of(Kind::FORWARD, false, rows, E, n, k), rows * n));
+    if (n % 16 == 0)
+        most = std::max(most, parts(plan_of(Kind::FORWARD, true, rows, E, n, k), rows * n));
+    return most;
 }
 
 hipError_t launch_linear(const Linear& p, hipStream_t stream)
@@ -1080,18 +1319,13 @@ hipError_t launch_linear_grad_input(const Linear& p, hipStream_t stream)
 
 hipError_t launch_linear_grad_weight(const Linear& p, hipStream_t stream)
 {
-    typedef Weights256 C;
-    const int m_tiles = (p.n + C::BM - 1) / C::BM, n_tiles = (p.k + C::BN - 1) / C::BN;
-    const int splits = weight_splits(p.rows, p.E, p.n, p.k);
-    static std::atomic<uint64_t> allowed{0};
-    const hipError_t e = allow_lds(linear_weight_kernel<C>, allowed);
-    if (e != hipSuccess)
+    const Plan s = plan_of(Kind::WEIGHT, false, p.rows, p.E, p.n, p.k);
+    const hipError_t e = with_tile(s.form, [&](auto c) {
+        return p.dbias ? launch_weight<decltype(c), true>(p, s, stream) : launch_weight<decltype(c), false>(p, s, stream);
+    });
+    if (e != hipSuccess || s.splits == 1)
         return e;
-    dim3 grid = grid_of(((int64_t)p.E * m_tiles * n_tiles + 7) / 8 * 8);
-    grid.z = splits;
-    linear_weight_kernel<C><<<grid, dim3(C::THREADS), C::LDS, stream>>>(p, m_tiles, n_tiles, splits);
-    if (splits > 1)
-        join_weight_kernel<<<blocks_of(((int64_t)p.E * p.n * p.k + 7) / 8), dim3(256), 0, stream>>>(p, splits);
+    join_weight_kernel<<<blocks_of(((int64_t)p.E * p.n * p.k + 7) / 8), dim3(256), 0, stream>>>(p, s.splits);
     return hipGetLastError();
 }
 

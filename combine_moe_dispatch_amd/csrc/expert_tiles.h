@@ -42,15 +42,17 @@ struct Place {
     int n_tile;
 };
 
+// Workgroups of a launch are numbered over both grid dimensions.
+__device__ inline int64_t workgroup_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Tile t of the launch: experts in order, each expert's tiles in groups of up
 // to 8 row tiles, row tiles fastest inside a group.  Every wave finds it for
 // itself: lane l holds experts [l*per, (l+1)*per), PER >= per of them in
 // registers, so that one trip to memory is enough.
 template <int BM, int PER>
 __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int64_t rows_max, int n_tiles,
-                                 Place& out)
+                                 Place& out, int64_t id = workgroup_id(), int lane = threadIdx.x & (WAVE - 1))
 {
-    const int lane = threadIdx.x & (WAVE - 1);
     const int per = (E + WAVE - 1) / WAVE;
     const int rmax = (int)rows_max;
     int o[PER + 1];
@@ -69,7 +71,6 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     // consecutive workgroups go to the 8 XCDs in turn: each XCD takes one
     // contiguous run of tiles, so that the tiles sharing weights share its L2
     const int64_t per_xcd = (tiles + 7) / 8;
-    const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int64_t at = id >> 3;
     const int64_t t = (id & 7) * per_xcd + at;
     if (at >= per_xcd || t >= tiles)
