@@ -14,6 +14,7 @@
 // LDS read.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "expert_tiles.h"
@@ -1193,7 +1194,7 @@ hipError_t allow_lds(K kernel, std::atomic<uint64_t>& allowed)
 dim3 blocks_of(int64_t threads) { return grid_of((threads + 255) / 256); }
 
 // The tiles of a launch, from high to low.
-enum class Form { T256, T128W, T128, T64, T32W, T32, COUNT };
+enum class Form { T256, T128W, T128, T64, T32W, T32 };
 
 template <Form F>
 struct Tile;
@@ -1243,15 +1244,77 @@ void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, i
     });
 }
 
+// The tile and the number of splits that an estimate of the launch's time finds
+// best: rounds of workgroups, each of its steps and of what a tile costs beside
+// them (finding it, its first loads, its outputs); a join where sums are split
+// (a second launch, the partial sums written and read); never less than the
+// bytes take.  Steps and tiles (us, all workgroups of a CU together) are fitted
+// to 80 measured shapes of all three products, from 1 to 32768 rows, 1 to 256
+// experts and 8 to 7168 columns, every tile and split of each (the choice was
+// 2.4% above the best of them in the mean, 20% at most).  Both sides of some
+// choices, us:
+//  - 256 x 256 against 128 x 256 and 128 x 128: 4096 x 4096 x 4096 109, 138,
+//    158; 16 experts, 32768 rows, 4096 x 2048 521, 565, 621; 64 experts of about
+//    128 rows, 2048 x 2048 184, 147, 154 (64 x 128: 157);
+//  - 64 x 128 against 128 x 128: one expert, 1000 rows, 4096 x 4096 41.5
+//    against 44.7 (256 x 256 in four splits 51.5); 64 experts of about 64 rows 127
+//    against 136;
+//  - 32 x 128 against 32 x 256: 64 experts of 4 rows, 4096 x 2048 167 against 164,
+//    one expert, 1000 rows, 512 x 512 6.8 against 7.6; against 64 x 128: 8 experts
+//    of about 37 rows, 1000 x 384, to the input 9.3 against 10.6;
+//  - splits: 128 rows, 256 x 7168 in 1, 4, 8, 16 splits 20, 13.8, 11.1, 11.6; 64
+//    rows, 4096 x 4096 in 1, 2, 4, 8 24, 15.1, 13.0, 15.0.
+struct Cost {
+    Form form;
+    int bm, bn, per_cu;
+    float step, tile;
+};
+constexpr Cost COSTS[] = {
+    {Form::T256, 256, 256, 1, 1.50f, 6.8f}, {Form::T128W, 128, 256, 1, 0.95f, 4.0f},
+    {Form::T128, 128, 128, 2, 1.08f, 3.3f}, {Form::T64, 64, 128, 2, 0.61f, 2.65f},
+    {Form::T32W, 32, 256, 2, 0.93f, 1.83f}, {Form::T32, 32, 128, 2, 0.44f, 1.8f},
+};
+
 Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
 {
-    Plan s{};
+    const bool weight = kind == Kind::WEIGHT;
+    const int width = kind == Kind::FORWARD ? n : k;
+    const float used = (float)std::max<int64_t>(std::min<int64_t>(rows, E), 1);
     const int64_t total = kind == Kind::FORWARD ? k : kind == Kind::INPUT ? n : rows / E;
-    const int64_t steps = (total + STEP - 1) / STEP;
-    set_tiles(s, kind == Kind::WEIGHT || rows / E > 48 ? Form::T256 : Form::T32W, kind, gated, rows, E, n, k);
-    s.splits = 1;
-    if (s.groups <= 128 && steps >= 8)
-        s.splits = (int)std::max<int64_t>(std::min<int64_t>({256 / s.groups, steps / 4, 32}), 1);
+    const int steps = (int)std::max<int64_t>((total + STEP - 1) / STEP, 1);
+    const float outputs = weight ? (float)E * n * k : (float)rows * width;
+    const float bytes = 2.0f * ((weight ? (float)E : used) * n * k + (float)rows * n + (float)rows * k);
+    float best = 0.0f;
+    const Cost* form = nullptr;
+    int best_splits = 1;
+    for (const Cost& c : COSTS) {
+        const float across = (float)((width + c.bn - 1) / c.bn);
+        float tiles;
+        if (weight)
+            tiles = (float)E * ((n + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
+        else if (E == 1)
+            tiles = (float)((rows + c.bm - 1) / c.bm) * across;
+        else                                             // an expert's last tile is half full
+            tiles = std::max(used, (float)rows / c.bm + 0.5f * used) * across;
+        for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
+            const float load = tiles * splits / (256.0f * c.per_cu);
+            const bool counted = (weight || E == 1) && load <= 4.0f;
+            const float rounds = std::max(1.0f, counted ? std::ceil(load) : load + 0.5f);
+            const float step = load <= 0.5f ? 0.63f * c.step : c.step;       // a half empty chip's loads arrive sooner
+            float us = rounds * ((steps + splits - 1) / splits * step + c.tile);
+            if (splits > 1)
+                us += 2.9f + splits * outputs * 1e-6f;                       // 8 bytes at 8 TB/s
+            us = std::max(us, bytes / 5.94e6f) + 0.03f * us;
+            if (!form || us < best) {
+                best = us;
+                form = &c;
+                best_splits = splits;
+            }
+        }
+    }
+    Plan s{};
+    set_tiles(s, form->form, kind, gated, rows, E, n, k);
+    s.splits = best_splits;
     return s;
 }
 
@@ -1299,6 +1362,14 @@ hipError_t launch_weight(const Linear& p, const Plan& s, hipStream_t stream)
 }
 
 }  // namespace
+
+const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k, int* splits)
+{
+    const Plan s = plan_of((Kind)kind, gated, rows, E, n, k);
+    *splits = s.splits;
+    static const char* const names[] = {"256 x 256", "128 x 256", "128 x 128", "64 x 128", "32 x 256", "32 x 128"};
+    return names[(int)s.form];
+}
 
 size_t linear_workspace(int64_t rows, int E, int n, int k)
 {

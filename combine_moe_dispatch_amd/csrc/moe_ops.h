@@ -108,6 +108,9 @@ struct Linear {
     void* workspace;
 };
 
+// The tile and splits that a call takes (kind 0 the product, 1 the gradient to
+// its input, 2 to its weights), for the tests.
+const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k, int* splits);
 size_t linear_workspace(int64_t rows, int E, int n, int k);
 hipError_t launch_linear(const Linear& p, hipStream_t stream);
 hipError_t launch_linear_grad_input(const Linear& p, hipStream_t stream);

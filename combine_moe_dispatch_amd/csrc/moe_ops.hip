@@ -170,7 +170,7 @@ int moe_expert_gate_up(int32_t rows, int32_t num_experts, int32_t f, int32_t k, 
     return from_hip(moe::ops::launch_expert_gate_up(p, stream));
 }
 
-// These two are not part of the public ABI: which kernels a call takes (n: weight
+// These three are not part of the public ABI: which kernels a call takes (n: weight
 // rows per expert, 2f for gate_up), so that tests can say what they check; ""
 // for sizes that no call takes.
 const char* moe_ops_product_form(int32_t gate_up, int32_t rows, int32_t num_experts, int32_t n)
@@ -196,6 +196,14 @@ const char* moe_ops_few_token_form(int32_t num_tokens, int32_t num_experts, int3
     p.H = hidden;
     p.F = f;
     return moe::ops::few_token_form(p);
+}
+
+const char* moe_ops_linear_form(int32_t kind, int32_t gated, int32_t rows, int32_t num_experts, int32_t n, int32_t k,
+                                int32_t* splits)
+{
+    if (kind < 0 || kind > 2 || !linear_sizes(rows, num_experts, n, k) || (gated && (kind != 0 || n % 16 != 0)))
+        return "";
+    return moe::ops::linear_form(kind, gated != 0, rows, num_experts, n, k, splits);
 }
 
 size_t moe_few_token_workspace(int32_t num_tokens, int32_t top_k, int32_t hidden, int32_t f)
