@@ -1010,6 +1010,69 @@ __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear 
     run_tile<C, false, false, false, BIAS>(lds, tiles);
 }
 
+// grad_weight where an expert has a few rows: the weights' gradient is then what
+// costs, written once.  A lane has eight columns of x of FEW_ROWS rows in
+// registers, a wave goes through 8 weight rows at a time, whose dz are uniform;
+// a workgroup has 512 columns by 64 weight rows.  Against the 256 x 256 tile,
+// whose one step costs less than finding it, its first loads and its outputs, 64
+// experts, 4096 x 2048 (1.07 GB): 177 us against 281 with 1 row each, 231
+// against 286 with 4, 309 against 286 with 8, where the vector unit's
+// multiply-adds are what bounds it; of small gradients the latencies (16 experts
+// of 6 rows, 1000 x 384 14 us against 8).
+constexpr int FEW_ROWS = 8, FEW_COLS = 512, FEW_N = 64;
+constexpr int FEW_MEAN = 5;                      // rows per expert
+constexpr int64_t FEW_LEAST = 1 << 24;           // weights
+
+__global__ __launch_bounds__(256) void linear_weight_few_kernel(const Linear p, int n_chunks, int k_chunks)
+{
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    int64_t id = workgroup_id();
+    const int kc = (int)(id % k_chunks);
+    id /= k_chunks;
+    const int e = (int)(id / n_chunks), nc = (int)(id % n_chunks);
+    if (e >= p.E)
+        return;
+    int64_t a, b;
+    expert_rows(p, e, a, b);
+    const int col = kc * FEW_COLS + lane * 8;
+    const bool live = col < p.k;
+    constexpr int EACH = FEW_N / 4;                  // weight rows per wave
+#pragma unroll 1
+    for (int n0 = nc * FEW_N + wave * EACH; n0 < min(nc * FEW_N + (wave + 1) * EACH, p.n); n0 += 8) {
+        float acc[8][8] = {}, alone = 0.0f;
+#pragma unroll 1
+        for (int64_t r0 = a; r0 < b; r0 += FEW_ROWS) {
+            v4u x[FEW_ROWS];
+#pragma unroll
+            for (int r = 0; r < FEW_ROWS; ++r)
+                x[r] = live && r0 + r < b ? load8(p.x + (r0 + r) * p.k + col) : v4u{0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < FEW_ROWS; ++r)
+                if (r0 + r < b) {
+                    float d[8], v[8];
+                    open8(load8(p.dz + (r0 + r) * p.n + n0), d);
+                    open8(x[r], v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            acc[j][c] = fmaf(d[j], v[c], acc[j][c]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        alone += lane == j ? d[j] : 0.0f;
+                }
+        }
+        const int64_t at = (int64_t)e * p.n + n0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (live)
+                store_out(p, (at + j) * p.k + col, acc[j]);
+        if (p.dbias && kc == 0 && lane < 8)
+            p.dbias[at + lane] = alone;
+    }
+}
+
 // --- joins of split sums -----------------------------------------------------------------------
 
 // The sum of eight neighbours over the splits, in their order, four splits in flight.
@@ -1194,7 +1257,7 @@ hipError_t allow_lds(K kernel, std::atomic<uint64_t>& allowed)
 dim3 blocks_of(int64_t threads) { return grid_of((threads + 255) / 256); }
 
 // The tiles of a launch, from high to low.
-enum class Form { T256, T128W, T128, T64, T32W, T32 };
+enum class Form { T256, T128W, T128, T64, T32W, T32, FEW };
 
 template <Form F>
 struct Tile;
@@ -1249,9 +1312,9 @@ void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, i
 // them (finding it, its first loads, its outputs); a join where sums are split
 // (a second launch, the partial sums written and read); never less than the
 // bytes take.  Steps and tiles (us, all workgroups of a CU together) are fitted
-// to 80 measured shapes of all three products, from 1 to 32768 rows, 1 to 256
+// to 120 measured shapes of all three products, from 1 to 32768 rows, 1 to 256
 // experts and 8 to 7168 columns, every tile and split of each (the choice was
-// 2.4% above the best of them in the mean, 20% at most).  Both sides of some
+// 2.2% above the best of them in the mean, 28% at most).  Both sides of some
 // choices, us:
 //  - 256 x 256 against 128 x 256 and 128 x 128: 4096 x 4096 x 4096 109, 138,
 //    158; 16 experts, 32768 rows, 4096 x 2048 521, 565, 621; 64 experts of about
@@ -1270,14 +1333,23 @@ struct Cost {
     float step, tile;
 };
 constexpr Cost COSTS[] = {
-    {Form::T256, 256, 256, 1, 1.50f, 6.8f}, {Form::T128W, 128, 256, 1, 0.95f, 4.0f},
-    {Form::T128, 128, 128, 2, 1.08f, 3.3f}, {Form::T64, 64, 128, 2, 0.61f, 2.65f},
-    {Form::T32W, 32, 256, 2, 0.93f, 1.83f}, {Form::T32, 32, 128, 2, 0.44f, 1.8f},
+    {Form::T256, 256, 256, 1, 1.53f, 6.5f}, {Form::T128W, 128, 256, 1, 0.89f, 4.9f},
+    {Form::T128, 128, 128, 2, 1.02f, 3.3f}, {Form::T64, 64, 128, 2, 0.58f, 2.7f},
+    {Form::T32W, 32, 256, 2, 0.94f, 1.7f},  {Form::T32, 32, 128, 2, 0.44f, 1.9f},
 };
 
 Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
 {
     const bool weight = kind == Kind::WEIGHT;
+    if (weight && rows <= (int64_t)FEW_MEAN * E && k >= FEW_COLS / 2 && (int64_t)E * n * k >= FEW_LEAST) {
+        Plan few{};
+        few.form = Form::FEW;
+        few.m_tiles = (n + FEW_N - 1) / FEW_N;
+        few.n_tiles = (k + FEW_COLS - 1) / FEW_COLS;
+        few.groups = (int64_t)E * few.m_tiles * few.n_tiles;
+        few.splits = 1;
+        return few;
+    }
     const int width = kind == Kind::FORWARD ? n : k;
     const float used = (float)std::max<int64_t>(std::min<int64_t>(rows, E), 1);
     const int64_t total = kind == Kind::FORWARD ? k : kind == Kind::INPUT ? n : rows / E;
@@ -1299,12 +1371,13 @@ Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
         for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
             const float load = tiles * splits / (256.0f * c.per_cu);
             const bool counted = (weight || E == 1) && load <= 4.0f;
-            const float rounds = std::max(1.0f, counted ? std::ceil(load) : load + 0.5f);
-            const float step = load <= 0.5f ? 0.63f * c.step : c.step;       // a half empty chip's loads arrive sooner
+            const float rounds =
+                std::max(1.0f, counted ? std::ceil(load) : load <= 3.0f ? std::ceil(1.05f * load) : load + 0.5f);
+            const float step = load <= 0.5f ? 0.64f * c.step : c.step;       // a half empty chip's loads arrive sooner
             float us = rounds * ((steps + splits - 1) / splits * step + c.tile);
             if (splits > 1)
                 us += 2.9f + splits * outputs * 1e-6f;                       // 8 bytes at 8 TB/s
-            us = std::max(us, bytes / 5.94e6f) + 0.03f * us;
+            us = std::max(us, bytes / 6.05e6f) + 0.03f * us;
             if (!form || us < best) {
                 best = us;
                 form = &c;
@@ -1367,7 +1440,7 @@ const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k,
 {
     const Plan s = plan_of((Kind)kind, gated, rows, E, n, k);
     *splits = s.splits;
-    static const char* const names[] = {"256 x 256", "128 x 256", "128 x 128", "64 x 128", "32 x 256", "32 x 128"};
+    static const char* const names[] = {"256 x 256", "128 x 256", "128 x 128", "64 x 128", "32 x 256", "32 x 128", "few rows"};
     return names[(int)s.form];
 }
 
@@ -1396,6 +1469,10 @@ hipError_t launch_linear_grad_input(const Linear& p, hipStream_t stream)
 hipError_t launch_linear_grad_weight(const Linear& p, hipStream_t stream)
 {
     const Plan s = plan_of(Kind::WEIGHT, false, p.rows, p.E, p.n, p.k);
+    if (s.form == Form::FEW) {
+        linear_weight_few_kernel<<<grid_of(s.groups), dim3(256), 0, stream>>>(p, s.m_tiles, s.n_tiles);
+        return hipGetLastError();
+    }
     const hipError_t e = with_tile(s.form, [&](auto c) {
         return p.dbias ? launch_weight<decltype(c), true>(p, s, stream) : launch_weight<decltype(c), false>(p, s, stream);
     });

@@ -402,3 +402,75 @@ def test_offsets_out_of_order():
         torch.cuda.synchronize()
         for t in (y[rows:], dx[rows:], dw[E:]):
             assert bool((t == 9).all())
+
+
+
+# (tile, splits, product / to the input / to the weights, gated, rows, E, n, k): every tile with
+# and without splits, long enough for its steady loop, most with a tail and ragged experts
+FORMS = [
+    ("128 x 128", 1, 0, 0, 2437, 2, 1632, 480), ("128 x 128", 8, 0, 0, 4191, 2, 16, 4432),
+    ("128 x 128", 1, 0, 1, 3393, 3, 1072, 472), ("128 x 128", 8, 0, 1, 4505, 5, 16, 4048),
+    ("128 x 128", 1, 1, 0, 3620, 3, 464, 1040), ("128 x 128", 8, 1, 0, 4237, 5, 3920, 8),
+    ("128 x 128", 1, 2, 0, 3847, 8, 2128, 144), ("128 x 256", 1, 0, 0, 3269, 1, 1168, 856),
+    ("128 x 256", 4, 0, 0, 4612, 2, 144, 3568), ("128 x 256", 1, 0, 1, 2186, 3, 1680, 880),
+    ("128 x 256", 4, 0, 1, 4365, 5, 144, 3976), ("128 x 256", 1, 1, 0, 4246, 5, 784, 920),
+    ("128 x 256", 4, 1, 0, 4092, 16, 3232, 136), ("128 x 256", 1, 2, 0, 4153, 5, 3792, 168),
+    ("128 x 256", 4, 2, 0, 4364, 1, 1216, 808), ("256 x 256", 1, 0, 0, 2159, 5, 3504, 480),
+    ("256 x 256", 1, 0, 1, 3083, 5, 2480, 464), ("256 x 256", 1, 1, 0, 4373, 3, 528, 1672),
+    ("256 x 256", 1, 2, 0, 3749, 8, 2912, 272), ("32 x 128", 1, 0, 0, 13, 2, 16, 472),
+    ("32 x 128", 8, 0, 0, 11, 2, 16, 3632), ("32 x 128", 1, 0, 1, 18, 2, 16, 456),
+    ("32 x 128", 8, 0, 1, 19, 2, 16, 3704), ("32 x 128", 1, 1, 0, 8, 2, 464, 8),
+    ("32 x 128", 8, 1, 0, 9, 2, 3616, 8), ("32 x 128", 1, 2, 0, 907, 2, 16, 8),
+    ("32 x 128", 8, 2, 0, 3641, 1, 16, 8), ("32 x 256", 1, 0, 0, 3951, 5, 400, 552),
+    ("32 x 256", 1, 0, 1, 1258, 5, 1424, 464), ("32 x 256", 1, 1, 0, 2672, 2, 464, 664),
+    ("32 x 256", 1, 2, 0, 4703, 8, 80, 4176), ("64 x 128", 1, 0, 0, 4172, 8, 160, 776),
+    ("64 x 128", 8, 0, 0, 2172, 3, 16, 3672), ("64 x 128", 1, 0, 1, 4193, 5, 144, 848),
+    ("64 x 128", 8, 0, 1, 1944, 2, 16, 4176), ("64 x 128", 1, 1, 0, 4456, 3, 736, 144),
+    ("64 x 128", 4, 1, 0, 3917, 3, 1904, 8), ("64 x 128", 1, 2, 0, 2370, 3, 2848, 8),
+    ("64 x 128", 4, 2, 0, 3888, 2, 2064, 8), ("few rows", 1, 2, 0, 30, 8, 2048, 1032),
+    ("few rows", 1, 2, 0, 19, 5, 4096, 1000), ("few rows", 1, 2, 0, 3, 1, 4104, 4096)]
+
+
+def form_of(kind, gated, rows, E, n, k):
+    import ctypes
+    splits = ctypes.c_int32(0)
+    fn = mep._lib.moe_ops_linear_form
+    fn.argtypes, fn.restype = [ctypes.c_int32] * 6 + [ctypes.POINTER(ctypes.c_int32)], ctypes.c_char_p
+    return fn(kind, gated, rows, E, n, k, ctypes.byref(splits)).decode(), splits.value
+
+
+@pytest.mark.parametrize("form,splits,kind,gated,rows,E,n,k", FORMS)
+def test_forms(form, splits, kind, gated, rows, E, n, k):
+    """Every tile and split on whole numbers, asked of the library by its name."""
+    say(f"[gpu] linear form {form} splits={splits} kind={kind} gated={gated} rows={rows} E={E} n={n} k={k}")
+    assert form_of(kind, gated, rows, E, n, k) == (form, splits)
+    g = gen(10, kind, gated, rows, E, n, k)
+    r = np.random.default_rng([17, rows, E])
+    b = [0] + np.cumsum(r.multinomial(rows - 3, r.dirichlet(np.full(E, 4.0)))).tolist()
+    used = b[-1]                                     # three rows behind the last expert's
+    off = offsets(b)
+    x, dz, w, ws = whole(g, rows, k), whole(g, rows, n), whole(g, E, n, k), space(rows, E, n, k)
+    x[used:] = dz[used:] = float("nan")
+    if kind == 0 and gated:
+        z, y = torch.full((rows, n), 9.0, device=DEV, dtype=BF16), torch.full((rows, n // 2), 9.0, device=DEV, dtype=BF16)
+        mep.moe_expert_linear(rows, E, n, k, x, off, w, None, 4, None, z, y, mep.MOE_BF16, ws)
+        s = grouped(x, w, b, lambda a, v: a @ v.T)
+        assert torch.equal(z[:used], s.to(BF16)) and bool((z[used:] == 9).all()) and bool((y[used:] == 9).all())
+        want = value64("swiglu", s)
+        assert bool(((y[:used].double() - want).abs() <= (HALF[BF16] + EPI) * want.abs() + 1e-30).all())
+    elif kind == 0:
+        y = torch.full((rows, n), 9.0, device=DEV)
+        mep.moe_expert_linear(rows, E, n, k, x, off, w, None, 0, None, None, y, mep.MOE_FP32, ws)
+        assert torch.equal(y[:used].double(), grouped(x, w, b, lambda a, v: a @ v.T)) and bool((y[used:] == 9).all())
+    elif kind == 1:
+        dx = torch.full((rows, k), 9.0, device=DEV)
+        mep.moe_expert_linear_grad_input(rows, E, n, k, dz, off, w, 0, None, None, dx, mep.MOE_FP32, ws)
+        assert torch.equal(dx[:used].double(), grouped(dz, w, b, lambda a, v: a @ v)) and bool((dx[used:] == 9).all())
+    else:
+        for bias in (True, False):
+            dw, db = torch.full((E, n, k), 9.0, device=DEV), torch.full((E, n), 9.0, device=DEV)
+            mep.moe_expert_linear_grad_weight(rows, E, n, k, dz, x, off, dw, mep.MOE_FP32, db if bias else None, ws)
+            for e in range(E):
+                d, a = dz[b[e]:b[e + 1]].double(), x[b[e]:b[e + 1]].double()
+                assert torch.equal(dw[e].double(), d.T @ a), e
+                assert not bias or torch.equal(db[e].double(), d.sum(0)), e
