@@ -6,10 +6,12 @@
 // With it, w is the softmax over the chosen logits alone, and so is the
 // gradient: dz_e = w_e (g_e - sum of w_k dw_k) for those, 0 for the others.
 //
-// LANES lanes have a token: its logits in registers, read once, the chosen
-// experts' g in LDS, where each lane finds its own experts'.
+// LANES lanes have a token: its logits in registers, read once, and a row of
+// LDS through which the exponentials reach the lanes that have the chosen
+// experts, and those lanes' gradients the lanes that store them.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_kernels.h"
 #include "moe_ops.h"
@@ -36,145 +38,184 @@ __device__ inline float lanes_sum(float v)
     return v;
 }
 
-// exp(z - top): 0 for a masked logit (minus infinity, or NaN), 1 for plus infinity.
-__device__ inline float weight_of(float z, float top)
+// What exp(z - top) is formed of: with a top of plus infinity the logits that are it share all, as
+// zeros under a top of zero.  Masked logits (minus infinity, or NaN) give exp_of what is zero there,
+// also under a top of minus infinity.
+__device__ inline float under(float z, float top)
 {
-    if (!(z > -INFINITY))
-        return 0.0f;
-    return z == top ? 1.0f : exp_of(z - top);
+    return top == INFINITY ? (z == INFINITY ? 0.0f : -INFINITY) : z - top;
 }
 
 template <bool BF16>
 __device__ inline float logit(const void* z, int64_t i)
 {
-    const float v = BF16 ? __uint_as_float((uint32_t)((const uint16_t*)z)[i] << 16) : ((const float*)z)[i];
-    return v == v ? v : -INFINITY;
+    return BF16 ? __uint_as_float((uint32_t)((const uint16_t*)z)[i] << 16) : ((const float*)z)[i];
 }
 
-// VALS logits per lane in groups of W consecutive ones.
+// VALS logits per lane in groups of W consecutive ones; LANES * 4 >= top_k
+// (LANES, where that is 64).
 template <int LANES, int VALS, int W, bool BF16>
 __global__ __launch_bounds__(256) void topk_route_grad_kernel(const RouteGrad a)
 {
-    extern __shared__ __align__(16) float chosen[];     // [tokens of the workgroup][LANES * VALS]
-    constexpr int TOKENS = 256 / LANES;
+    extern __shared__ __align__(16) float rows[];       // [tokens of the workgroup][LANES * VALS]
+    constexpr int TOKENS = 256 / LANES, PER = LANES == WAVE ? 1 : 4;
     const int lane = threadIdx.x % LANES;
-    float* const add = chosen + threadIdx.x / LANES * (LANES * VALS);
+    float* const mine = rows + threadIdx.x / LANES * (LANES * VALS);
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int64_t t = block * TOKENS + threadIdx.x / LANES;
     const bool live = t < a.tokens;
     const int64_t row = live ? t * a.E : 0;
     auto expert = [&](int i) { return (i / W * LANES + lane) * W + i % W; };
+    // a row's lanes are of one wave: what they wrote is seen once the wave's writes are done
+    auto meet = [] { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+    // the chosen experts, LANES at a time
+    int e[PER];
+    float dw[PER], p[PER];
+    const int64_t first = live ? t * a.K : 0;
 #pragma unroll
-    for (int i = 0; i < VALS; ++i)
-        add[expert(i)] = 0.0f;
+    for (int c = 0; c < PER; ++c) {
+        const int k = c * LANES + lane;
+        e[c] = -1;
+        dw[c] = p[c] = 0.0f;
+        if (k < a.K) {
+            const int id = a.idx[first + k];
+            dw[c] = a.dw[first + k];
+            e[c] = (uint32_t)id < (uint32_t)a.E ? id : -1;
+        }
+    }
     float z[VALS];
     float top = -INFINITY, sum = 0.0f;
     if (!a.renorm) {
 #pragma unroll
         for (int i = 0; i < VALS; i += W) {
-            const int e = expert(i);
-            if constexpr (W == 4) {
-                z[i] = z[i + 1] = z[i + 2] = z[i + 3] = -INFINITY;
-                if (e < a.E) {
-                    if constexpr (BF16) {
-                        const v2u u = *(const v2u*)((const uint16_t*)a.logits + row + e);
-                        z[i] = bf16_lo(u.x);
-                        z[i + 1] = bf16_hi(u.x);
-                        z[i + 2] = bf16_lo(u.y);
-                        z[i + 3] = bf16_hi(u.y);
-                    } else {
-                        const v4f u = *(const v4f*)((const float*)a.logits + row + e);
+            const int at = expert(i);
+            if constexpr (W == 1) {
+                z[i] = at < a.E ? logit<BF16>(a.logits, row + at) : -INFINITY;
+            } else {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < W; ++c)
+                    z[i + c] = -INFINITY;
+                if (at < a.E) {
+                    if constexpr (BF16) {
+                        typedef uint32_t vu __attribute__((ext_vector_type(W / 2)));
+                        const vu u = *(const vu*)((const uint16_t*)a.logits + row + at);
+#pragma unroll
+                        for (int c = 0; c < W / 2; ++c) {
+                            z[i + 2 * c] = bf16_lo(u[c]);
+                            z[i + 2 * c + 1] = bf16_hi(u[c]);
+                        }
+                    } else {
+                        typedef float vf __attribute__((ext_vector_type(W)));
+                        const vf u = *(const vf*)((const float*)a.logits + row + at);
+#pragma unroll
+                        for (int c = 0; c < W; ++c)
                             z[i + c] = u[c];
                     }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        z[i + c] = z[i + c] == z[i + c] ? z[i + c] : -INFINITY;
                 }
-            } else {
-                z[i] = e < a.E ? logit<BF16>(a.logits, row + e) : -INFINITY;
             }
         }
 #pragma unroll
         for (int i = 0; i < VALS; ++i)
             top = fmaxf(top, z[i]);
         top = lanes_max<LANES>(top);
+        if (top < INFINITY) {
+#pragma unroll
+            for (int i = 0; i < VALS; ++i)
+                z[i] = exp_of(z[i] - top);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VALS; ++i)
+                z[i] = exp_of(under(z[i], top));
+        }
 #pragma unroll
         for (int i = 0; i < VALS; ++i) {
-            z[i] = weight_of(z[i], top);
             sum += z[i];
+            mine[expert(i)] = z[i];
         }
-        sum = lanes_sum<LANES>(sum);
-    }
-    // the chosen experts, LANES at a time
-    const int64_t first = live ? t * a.K : 0;
-    if (a.renorm) {
-        for (int k = lane; k < a.K; k += LANES) {
-            const int e = a.idx[first + k];
-            if ((uint32_t)e < (uint32_t)a.E)
-                top = fmaxf(top, logit<BF16>(a.logits, row + e));
+        meet();
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            if (e[c] >= 0)
+                p[c] = mine[e[c]];
+        meet();
+    } else {
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+            p[c] = e[c] >= 0 ? logit<BF16>(a.logits, row + e[c]) : -INFINITY;
+            top = fmaxf(top, p[c]);
         }
         top = lanes_max<LANES>(top);
-        for (int k = lane; k < a.K; k += LANES) {
-            const int e = a.idx[first + k];
-            if ((uint32_t)e < (uint32_t)a.E)
-                sum += weight_of(logit<BF16>(a.logits, row + e), top);
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+            p[c] = exp_of(under(p[c], top));
+            sum += p[c];
         }
-        sum = lanes_sum<LANES>(sum);
     }
+    sum = lanes_sum<LANES>(sum);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     float G = 0.0f;
-    for (int k = lane; k < a.K; k += LANES) {
-        const int e = a.idx[first + k];
-        if ((uint32_t)e < (uint32_t)a.E) {
-            const float p = weight_of(logit<BF16>(a.logits, row + e), top) * inv;
-            G += p > 0.0f ? p * a.dw[first + k] : 0.0f;
-        }
+#pragma unroll
+    for (int c = 0; c < PER; ++c) {
+        p[c] *= inv;
+        G += p[c] > 0.0f ? p[c] * dw[c] : 0.0f;
     }
     G = lanes_sum<LANES>(G);
-    __syncthreads();
-    for (int k = lane; k < a.K; k += LANES) {
-        const int e = a.idx[first + k];
-        if ((uint32_t)e >= (uint32_t)a.E)
-            continue;
-        const float p = weight_of(logit<BF16>(a.logits, row + e), top) * inv;
-        float g = 0.0f;                       // in the order of k, whichever lane it is
-        for (int j = 0; j < a.K; ++j)
-            if (a.idx[first + j] == e)
-                g += a.dw[first + j];
-        if (p > 0.0f)
-            add[e] = a.renorm ? p * (g - G) : p * g;
+    // what an expert's choices sent, in their order, whichever lane has them
+    float g[PER];
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+        g[c] = 0.0f;
+#pragma unroll
+    for (int cj = 0; cj < PER; ++cj)
+        for (int j = 0; j < LANES && cj * LANES + j < a.K; ++j) {
+            const int ej = __shfl(e[cj], j, LANES);
+            const float dj = __shfl(dw[cj], j, LANES);
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                g[c] += ej == e[c] ? dj : 0.0f;
+        }
+#pragma unroll
+    for (int i = 0; i < VALS; ++i) {
+        const float q = a.renorm ? 0.0f : z[i] * inv;
+        mine[expert(i)] = q > 0.0f ? -q * G : 0.0f;
     }
-    __syncthreads();
+    meet();
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+        if (p[c] > 0.0f)
+            mine[e[c]] = p[c] * g[c] - p[c] * G;
+    meet();
     if (!live)
         return;
 #pragma unroll
     for (int i = 0; i < VALS; i += W) {
-        const int e = expert(i);
-        if (e >= a.E)
+        const int at = expert(i);
+        if (at >= a.E)
             continue;
         float d[W];
 #pragma unroll
-        for (int c = 0; c < W; ++c) {
-            d[c] = add[e + c];
-            if (!a.renorm) {
-                const float p = z[i + c] * inv;
-                d[c] = p > 0.0f ? d[c] - p * G : 0.0f;
-            }
-        }
+        for (int c = 0; c < W; ++c)
+            d[c] = mine[at + c];
         if (a.out_bf16) {
-            uint16_t* o = (uint16_t*)a.dlogits + row + e;
+            uint16_t* o = (uint16_t*)a.dlogits + row + at;
             if constexpr (W == 4)
                 *(v2u*)o = v2u{bf16_pack(d[0], d[1]), bf16_pack(d[2], d[3])};
+            else if constexpr (W == 2)
+                *(uint32_t*)o = bf16_pack(d[0], d[1]);
             else
                 *o = (uint16_t)bf16_pack(d[0], 0.0f);
         } else {
-            float* o = (float*)a.dlogits + row + e;
-            if constexpr (W == 4)
-                *(v4f*)o = v4f{d[0], d[1], d[2], d[3]};
-            else
+            float* o = (float*)a.dlogits + row + at;
+            if constexpr (W == 1) {
                 *o = d[0];
+            } else {
+                typedef float vf __attribute__((ext_vector_type(W)));
+                vf v;
+#pragma unroll
+                for (int c = 0; c < W; ++c)
+                    v[c] = d[c];
+                *(vf*)o = v;
+            }
         }
     }
 }
@@ -187,19 +228,19 @@ hipError_t launch(const RouteGrad& a, hipStream_t stream)
     const int64_t blocks = (a.tokens + TOKENS - 1) / TOKENS;
     const dim3 grid((uint32_t)std::min(blocks, ROW), (uint32_t)((blocks + ROW - 1) / ROW));
     const int bytes = 256 * VALS * 4;
-    const bool wide = a.E % 4 == 0;
-    if constexpr (VALS % 4 == 0)
-        if (wide) {
-            if (a.bf16)
-                topk_route_grad_kernel<LANES, VALS, 4, true><<<grid, dim3(256), bytes, stream>>>(a);
-            else
-                topk_route_grad_kernel<LANES, VALS, 4, false><<<grid, dim3(256), bytes, stream>>>(a);
-            return hipGetLastError();
-        }
-    if (a.bf16)
-        topk_route_grad_kernel<LANES, VALS, 1, true><<<grid, dim3(256), bytes, stream>>>(a);
+    auto run = [&](auto w) {
+        if (a.bf16)
+            topk_route_grad_kernel<LANES, VALS, w, true><<<grid, dim3(256), bytes, stream>>>(a);
+        else
+            topk_route_grad_kernel<LANES, VALS, w, false><<<grid, dim3(256), bytes, stream>>>(a);
+    };
+    // rows start where the vectors of their loads may
+    if (a.E % 4 == 0)
+        run(std::integral_constant<int, 4>{});
+    else if (a.E % 2 == 0)
+        run(std::integral_constant<int, 2>{});
     else
-        topk_route_grad_kernel<LANES, VALS, 1, false><<<grid, dim3(256), bytes, stream>>>(a);
+        run(std::integral_constant<int, 1>{});
     return hipGetLastError();
 }
 
@@ -211,8 +252,12 @@ hipError_t launch_topk_route_grad(const RouteGrad& a, hipStream_t stream)
         return launch<4, 4>(a, stream);
     if (a.E <= 64)
         return launch<16, 4>(a, stream);
+    if (a.E <= 128)
+        return launch<16, 8>(a, stream);
     if (a.E <= 256)
         return launch<16, 16>(a, stream);
+    if (a.E <= 512)
+        return launch<64, 8>(a, stream);
     return launch<64, 16>(a, stream);
 }
 
