@@ -21,7 +21,8 @@ namespace {
 // lanes with the same expert, found bit by bit of its id.
 // ---------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_RANGE = 8192;            // pairs of a workgroup, at least
+constexpr int PLAN_ALONE = 8192;            // pairs up to which one workgroup has all
+constexpr int PLAN_RANGE = 2048;            // pairs of a workgroup beyond, at least
 constexpr int PLAN_GROUPS = 128;            // workgroups, at most
 
 struct Plan {
@@ -56,14 +57,30 @@ template <int THREADS>
 __global__ __launch_bounds__(THREADS) void sort_plan_kernel(const Plan p)
 {
     constexpr int WAVES = THREADS / WAVE;
-    extern __shared__ int hist[];                  // [WAVES][E], then all[E + 1]
+    extern __shared__ int hist[];                  // [WAVES][E], then all[E + 1], then below[E]
     int* const all = hist + WAVES * p.E;
+    int* const below = all + p.E + 1;              // pairs of the workgroups before this one
     const int lane = threadIdx.x & (WAVE - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     int* const mine = hist + wave * p.E;
-    for (int e = threadIdx.x; e < WAVES * p.E; e += THREADS)
+    for (int e = threadIdx.x; e < (WAVES + 2) * p.E + 1; e += THREADS)
         hist[e] = 0;
     __syncthreads();
+    if (p.counts) {
+        // all threads share the [groups][E] counts: so many rows of them at a time
+        const int rows = max(THREADS / p.E, 1), e0 = threadIdx.x % p.E, g0 = threadIdx.x / p.E;
+        for (int e = e0; e < p.E && g0 < rows; e += THREADS) {
+            int before = 0, total = 0;
+#pragma unroll 8
+            for (int g = g0; g < p.groups; g += rows) {
+                const int c = p.counts[g * p.E + e];
+                before += g < (int)blockIdx.x ? c : 0;
+                total += c;
+            }
+            atomicAdd(&below[e], before);
+            atomicAdd(&all[e], total);
+        }
+    }
     const int64_t part = p.range / WAVES;          // a multiple of 64
     const int64_t begin = p.range * blockIdx.x + part * wave;
     const int64_t end = min(begin + part, p.pairs);
@@ -75,19 +92,15 @@ __global__ __launch_bounds__(THREADS) void sort_plan_kernel(const Plan p)
     __syncthreads();
     // each wave's pairs start behind those of the waves and workgroups before it
     for (int e = threadIdx.x; e < p.E; e += THREADS) {
-        int before = 0, total = 0;
-        for (int g = 0; g < p.groups && p.counts; ++g) {
-            const int c = p.counts[(int64_t)g * p.E + e];
-            before += g < (int)blockIdx.x ? c : 0;
-            total += c;
-        }
+        int before = below[e];
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const int c = hist[w * p.E + e];
             hist[w * p.E + e] = before;
             before += c;
         }
-        all[e] = p.counts ? total : before;
+        if (!p.counts)
+            all[e] = before;
     }
     __syncthreads();
     if (wave == 0) {
@@ -163,7 +176,22 @@ __device__ inline int64_t task_of()
     return t;
 }
 
-template <int LANES>
+// STREAM: the nontemporal hint, for rows that no cache will hold.
+template <bool STREAM>
+__device__ inline v4u load_row(const v4u* p)
+{
+    return STREAM ? __builtin_nontemporal_load(p) : *p;
+}
+template <bool STREAM>
+__device__ inline void store_row(const v4u& v, v4u* p)
+{
+    if (STREAM)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+
+template <int LANES, bool STREAM>
 __global__ __launch_bounds__(256) void sort_rows_kernel(const Rows r)
 {
     const int64_t task = task_of<LANES>();
@@ -179,7 +207,7 @@ __global__ __launch_bounds__(256) void sort_rows_kernel(const Rows r)
         if ((uint64_t)row >= (uint64_t)r.rows)
             continue;
         if (live)
-            ((v4u*)r.out)[row * r.vecs + v] = x;
+            store_row<STREAM>(x, (v4u*)r.out + row * r.vecs + v);
         if (v < r.extra)
             r.outs[row * r.extra + v] = s;
     }
@@ -217,7 +245,7 @@ constexpr int AHEAD = 8;      // rows of a token in flight
 
 // out[t] = sum over k, ascending, of w[t][k] * y[slot[t][k]]: an fp32 chain of
 // multiply-adds from +0, as moe_combine_recv forms it, rounded once.
-template <int LANES, bool F32>
+template <int LANES, bool F32, bool STREAM>
 __global__ __launch_bounds__(256) void unsort_rows_kernel(const Rows r)
 {
     typedef Vec<F32> V;
@@ -241,7 +269,7 @@ __global__ __launch_bounds__(256) void unsort_rows_kernel(const Rows r)
             has[a] = k0 + a < r.K && (uint64_t)row < (uint64_t)r.rows;
             w[a] = r.w ? r.w[at] : 1.0f;
             if (has[a])
-                u[a] = y[row * r.vecs];
+                u[a] = load_row<STREAM>(y + row * r.vecs);
         }
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a)
@@ -253,17 +281,20 @@ __global__ __launch_bounds__(256) void unsort_rows_kernel(const Rows r)
                     acc[c] = fmaf(w[a], f[c], acc[c]);
             }
     }
-    ((v4u*)r.out)[t * r.vecs + v] = V::close(acc);
+    store_row<STREAM>(V::close(acc), (v4u*)r.out + t * r.vecs + v);
 }
 
 // dy[slot[t][k]] = w[t][k] * dout[t];  dw[t][k] = dout[t] . y[slot[t][k]].
 // A token's row lies in the registers of `waves` waves (U vectors per lane)
-// while its K rows go by; a dot product is summed per lane, over the lanes,
-// then over the waves in their order.
-template <int LANES, int U, bool F32>
+// while its K rows go by, GRAD_AHEAD of them in flight; a dot product is summed
+// per lane, over the lanes, then over the waves in their order.
+constexpr int GRAD_AHEAD = 4;
+
+template <int LANES, int U, bool F32, bool STREAM>
 __global__ __launch_bounds__(1024) void unsort_rows_grad_kernel(const Rows r, int waves)
 {
     typedef Vec<F32> V;
+    constexpr int AT_ONCE = U > 4 ? 1 : GRAD_AHEAD;
     __shared__ float part[MAX_TOPK][16];
     const int lane = threadIdx.x % LANES;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -271,61 +302,69 @@ __global__ __launch_bounds__(1024) void unsort_rows_grad_kernel(const Rows r, in
     const int64_t t = LANES == WAVE ? block : block * (blockDim.x / LANES) + threadIdx.x / LANES;
     if (t >= r.tokens)
         return;
+    auto vec = [&](int u) { return (u * waves + wave) * LANES + lane; };
     float d[U][V::N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int v = (u * waves + wave) * LANES + lane;
         v4u raw{0, 0, 0, 0};
-        if (v < r.vecs)
-            raw = ((const v4u*)r.dout)[t * r.vecs + v];
+        if (vec(u) < r.vecs)
+            raw = ((const v4u*)r.dout)[t * r.vecs + vec(u)];
         V::open(raw, d[u]);
     }
-    for (int k = 0; k < r.K; ++k) {
-        const int64_t row = r.slot[t * r.K + k];
-        const bool has = (uint64_t)row < (uint64_t)r.rows;
-        const float w = r.w ? r.w[t * r.K + k] : 1.0f;
-        float dot = 0.0f;
-        if (has) {
-            v4u raw[U];
-            if (r.dw)
+    for (int k0 = 0; k0 < r.K; k0 += AT_ONCE) {
+        v4u raw[AT_ONCE][U];
+        int64_t row[AT_ONCE];
+        bool has[AT_ONCE];
+        float w[AT_ONCE], dot[AT_ONCE];
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+            const int64_t at = t * r.K + min(k0 + a, r.K - 1);
+            row[a] = r.slot[at];
+            has[a] = k0 + a < r.K && (uint64_t)row[a] < (uint64_t)r.rows;
+            w[a] = r.w ? r.w[at] : 1.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[a][u] = v4u{0, 0, 0, 0};
+                if (r.dw && has[a] && vec(u) < r.vecs)
+                    raw[a][u] = load_row<STREAM>((const v4u*)r.x + row[a] * r.vecs + vec(u));
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < AT_ONCE; ++a) {
+            if (r.dy && has[a])
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int v = (u * waves + wave) * LANES + lane;
-                    raw[u] = v4u{0, 0, 0, 0};
-                    if (v < r.vecs)
-                        raw[u] = ((const v4u*)r.x)[row * r.vecs + v];
-                }
-            if (r.dy)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int v = (u * waves + wave) * LANES + lane;
                     float g[V::N];
 #pragma unroll
                     for (int c = 0; c < V::N; ++c)
-                        g[c] = w * d[u][c];
-                    if (v < r.vecs)
-                        ((v4u*)r.dy)[row * r.vecs + v] = V::close(g);
+                        g[c] = w[a] * d[u][c];
+                    if (vec(u) < r.vecs)
+                        store_row<STREAM>(V::close(g), (v4u*)r.dy + row[a] * r.vecs + vec(u));
                 }
-            if (r.dw)
+            dot[a] = 0.0f;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[V::N];
-                    V::open(raw[u], f);
+            for (int u = 0; u < U; ++u) {
+                float f[V::N];
+                V::open(raw[a][u], f);
 #pragma unroll
-                    for (int c = 0; c < V::N; ++c)
-                        dot = fmaf(d[u][c], f[c], dot);
-                }
+                for (int c = 0; c < V::N; ++c)
+                    dot[a] = has[a] ? fmaf(d[u][c], f[c], dot[a]) : 0.0f;
+            }
         }
         if (r.dw) {
 #pragma unroll
             for (int s = LANES / 2; s; s >>= 1)
-                dot += __shfl_xor(dot, s, LANES);
-            if (LANES < WAVE || waves == 1) {
-                if (lane == 0)
-                    r.dw[t * r.K + k] = dot;
-            } else if (lane == 0) {
-                part[k][wave] = dot;
-            }
+#pragma unroll
+                for (int a = 0; a < AT_ONCE; ++a)
+                    dot[a] += __shfl_xor(dot[a], s, LANES);
+#pragma unroll
+            for (int a = 0; a < AT_ONCE; ++a)
+                if (lane == 0 && k0 + a < r.K) {
+                    if (LANES < WAVE || waves == 1)
+                        r.dw[t * r.K + k0 + a] = dot[a];
+                    else
+                        part[k0 + a][wave] = dot[a];
+                }
         }
     }
     if (LANES == WAVE && waves > 1 && r.dw) {
@@ -390,7 +429,7 @@ Rows rows_of(const SortRows& p, int elem_bytes)
 
 int plan_groups(int64_t pairs)
 {
-    return (int)std::min<int64_t>((pairs + PLAN_RANGE - 1) / PLAN_RANGE, PLAN_GROUPS);
+    return pairs <= PLAN_ALONE ? 1 : (int)std::min<int64_t>((pairs + PLAN_RANGE - 1) / PLAN_RANGE, PLAN_GROUPS);
 }
 
 }  // namespace
@@ -407,7 +446,7 @@ hipError_t launch_sort_plan(int64_t pairs, int E, const int32_t* idx, int32_t* o
     Plan p{};
     p.pairs = pairs;
     p.E = E;
-    p.groups = std::max(plan_groups(pairs), 1);
+    p.groups = plan_groups(pairs);
     while ((1 << p.bits) < E)
         ++p.bits;
     p.idx = idx;
@@ -420,8 +459,8 @@ hipError_t launch_sort_plan(int64_t pairs, int E, const int32_t* idx, int32_t* o
         p.counts = (int32_t*)workspace;
         count_pairs_kernel<<<dim3(p.groups), dim3(PLAN_THREADS), 0, stream>>>(p);
     }
-    auto launch = [&](auto threads) {                  // at most 36 KB of counts
-        const int bytes = (threads / WAVE * E + E + 1) * 4;
+    auto launch = [&](auto threads) {                  // at most 41 KB of counts
+        const int bytes = ((threads / WAVE + 2) * E + 1) * 4;
         sort_plan_kernel<threads><<<dim3(p.groups), dim3(threads), bytes, stream>>>(p);
     };
     if (E <= MAX_EXPERTS / 2)
@@ -431,13 +470,35 @@ hipError_t launch_sort_plan(int64_t pairs, int E, const int32_t* idx, int32_t* o
     return hipGetLastError();
 }
 
+// The nontemporal hint (us with it, without, on rows that no cache holds yet):
+// sort 131072 rows of 7168 401, 405, 24576 of 4096 39, 47, 8192 of 4096 14.2, 15.3;
+// unsort 364, 415, 41, 49, 14.2, 17.9; its gradient 793, 798, 81, 90, 28, 31.  Unsort
+// reads for the last time; what the other two write is the next operator's
+// input, so they take it only from a size on that the 256 MB cache would not keep
+// (sort 16384 rows of 4096 again and again 25.5, 23.1).  Not for rows that do not
+// fill a wave, whose lines would be written in parts: sort 400000 rows of 200
+// 56, 33.
+constexpr int64_t WRITTEN_PAST = 128 << 20, READ_PAST = 32 << 20;
+
+// Calls f with the hint as a constant, for the rows of `lanes` lanes.
+template <class L, class F>
+static void with_hint(L lanes, const Rows& r, int64_t from, F f)
+{
+    if constexpr (lanes == WAVE)
+        if (r.rows * r.vecs * 16 >= from)
+            return f(std::true_type{});
+    f(std::false_type{});
+}
+
 hipError_t launch_sort_rows(const SortRows& p, int elem_bytes, hipStream_t stream)
 {
     Rows r = rows_of(p, elem_bytes);
     r.extra = p.xs ? p.hidden / SCALE_BLOCK : 0;
     with_lanes(r.vecs, [&](auto lanes) {
         const int64_t blocks = (r.tokens * r.chunks + 256 / lanes - 1) / (256 / lanes);
-        sort_rows_kernel<lanes><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+        with_hint(lanes, r, WRITTEN_PAST, [&](auto hint) {
+            sort_rows_kernel<lanes, hint><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+        });
     });
     return hipGetLastError();
 }
@@ -447,10 +508,12 @@ hipError_t launch_unsort_rows(const SortRows& p, bool f32, hipStream_t stream)
     const Rows r = rows_of(p, f32 ? 4 : 2);
     with_lanes(r.vecs, [&](auto lanes) {
         const int64_t blocks = (r.tokens * r.chunks + 256 / lanes - 1) / (256 / lanes);
-        if (f32)
-            unsort_rows_kernel<lanes, true><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
-        else
-            unsort_rows_kernel<lanes, false><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+        with_hint(lanes, r, READ_PAST, [&](auto hint) {
+            if (f32)
+                unsort_rows_kernel<lanes, true, hint><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+            else
+                unsort_rows_kernel<lanes, false, hint><<<grid_of(blocks), dim3(256), 0, stream>>>(r);
+        });
     });
     return hipGetLastError();
 }
@@ -461,10 +524,12 @@ static void launch_grad(const Rows& r, bool f32, int waves, hipStream_t stream)
     const int threads = LANES == WAVE ? waves * WAVE : 256;
     const int64_t per = LANES == WAVE ? 1 : 256 / LANES;
     const dim3 grid = grid_of((r.tokens + per - 1) / per);
-    if (f32)
-        unsort_rows_grad_kernel<LANES, U, true><<<grid, dim3(threads), 0, stream>>>(r, waves);
-    else
-        unsort_rows_grad_kernel<LANES, U, false><<<grid, dim3(threads), 0, stream>>>(r, waves);
+    with_hint(std::integral_constant<int, LANES>{}, r, WRITTEN_PAST, [&](auto hint) {
+        if (f32)
+            unsort_rows_grad_kernel<LANES, U, true, hint><<<grid, dim3(threads), 0, stream>>>(r, waves);
+        else
+            unsort_rows_grad_kernel<LANES, U, false, hint><<<grid, dim3(threads), 0, stream>>>(r, waves);
+    });
 }
 
 hipError_t launch_unsort_rows_grad(const SortRows& p, bool f32, hipStream_t stream)
