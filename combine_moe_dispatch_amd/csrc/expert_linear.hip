@@ -1170,25 +1170,28 @@ __global__ __launch_bounds__(256) void join_weight_kernel(const Linear p, int sp
 }
 
 // dz = dy * act'(z), eight outputs per thread.  What is handed on is bf16, and
-// sums over many rows of it follow, where a border rounded the other way counts
-// more than all of fp32's roundings: so a product that fp32 (off by less than 8
-// of its roundings) cannot tell from the middle between two bf16 numbers is
-// formed again in 64 bits.  That is one in a thousand: 32768 x 4096, SWIGLU, 200 us
-// against 196 without.
-__device__ inline double slope64(int act, double z)
+// sums over many rows of it follow, in which a value next to a border that is
+// rounded the other way counts more than all of their own roundings (one in
+// 50000 values, 2^-8 of itself).  So the slopes are the formulas' elementary
+// operations in fp32 in the order written here, each rounded once and none fused:
+// whoever forms them so gets the same bf16 numbers.  Off by a few roundings of
+// 2^-24 of |dy|; GELU's lower tail, 1 + erf, is exact to 2^-24 absolutely.
+__device__ inline float logistic_by_steps(float z)
 {
-    if (act == MOE_ACT_GELU)
-        return 0.5 * erfc(-0.70710678118654752440 * z) + z * exp(-0.5 * z * z) * 0.39894228040143267794;
-    const double p = 1.0 / (1.0 + exp(-z));
-    return p * (1.0 + z * (1.0 - p));
+#pragma clang fp contract(off)
+    return 1.0f / (1.0f + expf(-z));
 }
-__device__ inline double silu64(double z) { return z / (1.0 + exp(-z)); }
-
-// v, off by less than `err`, might round to bf16 as another number.
-__device__ inline bool near_border(float v, float err)
+// (d * p) * (1 + z * (1 - p))
+__device__ inline float silu_grad_by_steps(float d, float z, float p)
 {
-    const float border = __uint_as_float((__float_as_uint(v) & 0xFFFF0000u) | 0x8000u);
-    return fabsf(v - border) <= err;
+#pragma clang fp contract(off)
+    return d * p * (1.0f + z * (1.0f - p));
+}
+__device__ inline float gelu_grad_by_steps(float d, float z)
+{
+#pragma clang fp contract(off)
+    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+    return d * (cdf + z * expf(-0.5f * z * z) * 0.39894228040143268f);
 }
 
 __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, const uint16_t* dy)
@@ -1200,7 +1203,6 @@ __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, co
     const int64_t rows = p.offsets ? min(p.rows, (int64_t)p.offsets[p.E]) : p.rows;
     if (row >= rows)
         return;
-    constexpr float ERR = 0x1p-21f;
     float d[8], z[8], v[8];
     open8(load8(dy + row * f + col), d);
     uint16_t* out = (uint16_t*)p.out + row * p.n + col;
@@ -1210,27 +1212,26 @@ __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, co
         open8(load8(p.z_in + row * p.n + f + col), u);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const float g = d[c] * u[c];
-            v[c] = g * silu_slope(z[c]);
-            w[c] = d[c] * silu(z[c]);
-            if (near_border(v[c], ERR * fabsf(g)))
-                v[c] = (float)((double)d[c] * u[c] * slope64(MOE_ACT_SILU, z[c]));
-            if (near_border(w[c], ERR * fabsf(w[c])))
-                w[c] = (float)(d[c] * silu64(z[c]));
+            const float s = logistic_by_steps(z[c]);
+            v[c] = silu_grad_by_steps(d[c] * u[c], z[c], s);
+            w[c] = d[c] * z[c] * s;
         }
         store8(out, v);
         store8(out + f, w);
         return;
     }
+    if (p.act == MOE_ACT_RELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        v[c] = z[c];
-    slopes8(p.act, v);
+        for (int c = 0; c < 8; ++c)
+            v[c] = z[c] > 0.0f ? d[c] : 0.0f;
+    } else if (p.act == MOE_ACT_GELU) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        v[c] *= d[c];
-        if (p.act != MOE_ACT_RELU && near_border(v[c], ERR * fabsf(d[c])))
-            v[c] = (float)(d[c] * slope64(p.act, z[c]));
+        for (int c = 0; c < 8; ++c)
+            v[c] = gelu_grad_by_steps(d[c], z[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] = silu_grad_by_steps(d[c], z[c], logistic_by_steps(z[c]));
     }
     store8(out, v);
 }
