@@ -45,11 +45,34 @@ struct Place {
 // Workgroups of a launch are numbered over both grid dimensions.
 __device__ inline int64_t workgroup_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
 
+// The tile of workgroup `id` of a launch.  Consecutive workgroups go to the 8
+// XCDs in turn: each XCD takes one contiguous run of tiles, so that the tiles
+// sharing weights share its L2.  TURNS: runs of 32 tiles in turn, as many as run on
+// an XCD at once, so that the XCDs work near each other and share the cache behind
+// their L2 too; what is left of a whole round of 256 in one run each.
+template <bool TURNS>
+__device__ inline bool tile_of_id(int64_t id, int64_t tiles, int64_t& t)
+{
+    int64_t first = 0;
+    if (TURNS) {
+        first = tiles & ~(int64_t)255;
+        if (id < first) {
+            t = (id & ~(int64_t)255) + ((id & 7) << 5) + (id >> 3 & 31);
+            return true;
+        }
+        id -= first;
+    }
+    const int64_t per_xcd = (tiles - first + 7) / 8;
+    const int64_t at = id >> 3;
+    t = first + (id & 7) * per_xcd + at;
+    return at < per_xcd && t < tiles;
+}
+
 // Tile t of the launch: experts in order, each expert's tiles in groups of up
 // to 8 row tiles, row tiles fastest inside a group.  Every wave finds it for
 // itself: lane l holds experts [l*per, (l+1)*per), PER >= per of them in
 // registers, so that one trip to memory is enough.
-template <int BM, int PER>
+template <int BM, int PER, bool TURNS = false>
 __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int64_t rows_max, int n_tiles,
                                  Place& out, int64_t id = workgroup_id(), int lane = threadIdx.x & (WAVE - 1))
 {
@@ -68,12 +91,8 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     }
     const int upto = wave_scan(mine);
     const int64_t tiles = (int64_t)__builtin_amdgcn_readlane(upto, WAVE - 1) * n_tiles;
-    // consecutive workgroups go to the 8 XCDs in turn: each XCD takes one
-    // contiguous run of tiles, so that the tiles sharing weights share its L2
-    const int64_t per_xcd = (tiles + 7) / 8;
-    const int64_t at = id >> 3;
-    const int64_t t = (id & 7) * per_xcd + at;
-    if (at >= per_xcd || t >= tiles)
+    int64_t t;
+    if (!tile_of_id<TURNS>(id, tiles, t))
         return false;
     // the lane whose experts hold the tile, and there the expert
     const int src = __popcll(__ballot((int64_t)upto * n_tiles <= t));
