@@ -241,9 +241,15 @@ __device__ inline void open8(const v4u& u, float (&f)[8])
     }
 }
 __device__ inline v4u load8(const uint16_t* p) { return *(const v4u*)p; }
+// Results are stored past the caches where a wave's stores are whole lines, which
+// all bf16 ones are: to the weights 256 experts of 128 rows, 2048 x 1024 370 us so and 455
+// without, forward 295 and 319, 8192 x 8192 x 8192 775 and 787; nothing is lost where
+// the next call reads them (4096 x 4096 after itself 204 and 206 us, 1024 rows of 1024
+// alike).  Half lines are not: fp32 weights' gradients took 446 us so, 296 without.
 __device__ inline void store8(uint16_t* p, const float (&f)[8])
 {
-    *(v4u*)p = v4u{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7])};
+    const v4u u{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7])};
+    __builtin_nontemporal_store(u, (v4u*)p);
 }
 __device__ inline void store8(float* p, const float (&f)[8])
 {
@@ -604,6 +610,16 @@ __device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows,
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
             const int row = q * 8 + row0, u = C::u_row_of(i, wm) + row;
+            if (tiles.apart()) {                     // fp32: four and four, so that stores are whole lines
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const v4f x = *(const v4f*)place(row, h * 8 + col);
+                    const int at = wn * 64 + h * 32 + col * 4;
+                    if (u < u_rows && at < v_rows)
+                        tiles.finish4(u, at, x);
+                }
+                continue;
+            }
             float a[8], b[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -933,6 +949,8 @@ struct RowTiles {
         whole(row, col, a, b, e, bias);
     }
     __device__ inline void finish_bias(int, float) const {}
+    static __device__ constexpr bool apart() { return false; }
+    __device__ inline void finish4(int, int, v4f) const {}
 };
 
 template <Kind KIND, class C, bool GATED>
@@ -981,14 +999,25 @@ struct WeightTiles {
     __device__ inline bool with_bias() const { return at.n == 0; }
     __device__ inline Extra fetch(int, int) const { return Extra{}; }
     __device__ inline void fetch_bias(int, v4u (&)[2]) const {}
+    // outputs that are fp32, the split sums' too, go out as whole lines
+    __device__ inline bool apart() const { return splits > 1 || args->out_f32; }
+    __device__ inline int64_t out_at(const Linear& p, int u, int v) const
+    {
+        return ((int64_t)at.e * p.n + at.m * C::BM + u) * p.k + at.n * C::BN + v;
+    }
     __device__ inline void finish(int u, int v, float (&o)[8], float (&)[8], const Extra&, const v4u (&)[2]) const
     {
         const Linear& p = *args;
-        const int64_t i = ((int64_t)at.e * p.n + at.m * C::BM + u) * p.k + at.n * C::BN + v;
+        store8((uint16_t*)p.out + out_at(p, u, v), o);
+    }
+    __device__ inline void finish4(int u, int v, v4f o) const
+    {
+        const Linear& p = *args;
+        const int64_t i = out_at(p, u, v);
         if (splits > 1)
-            store8((float*)p.workspace + (int64_t)blockIdx.z * p.E * p.n * p.k + i, o);
+            *(v4f*)((float*)p.workspace + (int64_t)blockIdx.z * p.E * p.n * p.k + i) = o;
         else
-            store_out(p, i, o);
+            __builtin_nontemporal_store(o, (v4f*)((float*)p.out + i));
     }
     __device__ inline void finish_bias(int u, float s) const
     {
