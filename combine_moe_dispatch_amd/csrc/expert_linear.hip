@@ -246,10 +246,10 @@ __device__ inline v4u load8(const uint16_t* p) { return *(const v4u*)p; }
 // without, forward 295 and 319, 8192 x 8192 x 8192 775 and 787; nothing is lost where
 // the next call reads them (4096 x 4096 after itself 204 and 206 us, 1024 rows of 1024
 // alike).  Half lines are not: fp32 weights' gradients took 446 us so, 296 without.
+__device__ inline void store_past(uint16_t* p, v4u u) { __builtin_nontemporal_store(u, (v4u*)p); }
 __device__ inline void store8(uint16_t* p, const float (&f)[8])
 {
-    const v4u u{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7])};
-    __builtin_nontemporal_store(u, (v4u*)p);
+    store_past(p, v4u{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3]), bf16_pack(f[4], f[5]), bf16_pack(f[6], f[7])});
 }
 __device__ inline void store8(float* p, const float (&f)[8])
 {
@@ -562,6 +562,41 @@ struct Sums {
     }
 };
 
+// Where nothing but a rounding is left to do: rounded sums through the wave's 4 KB of LDS, two parts
+// of 16 rows of U by 64 of V at once.
+template <class C, class Tiles>
+__device__ __forceinline__ void hand_over_plain(const Sums<C>& sums, int u_rows, int v_rows, uint16_t* part, int wm, int wn,
+                                                int lane, Tiles& tiles)
+{
+    constexpr int PARTS = C::MT > 1 ? 2 : 1;
+    const int r = lane & 15, g = lane >> 4;
+    // 16-byte piece q of row r lies at place q ^ r % 8
+    auto place = [&](int row, int q) { return part + row * 64 + ((q ^ (row & 7)) << 3); };
+#pragma unroll 1
+    for (int i = 0; i < C::MT; i += PARTS) {
+        // lane (r, g) holds row r of U and rows 4g .. 4g+3 of each subtile of V
+#pragma unroll
+        for (int s = 0; s < C::MT; ++s)
+            if (s / PARTS * PARTS == i)
+#pragma unroll
+                for (int j = 0; j < C::NT; ++j) {
+                    const v4f a = sums.acc[j][s];
+                    *(v2u*)(place(s % PARTS * 16 + r, j * 2 + (g >> 1)) + ((g & 1) << 2)) =
+                        v2u{bf16_pack(a[0], a[1]), bf16_pack(a[2], a[3])};
+                }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int q = 0; q < 2 * PARTS; ++q) {
+            const int row = q * 8 + (lane >> 3), c = lane & 7;
+            const int u = C::u_row_of(i, wm) + row, v = wn * 64 + c * 8;
+            const v4u o = *(const v4u*)place(row, c);
+            if (u < u_rows && v < v_rows)
+                tiles.finish_plain(u, v, o);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
 // Hands a wave's sums to the tiles' finish, eight consecutive outputs at a time:
 // 16 rows of U by the wave's 64 of V go through 4 KB of LDS of its own, so that
 // its stores are whole lines (four lanes of 16 bytes from the sums' own layout
@@ -572,9 +607,21 @@ __device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows,
                                           Tiles& tiles)
 {
     static_assert(C::NT == 4, "a wave has 64 rows of V");
-    constexpr int PASSES = GATED ? 1 : 2;            // by 8 (GATED: 16) rows of U
     const int wm = wave % C::WM, wn = wave / C::WM;
     float* const part = (float*)(lds + wave * 4096);
+    if constexpr (BIAS)
+        if (sums.mine)
+#pragma unroll
+            for (int i = 0; i < Sums<C>::ALONE; ++i) {
+                const int u = C::u_row_of(wn * Sums<C>::ALONE + i, wm) + lane;
+                if (wn * Sums<C>::ALONE + i < C::MT && lane < 16 && u < u_rows)
+                    tiles.finish_bias(u, sums.alone[i][0]);
+            }
+    if (!GATED && tiles.plain()) {
+        hand_over_plain(sums, u_rows, v_rows, (uint16_t*)part, wm, wn, lane, tiles);
+        return;
+    }
+    constexpr int PASSES = GATED ? 1 : 2;            // by 8 (GATED: 16) rows of U
     // 16-byte piece q of row r lies at place q ^ r: rows apart in the banks both ways
     auto place = [&](int row, int q) { return part + row * 64 + ((q ^ row) << 2); };
     const int row0 = GATED ? lane >> 2 : lane >> 3, col = GATED ? lane & 3 : lane & 7;
@@ -639,14 +686,6 @@ __device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows,
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    if constexpr (BIAS)
-        if (sums.mine)
-#pragma unroll
-            for (int i = 0; i < Sums<C>::ALONE; ++i) {
-                const int u = C::u_row_of(wn * Sums<C>::ALONE + i, wm) + lane;
-                if (wn * Sums<C>::ALONE + i < C::MT && lane < 16 && u < u_rows)
-                    tiles.finish_bias(u, sums.alone[i][0]);
-            }
 }
 
 // The product of one tile, with S stages of both operands in LDS.
@@ -951,6 +990,15 @@ struct RowTiles {
     __device__ inline void finish_bias(int, float) const {}
     static __device__ constexpr bool apart() { return false; }
     __device__ inline void finish4(int, int, v4f) const {}
+    __device__ inline bool plain() const
+    {
+        const Linear& p = *args;
+        return splits == 1 && !p.out_f32 && p.act == MOE_ACT_NONE && !p.residual && !(FWD && (p.bias || p.z_out));
+    }
+    __device__ inline void finish_plain(int u, int v, v4u o) const
+    {
+        store_past((uint16_t*)args->out + (int64_t)(at.m0 + u) * width(*args) + first_col(at) + v, o);
+    }
 };
 
 template <Kind KIND, class C, bool GATED>
@@ -1005,11 +1053,13 @@ struct WeightTiles {
     {
         return ((int64_t)at.e * p.n + at.m * C::BM + u) * p.k + at.n * C::BN + v;
     }
-    __device__ inline void finish(int u, int v, float (&o)[8], float (&)[8], const Extra&, const v4u (&)[2]) const
+    __device__ inline bool plain() const { return !apart(); }
+    __device__ inline void finish_plain(int u, int v, v4u o) const
     {
         const Linear& p = *args;
-        store8((uint16_t*)p.out + out_at(p, u, v), o);
+        store_past((uint16_t*)p.out + out_at(p, u, v), o);
     }
+    __device__ inline void finish(int, int, float (&)[8], float (&)[8], const Extra&, const v4u (&)[2]) const {}
     __device__ inline void finish4(int u, int v, v4f o) const
     {
         const Linear& p = *args;
