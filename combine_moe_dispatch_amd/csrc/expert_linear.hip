@@ -936,7 +936,7 @@ struct RowTiles {
     static constexpr bool FWD = KIND == Kind::FORWARD;
     int n_tiles, splits;
     Place at;
-    const Linear* args;
+    Linear args;              // (read once: through the epilogue's loop they stay in scalar registers)
 
     // columns of an output row's sums, and those that tiles divide
     static __device__ inline int width(const Linear& p) { return FWD ? p.n : p.k; }
@@ -962,19 +962,19 @@ struct RowTiles {
         w.us.terms = w.vs.terms = (int)(t1 - t0);
         return true;
     }
-    __device__ inline void begin_finish() { args = &arguments(); }
+    __device__ inline void begin_finish() { args = arguments(); }
     __device__ inline bool with_bias() const { return false; }
     __device__ inline Extra fetch(int u, int v) const
     {
-        return splits > 1 ? Extra{} : Finish<KIND, GATED>(*args).fetch(at.m0 + u, first_col(at) + v);
+        return splits > 1 ? Extra{} : Finish<KIND, GATED>(args).fetch(at.m0 + u, first_col(at) + v);
     }
     __device__ inline void fetch_bias(int v, v4u (&bias)[2]) const
     {
-        Finish<KIND, GATED>(*args).fetch_bias(at.e, first_col(at) + v, bias);
+        Finish<KIND, GATED>(args).fetch_bias(at.e, first_col(at) + v, bias);
     }
     __device__ inline void finish(int u, int v, float (&a)[8], float (&b)[8], const Extra& e, const v4u (&bias)[2]) const
     {
-        const Linear& p = *args;
+        const Linear& p = args;
         const int64_t row = at.m0 + u;
         const int col = first_col(at) + v;
         if (splits > 1) {
@@ -992,12 +992,12 @@ struct RowTiles {
     __device__ inline void finish4(int, int, v4f) const {}
     __device__ inline bool plain() const
     {
-        const Linear& p = *args;
+        const Linear& p = args;
         return splits == 1 && !p.out_f32 && p.act == MOE_ACT_NONE && !p.residual && !(FWD && (p.bias || p.z_out));
     }
     __device__ inline void finish_plain(int u, int v, v4u o) const
     {
-        store_past((uint16_t*)args->out + (int64_t)(at.m0 + u) * width(*args) + first_col(at) + v, o);
+        store_past((uint16_t*)args.out + (int64_t)(at.m0 + u) * width(args) + first_col(at) + v, o);
     }
 };
 
