@@ -1483,31 +1483,33 @@ void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, i
 // best: rounds of workgroups, each of its steps and of what a tile costs beside
 // them (finding it, its first loads, its outputs); a join where sums are split
 // (a second launch, the partial sums written and read); never less than the
-// bytes take.  Steps and tiles (us, all workgroups of a CU together) are fitted
-// to 120 measured shapes of all three products, from 1 to 32768 rows, 1 to 256
-// experts and 8 to 7168 columns, every tile and split of each (the choice was
-// 2.2% above the best of them in the mean, 28% at most).  Both sides of some
-// choices, us:
-//  - 256 x 256 against 128 x 256 and 128 x 128: 4096 x 4096 x 4096 109, 138,
-//    158; 16 experts, 32768 rows, 4096 x 2048 521, 565, 621; 64 experts of about
-//    128 rows, 2048 x 2048 184, 147, 154 (64 x 128: 157);
-//  - 64 x 128 against 128 x 128: one expert, 1000 rows, 4096 x 4096 41.5
-//    against 44.7 (256 x 256 in four splits 51.5); 64 experts of about 64 rows 127
-//    against 136;
-//  - 32 x 128 against 32 x 256: 64 experts of 4 rows, 4096 x 2048 167 against 164,
-//    one expert, 1000 rows, 512 x 512 6.8 against 7.6; against 64 x 128: 8 experts
-//    of about 37 rows, 1000 x 384, to the input 9.3 against 10.6;
-//  - splits: 128 rows, 256 x 7168 in 1, 4, 8, 16 splits 20, 13.8, 11.1, 11.6; 64
-//    rows, 4096 x 4096 in 1, 2, 4, 8 24, 15.1, 13.0, 15.0.
+// bytes take.  Steps and tiles (us, all workgroups of a CU together; other by a
+// factor to the weights) are fitted to 120 measured shapes of all three
+// products, from 1 to 32768 rows, 1 to 256 experts and 8 to 7168 columns, every
+// tile and split of each (the choice was 1.6% above the best of them in the
+// mean, 16% at most).  Both sides of some choices, us:
+//  - 256 x 256 against 128 x 256 and 128 x 128: 4096 x 4096 x 4096 105, 143,
+//    166; 16 experts, 32768 rows, 4096 x 2048 494, 547, 618; 64 experts of about
+//    128 rows, 2048 x 2048 177, 136, 145 (64 x 128: 153);
+//  - 64 x 128 against 128 x 128: one expert, 1000 rows, 4096 x 4096 43.8
+//    against 45.9 (256 x 256 in four splits 54.5); 64 experts of about 64 rows 121
+//    against 134;
+//  - 32 x 128 against 32 x 256: 64 experts, 16 rows, 4096 x 2048 37.4 against 36.4,
+//    one expert, 1000 rows, 512 x 512 7.4 against 8.1; against 64 x 128: 8 experts of
+//    about 37 rows, 1000 x 384, to the input 8.7 against 10.4;
+//  - 128 x 128 against 256 x 256 to the weights: 8 experts of about 250 rows, 4096 x
+//    2048 57 against 64;
+//  - splits: 128 rows, 256 x 7168 in 1, 4, 8, 16 splits 20, 13.6, 11.6, 11.7; 64
+//    rows, 4096 x 4096 in 1, 2, 4, 8 24, 14.5, 13.1, 14.9.
 struct Cost {
     Form form;
     int bm, bn, per_cu;
     float step, tile;
 };
 constexpr Cost COSTS[] = {
-    {Form::T256, 256, 256, 1, 1.53f, 6.5f}, {Form::T128W, 128, 256, 1, 0.89f, 4.9f},
-    {Form::T128, 128, 128, 2, 1.02f, 3.3f}, {Form::T64, 64, 128, 2, 0.58f, 2.7f},
-    {Form::T32W, 32, 256, 2, 0.94f, 1.7f},  {Form::T32, 32, 128, 2, 0.44f, 1.9f},
+    {Form::T256, 256, 256, 1, 1.38f, 8.7f}, {Form::T128W, 128, 256, 1, 0.89f, 3.7f},
+    {Form::T128, 128, 128, 2, 1.03f, 3.3f}, {Form::T64, 64, 128, 2, 0.57f, 3.4f},
+    {Form::T32W, 32, 256, 2, 1.10f, 1.7f},  {Form::T32, 32, 128, 2, 0.49f, 2.15f},
 };
 
 Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
@@ -1539,17 +1541,18 @@ Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
         else if (E == 1)
             tiles = (float)((rows + c.bm - 1) / c.bm) * across;
         else                                             // an expert's last tile is half full
-            tiles = std::max(used, (float)rows / c.bm + 0.5f * used) * across;
+            tiles = std::max(used, (float)rows / c.bm + 0.54f * used) * across;
         for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
             const float load = tiles * splits / (256.0f * c.per_cu);
             const bool counted = (weight || E == 1) && load <= 4.0f;
             const float rounds =
                 std::max(1.0f, counted ? std::ceil(load) : load <= 3.0f ? std::ceil(1.05f * load) : load + 0.5f);
-            const float step = load <= 0.5f ? 0.64f * c.step : c.step;       // a half empty chip's loads arrive sooner
-            float us = rounds * ((steps + splits - 1) / splits * step + c.tile);
+            const float step = (load <= 0.5f ? 0.66f : 1.0f) * (weight ? 0.91f : 1.0f) * c.step;
+            const float tile = (weight ? 1.17f : 1.0f) * c.tile;
+            float us = rounds * ((steps + splits - 1) / splits * step + tile);
             if (splits > 1)
-                us += 2.9f + splits * outputs * 1e-6f;                       // 8 bytes at 8 TB/s
-            us = std::max(us, bytes / 6.05e6f) + 0.03f * us;
+                us += 4.5f + splits * outputs * 1.2e-6f;                     // 8 bytes at 6.75 TB/s
+            us = std::max(us, bytes / 5.6e6f) + 0.03f * us;
             if (!form || us < best) {
                 best = us;
                 form = &c;
