@@ -8,7 +8,10 @@
 //
 // LANES lanes have a token: its logits in registers, read once, and a row of
 // LDS through which the exponentials reach the lanes that have the chosen
-// experts, and those lanes' gradients the lanes that store them.
+// experts, and those lanes' gradients the lanes that store them.  Bound by HBM:
+// 131072 tokens, 256 experts, top 8, fp32 in and out 50 us, 5.6 TB/s, on logits
+// that no cache holds (44 us where it does); 128 tokens 2.8 us, the launch's
+// latency.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
