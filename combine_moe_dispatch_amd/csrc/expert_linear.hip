@@ -1196,12 +1196,13 @@ __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear 
 // registers, a wave goes through 8 weight rows at a time, whose dz are uniform;
 // a workgroup has 512 columns by 64 weight rows.  Against the 256 x 256 tile,
 // whose one step costs less than finding it, its first loads and its outputs, 64
-// experts, 4096 x 2048 (1.07 GB): 177 us against 281 with 1 row each, 231
-// against 286 with 4, 309 against 286 with 8, where the vector unit's
-// multiply-adds are what bounds it; of small gradients the latencies (16 experts
-// of 6 rows, 1000 x 384 14 us against 8).
+// experts, 4096 x 2048 (1.07 GB): 184 us against 230 with 1 row each, 181 against
+// 237 with 4, 197 against 241 with 6, 227 against 241 with 8, where the vector
+// unit's multiply-adds are what bounds it (8 ragged rows each of 8 experts of 4096
+// x 4096 63 to 72 against 61 to 64); of small gradients the latencies (16 experts of
+// 6 rows, 1000 x 384 14 us against 8).
 constexpr int FEW_ROWS = 8, FEW_COLS = 512, FEW_N = 64;
-constexpr int FEW_MEAN = 5;                      // rows per expert
+constexpr int FEW_MEAN = 7;                      // rows per expert
 constexpr int64_t FEW_LEAST = 1 << 24;           // weights
 
 __global__ __launch_bounds__(256) void linear_weight_few_kernel(const Linear p, int n_chunks, int k_chunks)
