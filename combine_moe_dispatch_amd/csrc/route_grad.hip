@@ -4,7 +4,8 @@
 // Without renormalisation w_k = p[idx_k], p the softmax over all experts:
 //   dz_e = p_e (g_e - G),  g_e = sum of dw_k over idx_k = e,  G = sum of p[idx_k] dw_k.
 // With it, w is the softmax over the chosen logits alone, and so is the
-// gradient: dz_e = w_e (g_e - sum of w_k dw_k) for those, 0 for the others.
+// gradient: dz_e = w_e (g_e - n_e sum of w_k dw_k) for those, 0 for the others,
+// n_e how many of the choices are e (1, unless a caller's own choices repeat).
 //
 // LANES lanes have a token: its logits in registers, read once, and a row of
 // LDS through which the exponentials reach the lanes that have the chosen
@@ -164,10 +165,25 @@ __global__ __launch_bounds__(256) void topk_route_grad_kernel(const RouteGrad a)
     }
     G = lanes_sum<LANES>(G);
     // what an expert's choices sent, in their order, whichever lane has them
-    float g[PER];
+    float g[PER], times[PER];
 #pragma unroll
-    for (int c = 0; c < PER; ++c)
+    for (int c = 0; c < PER; ++c) {
         g[c] = 0.0f;
+        times[c] = 1.0f;
+    }
+    if (a.renorm) {
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            times[c] = 0.0f;
+#pragma unroll
+        for (int cj = 0; cj < PER; ++cj)
+            for (int j = 0; j < LANES && cj * LANES + j < a.K; ++j) {
+                const int ej = __shfl(e[cj], j, LANES);
+#pragma unroll
+                for (int c = 0; c < PER; ++c)
+                    times[c] += ej == e[c] ? 1.0f : 0.0f;
+            }
+    }
 #pragma unroll
     for (int cj = 0; cj < PER; ++cj)
         for (int j = 0; j < LANES && cj * LANES + j < a.K; ++j) {
@@ -186,7 +202,7 @@ __global__ __launch_bounds__(256) void topk_route_grad_kernel(const RouteGrad a)
 #pragma unroll
     for (int c = 0; c < PER; ++c)
         if (p[c] > 0.0f)
-            mine[e[c]] = p[c] * g[c] - p[c] * G;
+            mine[e[c]] = p[c] * g[c] - p[c] * (times[c] * G);
     meet();
     if (!live)
         return;

@@ -562,8 +562,9 @@ int moe_unsort_rows_grad(int32_t tokens, int32_t top_k, int32_t rows, int32_t hi
  *   dlogits         [tokens][num_experts], MOE_BF16 or MOE_FP32 (dlogits_dtype)
  * With p the softmax over all experts, g_e the sum of dweights over the k with
  * topk_idx = e: dlogits_e = p_e (g_e - sum over k of p dweights); with
- * renormalise the same with the softmax over the chosen logits, and 0 for all
- * others.  A weight of 0 (masked experts and tokens) passes no gradient,
+ * renormalise p is the softmax over the top_k chosen logits, dlogits_e =
+ * p_e (g_e - n_e * the sum) for an expert chosen n_e times (once, by
+ * moe_topk_route), and 0 for all others.  A weight of 0 (masked experts and tokens) passes no gradient,
  * whatever its dweights; an id outside [0, num_experts) has none. */
 int moe_topk_route_grad(int32_t tokens, int32_t num_experts, int32_t top_k, const void* logits,
                         int32_t logits_dtype, int32_t renormalise, const int32_t* topk_idx,

@@ -264,11 +264,11 @@ def route_grad_ref(z, idx, dw, renorm):
         for k, e in live:
             g[e] += dw[t, k]
             gabs[e] += abs(dw[t, k])
-        mask = np.zeros(E, bool)
-        mask[[e for _, e in ids]] = True
-        use = mask if renorm else np.ones(E, bool)
-        d[t] = np.where(use & (p > 0), p * (g - G), 0)
-        scale[t] = np.where(use, p * (gabs + Gabs), 0)
+        times = np.ones(E)
+        if renorm:
+            times = np.bincount([e for _, e in ids], minlength=E)
+        d[t] = np.where((times > 0) & (p > 0), p * (g - times * G), 0)
+        scale[t] = np.where(times > 0, p * (gabs + times * Gabs), 0)
     return d, scale
 
 
@@ -317,14 +317,18 @@ def test_route_grad_masks(renorm):
 
 
 @pytest.mark.parametrize("renorm", [False, True])
-def test_route_grad_by_differences(renorm):
+@pytest.mark.parametrize("repeats", [False, True], ids=["", "repeats"])
+def test_route_grad_by_differences(renorm, repeats):
     """Against differences of the 64-bit weights: central ones of step 1e-4 are off by about
     h^2 |f'''| / 6 < 1e-8 of the weights' size."""
-    say(f"[gpu] route gradient by differences renorm={renorm}")
+    say(f"[gpu] route gradient by differences renorm={renorm} repeats={repeats}")
     T, E, K, h = 4, 24, 5, 1e-4
     g = rng(7)
     z = R.f64(dev(g.standard_normal((T, E)).astype(np.float32)))
     idx = np.argsort(-z, axis=1, kind="stable")[:, :K]
+    if repeats:                                      # a caller's own choices may name an expert twice
+        idx[:, 3] = idx[:, 1]
+        idx[0] = idx[0, 0]
     dw = g.standard_normal((T, K)).astype(np.float32).astype(np.float64)
 
     def loss(z):
@@ -337,6 +341,7 @@ def test_route_grad_by_differences(renorm):
     got = torch.empty((T, E), device=DEV)
     mep.moe_topk_route_grad(T, E, K, dev(z.astype(np.float32)), mep.MOE_FP32, renorm, dev(idx.astype(np.int32)),
                             dev(dw.astype(np.float32)), got, mep.MOE_FP32)
+    check_route_grad(z, idx, dw, renorm, F32, F32)
     for e in range(E):
         step = np.zeros((T, E))
         step[:, e] = h
