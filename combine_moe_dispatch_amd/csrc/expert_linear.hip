@@ -982,16 +982,9 @@ struct DeepTile {
     }
 };
 
-// A workgroup's tile: tiles.next() describes it (false: there is none), and its
-// outputs go to tiles.finish().
 template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Tiles>
-__device__ __forceinline__ void run_tile(uint8_t* lds, Tiles& tiles)
+__device__ __forceinline__ void sum_and_hand_over(uint8_t* lds, Tiles& tiles, const Work& w, int wave, int lane)
 {
-    const int lane = threadIdx.x & (WAVE - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-    Work w;
-    if (!tiles.next(workgroup_id(), w))
-        return;
     Sums<C> sums;
     sums.clear(BIAS && tiles.with_bias() ? Sums<C>::of_wave(wave / C::WM) : 0);
     if constexpr (C::DEEP) {
@@ -1004,6 +997,30 @@ __device__ __forceinline__ void run_tile(uint8_t* lds, Tiles& tiles)
     }
     tiles.begin_finish();
     hand_over<C, GATED, BIAS>(sums, w.us.valid, w.vs.valid, lds, wave, anew(lane), tiles);
+}
+
+// A workgroup's tile: tiles.next() describes it (false: there is none), and its
+// outputs go to tiles.finish().
+template <class C, bool U_CONTIG, bool V_CONTIG, bool GATED, bool BIAS, class Tiles>
+__device__ __forceinline__ void run_tile(uint8_t* lds, Tiles& tiles)
+{
+    const int lane = threadIdx.x & (WAVE - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    Work w;
+    if (!tiles.next(workgroup_id(), w))
+        return;
+    if constexpr (C::DEEP) {
+        // an expert's last rows, where half the tile is enough (us, without and with it, of the
+        // gradient to the input: 16 experts, 32768 rows, 7168 x 2048 792, 771, of the product 64 experts,
+        // 2048 x 4096 541, 528; nothing lost where all tiles are full)
+        typedef Block<C::BM / 2, C::BN, C::WM, C::WN, 3> Low;
+        static_assert(Low::LDS <= C::LDS && Low::THREADS == C::THREADS, "in the same launch");
+        if (w.us.valid <= Low::BM) {
+            sum_and_hand_over<Low, U_CONTIG, V_CONTIG, GATED, BIAS>(lds, tiles, w, wave, lane);
+            return;
+        }
+    }
+    sum_and_hand_over<C, U_CONTIG, V_CONTIG, GATED, BIAS>(lds, tiles, w, wave, lane);
 }
 
 // The part of [0, steps * STEP) that split `s` of `splits` sums.
@@ -1500,11 +1517,11 @@ void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, i
 // bytes take.  Steps and tiles (us, all workgroups of a CU together; other by a
 // factor to the weights) are fitted to 120 measured shapes of all three
 // products, from 1 to 32768 rows, 1 to 256 experts and 8 to 7168 columns, every
-// tile and split of each (the choice was 1.6% above the best of them in the
-// mean, 16% at most).  Both sides of some choices, us:
+// tile and split of each (the choice was 1.7% above the best of them in the
+// mean, 17% at most).  Both sides of some choices, us:
 //  - 256 x 256 against 128 x 256 and 128 x 128: 4096 x 4096 x 4096 105, 143,
-//    166; 16 experts, 32768 rows, 4096 x 2048 494, 547, 618; 64 experts of about
-//    128 rows, 2048 x 2048 177, 136, 145 (64 x 128: 153);
+//    166; 16 experts, 32768 rows, 4096 x 2048 489, 540, 618; 64 experts of about
+//    128 rows, 2048 x 2048 154, 135, 144 (64 x 128: 155);
 //  - 64 x 128 against 128 x 128: one expert, 1000 rows, 4096 x 4096 43.8
 //    against 45.9 (256 x 256 in four splits 54.5); 64 experts of about 64 rows 121
 //    against 134;
@@ -1519,11 +1536,12 @@ struct Cost {
     Form form;
     int bm, bn, per_cu;
     float step, tile;
+    float last;               // tiles that an expert has beyond its rows' share
 };
 constexpr Cost COSTS[] = {
-    {Form::T256, 256, 256, 1, 1.38f, 8.7f}, {Form::T128W, 128, 256, 1, 0.89f, 3.7f},
-    {Form::T128, 128, 128, 2, 1.03f, 3.3f}, {Form::T64, 64, 128, 2, 0.57f, 3.4f},
-    {Form::T32W, 32, 256, 2, 1.10f, 1.7f},  {Form::T32, 32, 128, 2, 0.49f, 2.15f},
+    {Form::T256, 256, 256, 1, 1.29f, 9.5f, 0.27f}, {Form::T128W, 128, 256, 1, 0.89f, 4.2f, 0.54f},
+    {Form::T128, 128, 128, 2, 1.03f, 3.4f, 0.54f}, {Form::T64, 64, 128, 2, 0.59f, 3.4f, 0.54f},
+    {Form::T32W, 32, 256, 2, 1.22f, 1.7f, 0.54f},  {Form::T32, 32, 128, 2, 0.49f, 2.2f, 0.54f},
 };
 
 Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
@@ -1554,14 +1572,14 @@ Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
             tiles = (float)E * ((n + c.bm - 1) / c.bm) * ((k + c.bn - 1) / c.bn);
         else if (E == 1)
             tiles = (float)((rows + c.bm - 1) / c.bm) * across;
-        else                                             // an expert's last tile is half full
-            tiles = std::max(used, (float)rows / c.bm + 0.54f * used) * across;
+        else                                             // an expert's last tile is half full, or a half one
+            tiles = std::max(used, (float)rows / c.bm + c.last * used) * across;
         for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
             const float load = tiles * splits / (256.0f * c.per_cu);
             const bool counted = (weight || E == 1) && load <= 4.0f;
             const float rounds =
                 std::max(1.0f, counted ? std::ceil(load) : load <= 3.0f ? std::ceil(1.05f * load) : load + 0.5f);
-            const float step = (load <= 0.5f ? 0.66f : 1.0f) * (weight ? 0.91f : 1.0f) * c.step;
+            const float step = (load <= 0.5f ? 0.66f : 1.0f) * (weight ? 0.82f : 1.0f) * c.step;
             const float tile = (weight ? 1.17f : 1.0f) * c.tile;
             float us = rounds * ((steps + splits - 1) / splits * step + tile);
             if (splits > 1)

@@ -434,23 +434,76 @@ FORMS = [
     ("128 x 128", 1, 0, 0, 3457, 16, 1600, 480), ("128 x 128", 8, 0, 0, 4055, 5, 16, 3832),
     ("128 x 128", 1, 0, 1, 3393, 3, 1072, 472), ("128 x 128", 8, 0, 1, 4195, 3, 16, 3704),
     ("128 x 128", 1, 1, 0, 4450, 2, 608, 816), ("128 x 128", 8, 1, 0, 3864, 3, 3920, 8),
-    ("128 x 128", 1, 2, 0, 3646, 8, 2352, 264), ("128 x 256", 1, 0, 0, 2437, 2, 1632, 480),
-    ("128 x 256", 8, 0, 0, 2067, 8, 144, 4464), ("128 x 256", 1, 0, 1, 2544, 1, 1568, 456),
+    ("128 x 128", 1, 2, 0, 3847, 8, 2128, 144), ("128 x 256", 1, 0, 0, 2437, 2, 1632, 480),
+    ("128 x 256", 8, 0, 0, 2067, 8, 144, 4464), ("128 x 256", 1, 0, 1, 3749, 8, 960, 480),
     ("128 x 256", 8, 0, 1, 2055, 1, 144, 4680), ("128 x 256", 1, 1, 0, 3620, 3, 464, 1040),
-    ("128 x 256", 8, 1, 0, 2286, 5, 3888, 136), ("128 x 256", 1, 2, 0, 3847, 8, 2128, 144),
+    ("128 x 256", 8, 1, 0, 2286, 5, 3888, 136), ("128 x 256", 1, 2, 0, 2583, 5, 3728, 136),
     ("256 x 256", 1, 0, 0, 2159, 5, 3504, 480), ("256 x 256", 1, 0, 1, 3673, 8, 1968, 472),
     ("256 x 256", 1, 1, 0, 3989, 16, 464, 1696), ("256 x 256", 1, 2, 0, 3749, 8, 2912, 272),
     ("32 x 128", 1, 0, 0, 13, 2, 16, 472), ("32 x 128", 8, 0, 0, 11, 2, 16, 3632),
     ("32 x 128", 1, 0, 1, 18, 2, 16, 456), ("32 x 128", 8, 0, 1, 19, 2, 16, 3704),
     ("32 x 128", 1, 1, 0, 8, 2, 464, 8), ("32 x 128", 8, 1, 0, 9, 2, 3616, 8), ("32 x 128", 1, 2, 0, 907, 2, 16, 8),
-    ("32 x 128", 4, 2, 0, 3714, 2, 1072, 8), ("32 x 256", 1, 0, 0, 3951, 5, 400, 552),
-    ("32 x 256", 1, 0, 1, 3925, 5, 400, 464), ("32 x 256", 1, 1, 0, 2672, 2, 464, 664),
-    ("32 x 256", 1, 2, 0, 4703, 8, 80, 4176), ("64 x 128", 1, 0, 0, 4208, 8, 176, 696),
-    ("64 x 128", 8, 0, 0, 2172, 3, 16, 3672), ("64 x 128", 1, 0, 1, 4227, 5, 176, 656),
-    ("64 x 128", 8, 0, 1, 1944, 2, 16, 4176), ("64 x 128", 1, 1, 0, 4207, 3, 688, 144),
-    ("64 x 128", 4, 1, 0, 3917, 3, 1904, 8), ("64 x 128", 1, 2, 0, 2934, 3, 2880, 8),
-    ("64 x 128", 8, 2, 0, 4020, 1, 2112, 8), ("few rows", 1, 2, 0, 30, 8, 2048, 1032),
-    ("few rows", 1, 2, 0, 19, 5, 4096, 1000), ("few rows", 1, 2, 0, 3, 1, 4104, 4096)]
+    ("32 x 128", 4, 2, 0, 3714, 2, 1072, 8), ("32 x 256", 1, 0, 0, 227, 64, 904, 472),
+    ("32 x 256", 1, 0, 1, 540, 16, 3984, 520),
+    ("32 x 256", 1, 1, 0, 30, 16, 480, 3904), ("32 x 256", 1, 2, 0, 4703, 8, 80, 4176),
+    ("64 x 128", 1, 0, 0, 4172, 8, 160, 776), ("64 x 128", 8, 0, 0, 2172, 3, 16, 3672),
+    ("64 x 128", 1, 0, 1, 4193, 5, 144, 848), ("64 x 128", 8, 0, 1, 1944, 2, 16, 4176),
+    ("64 x 128", 1, 1, 0, 4456, 3, 736, 144), ("64 x 128", 4, 1, 0, 3917, 3, 1904, 8),
+    ("64 x 128", 1, 2, 0, 2463, 5, 3616, 8), ("64 x 128", 8, 2, 0, 4020, 1, 2112, 8),
+    ("few rows", 1, 2, 0, 30, 8, 2048, 1032), ("few rows", 1, 2, 0, 19, 5, 4096, 1000),
+    ("few rows", 1, 2, 0, 3, 1, 4104, 4096)]
+
+
+@pytest.mark.parametrize("last", [1, 127, 128, 129, 255])
+def test_last_rows(last):
+    """Experts whose last rows take half a 256 x 256 tile, beside ones that take all of it, and
+    weight rows alike."""
+    say(f"[gpu] linear last rows {last}")
+    b = [0]
+    for r in (1280 + last, 1536, last, 0, 1024 + last):
+        b.append(b[-1] + r)
+    rows, E, sum_ = b[-1], 5, 1160
+    g = gen(11, last)
+    off, a = offsets(b), whole(g, rows, sum_)
+
+    def width(kind, gated):                          # one that takes the tile, odd too
+        for c in range(1800 + last // 8 * 8, 9000, 256):
+            n, k = (sum_, c) if kind == 1 else (c - c % 16, sum_)
+            if form_of(kind, gated, rows, E, n, k) == ("256 x 256", 1):
+                return n, k
+        raise AssertionError("no such width")
+
+    n, k = width(0, 0)
+    w, ws = whole(g, E, n, k), space(rows, E, n, k)
+    s = grouped(a, w, b, lambda u, v: u @ v.T)
+    for kind in (BF16, F32):
+        y = torch.empty((rows, n), device=DEV, dtype=kind)
+        mep.moe_expert_linear(rows, E, n, k, a, off, w, None, 0, None, None, y, KIND[kind], ws)
+        assert torch.equal(y, s.to(kind))
+    n, k = width(0, 1)
+    w, ws = whole(g, E, n, k), space(rows, E, n, k)
+    s = grouped(a, w, b, lambda u, v: u @ v.T)
+    z, y = torch.empty((rows, n), device=DEV, dtype=BF16), torch.empty((rows, n // 2), device=DEV, dtype=BF16)
+    mep.moe_expert_linear(rows, E, n, k, a, off, w, None, 4, None, z, y, mep.MOE_BF16, ws)
+    want = value64("swiglu", s)
+    assert torch.equal(z, s.to(BF16))
+    assert bool(((y.double() - want).abs() <= (HALF[BF16] + EPI) * want.abs() + 1e-30).all())
+    n, k = width(1, 0)
+    w, ws = whole(g, E, n, k), space(rows, E, n, k)
+    s = grouped(a, w, b, lambda u, v: u @ v)
+    for kind in (BF16, F32):
+        dx = torch.empty((rows, k), device=DEV, dtype=kind)
+        mep.moe_expert_linear_grad_input(rows, E, n, k, a, off, w, 0, None, None, dx, KIND[kind], ws)
+        assert torch.equal(dx, s.to(kind))
+    n, k = width(2, 0)
+    dz, ws = whole(g, rows, n), space(rows, E, n, k)
+    for bias in (True, False):
+        dw, db = torch.empty((E, n, k), device=DEV, dtype=BF16), torch.empty((E, n), device=DEV)
+        mep.moe_expert_linear_grad_weight(rows, E, n, k, dz, a, off, dw, mep.MOE_BF16, db if bias else None, ws)
+        for e in range(E):
+            d, x = dz[b[e]:b[e + 1]].double(), a[b[e]:b[e + 1]].double()
+            assert torch.equal(dw[e], (d.T @ x).to(BF16)), e
+            assert not bias or torch.equal(db[e].double(), d.sum(0)), e
 
 
 def form_of(kind, gated, rows, E, n, k):
