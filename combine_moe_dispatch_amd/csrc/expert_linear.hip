@@ -672,30 +672,10 @@ __device__ __forceinline__ void hand_over_gated(const Sums<C>& sums, int u_rows,
 // its stores are whole lines (four lanes of 16 bytes from the sums' own layout
 // are half lines), its code is that of one such part, and what the next part
 // reads from memory is on its way meanwhile.
-template <class C, bool GATED, bool BIAS, class Tiles>
-__device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows, uint8_t* lds, int wave, int lane,
-                                          Tiles& tiles)
+template <class C, bool GATED, class Tiles>
+__device__ __forceinline__ void hand_over_rows(const Sums<C>& sums, int u_rows, int v_rows, float* part, int wm, int wn, int lane,
+                                               Tiles& tiles)
 {
-    static_assert(C::NT == 4, "a wave has 64 rows of V");
-    const int wm = wave % C::WM, wn = wave / C::WM;
-    float* const part = (float*)(lds + wave * 4096);
-    if constexpr (BIAS)
-        if (sums.mine)
-#pragma unroll
-            for (int i = 0; i < Sums<C>::ALONE; ++i) {
-                const int u = C::u_row_of(wn * Sums<C>::ALONE + i, wm) + lane;
-                if (wn * Sums<C>::ALONE + i < C::MT && lane < 16 && u < u_rows)
-                    tiles.finish_bias(u, sums.alone[i][0]);
-            }
-    if (!GATED && tiles.plain()) {
-        hand_over_plain(sums, u_rows, v_rows, (uint16_t*)part, wm, wn, lane, tiles);
-        return;
-    }
-    if constexpr (GATED)
-        if (tiles.plain_gated()) {
-            hand_over_gated(sums, u_rows, v_rows, lds, wave, lane, tiles);
-            return;
-        }
     constexpr int PASSES = GATED ? 1 : 2;            // by 8 (GATED: 16) rows of U
     // 16-byte piece q of row r lies at place q ^ r: rows apart in the banks both ways
     auto place = [&](int row, int q) { return part + row * 64 + ((q ^ row) << 2); };
@@ -732,16 +712,6 @@ __device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows,
 #pragma unroll
         for (int q = 0; q < PASSES; ++q) {
             const int row = q * 8 + row0, u = C::u_row_of(i, wm) + row;
-            if (tiles.apart()) {                     // fp32: four and four, so that stores are whole lines
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const v4f x = *(const v4f*)place(row, h * 8 + col);
-                    const int at = wn * 64 + h * 32 + col * 4;
-                    if (u < u_rows && at < v_rows)
-                        tiles.finish4(u, at, x);
-                }
-                continue;
-            }
             float a[8], b[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -761,6 +731,68 @@ __device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows,
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+}
+
+// fp32 outputs that nothing is done to, of the weights' gradient: four and four of a lane's lie 32
+// apart, so that stores are whole lines.
+template <class C, class Tiles>
+__device__ __forceinline__ void hand_over_fp32(const Sums<C>& sums, int u_rows, int v_rows, float* part, int wm, int wn, int lane,
+                                               Tiles& tiles)
+{
+    auto place = [&](int row, int q) { return part + row * 64 + ((q ^ row) << 2); };
+    const int row0 = lane >> 3, col = lane & 7;
+#pragma unroll 1
+    for (int i = 0; i < C::MT; ++i) {
+#pragma unroll
+        for (int s = 0; s < C::MT; ++s)
+            if (s == i)
+#pragma unroll
+                for (int j = 0; j < C::NT; ++j)
+                    *(v4f*)place(lane & 15, j * 4 + (lane >> 4)) = sums.acc[j][s];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = q * 8 + row0, u = C::u_row_of(i, wm) + row;
+                const v4f x = *(const v4f*)place(row, h * 8 + col);
+                const int v = wn * 64 + h * 32 + col * 4;
+                if (u < u_rows && v < v_rows)
+                    tiles.finish4(u, v, x);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// A tile's sums to its outputs.
+template <class C, bool GATED, bool BIAS, class Tiles>
+__device__ __forceinline__ void hand_over(Sums<C>& sums, int u_rows, int v_rows, uint8_t* lds, int wave, int lane,
+                                          Tiles& tiles)
+{
+    static_assert(C::NT == 4, "a wave has 64 rows of V");
+    const int wm = wave % C::WM, wn = wave / C::WM;
+    float* const part = (float*)(lds + wave * 4096);
+    if constexpr (BIAS)
+        if (sums.mine)
+#pragma unroll
+            for (int i = 0; i < Sums<C>::ALONE; ++i) {
+                const int u = C::u_row_of(wn * Sums<C>::ALONE + i, wm) + lane;
+                if (wn * Sums<C>::ALONE + i < C::MT && lane < 16 && u < u_rows)
+                    tiles.finish_bias(u, sums.alone[i][0]);
+            }
+    if (!GATED && tiles.plain()) {
+        hand_over_plain(sums, u_rows, v_rows, (uint16_t*)part, wm, wn, lane, tiles);
+        return;
+    }
+    if constexpr (GATED)
+        if (tiles.plain_gated()) {
+            hand_over_gated(sums, u_rows, v_rows, lds, wave, lane, tiles);
+            return;
+        }
+    if constexpr (Tiles::ROWS)
+        hand_over_rows<C, GATED>(sums, u_rows, v_rows, part, wm, wn, lane, tiles);
+    else
+        hand_over_fp32(sums, u_rows, v_rows, part, wm, wn, lane, tiles);
 }
 
 // The product of one tile, with S stages of both operands in LDS: for tiles of which two workgroups
@@ -1034,7 +1066,7 @@ __device__ inline void split_range(int64_t total, int splits, int s, int64_t& t0
 // forward and grad_input: out rows are the token rows
 template <Kind KIND, class C, bool GATED>
 struct RowTiles {
-    static constexpr bool FWD = KIND == Kind::FORWARD;
+    static constexpr bool ROWS = true, FWD = KIND == Kind::FORWARD;
     int n_tiles, splits;
     Place at;
     Linear args;              // (read once: through the epilogue's loop they stay in scalar registers)
@@ -1089,8 +1121,6 @@ struct RowTiles {
         whole(row, col, a, b, e, bias);
     }
     __device__ inline void finish_bias(int, float) const {}
-    static __device__ constexpr bool apart() { return false; }
-    __device__ inline void finish4(int, int, v4f) const {}
     __device__ inline bool plain() const
     {
         const Linear& p = args;
@@ -1132,6 +1162,7 @@ __global__ __launch_bounds__(C::THREADS) void linear_kernel(const Linear p, int 
 // grad_weight: out rows are an expert's weight rows
 template <class C>
 struct WeightTiles {
+    static constexpr bool ROWS = false;
     int m_tiles, n_tiles, splits;
     struct Spot {
         int e, m, n;
@@ -1165,21 +1196,16 @@ struct WeightTiles {
     }
     __device__ inline void begin_finish() { args = &arguments(); }
     __device__ inline bool with_bias() const { return at.n == 0; }
-    __device__ inline Extra fetch(int, int) const { return Extra{}; }
-    __device__ inline void fetch_bias(int, v4u (&)[2]) const {}
-    // outputs that are fp32, the split sums' too, go out as whole lines
-    __device__ inline bool apart() const { return splits > 1 || args->out_f32; }
     __device__ inline int64_t out_at(const Linear& p, int u, int v) const
     {
         return ((int64_t)at.e * p.n + at.m * C::BM + u) * p.k + at.n * C::BN + v;
     }
-    __device__ inline bool plain() const { return !apart(); }
+    __device__ inline bool plain() const { return splits == 1 && !args->out_f32; }
     __device__ inline void finish_plain(int u, int v, v4u o) const
     {
         const Linear& p = *args;
         store_past((uint16_t*)p.out + out_at(p, u, v), o);
     }
-    __device__ inline void finish(int, int, float (&)[8], float (&)[8], const Extra&, const v4u (&)[2]) const {}
     __device__ inline void finish4(int u, int v, v4f o) const
     {
         const Linear& p = *args;
