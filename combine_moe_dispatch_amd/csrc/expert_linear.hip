@@ -1570,7 +1570,10 @@ constexpr Cost COSTS[] = {
     {Form::T32W, 32, 256, 2, 1.22f, 1.7f, 0.54f},  {Form::T32, 32, 128, 2, 0.49f, 2.2f, 0.54f},
 };
 
-Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
+// f32: of the weights' gradient, whose tiles cost more in fp32, the more the smaller they are (256
+// experts of 128 rows, 2048 x 1024: 256 x 256 529 us, 128 x 256 572, 128 x 128 676; in bf16, 64 rows, 1024 x 1024: 139,
+// 156 and 140).
+Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k, bool f32 = false)
 {
     const bool weight = kind == Kind::WEIGHT;
     if (weight && rows <= (int64_t)FEW_MEAN * E && k >= FEW_COLS / 2 && (int64_t)E * n * k >= FEW_LEAST) {
@@ -1587,7 +1590,7 @@ Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
     const int64_t total = kind == Kind::FORWARD ? k : kind == Kind::INPUT ? n : rows / E;
     const int steps = (int)std::max<int64_t>((total + STEP - 1) / STEP, 1);
     const float outputs = weight ? (float)E * n * k : (float)rows * width;
-    const float bytes = 2.0f * ((weight ? (float)E : used) * n * k + (float)rows * n + (float)rows * k);
+    const float bytes = 2.0f * ((weight ? (f32 ? 2.0f : 1.0f) * E : used) * n * k + (float)rows * n + (float)rows * k);
     float best = 0.0f;
     const Cost* form = nullptr;
     int best_splits = 1;
@@ -1606,7 +1609,9 @@ Plan plan_of(Kind kind, bool gated, int64_t rows, int E, int n, int k)
             const float rounds =
                 std::max(1.0f, counted ? std::ceil(load) : load <= 3.0f ? std::ceil(1.05f * load) : load + 0.5f);
             const float step = (load <= 0.5f ? 0.66f : 1.0f) * (weight ? 0.82f : 1.0f) * c.step;
-            const float tile = (weight ? 1.17f : 1.0f) * c.tile;
+            float tile = (weight ? 1.17f : 1.0f) * c.tile;
+            if (f32 && splits == 1)
+                tile += (c.bm == 256 ? 1.0e-4f : 1.5e-4f) * c.per_cu * c.bm * c.bn;
             float us = rounds * ((steps + splits - 1) / splits * step + tile);
             if (splits > 1)
                 us += 4.5f + splits * outputs * 1.2e-6f;                     // 8 bytes at 6.75 TB/s
@@ -1671,7 +1676,7 @@ hipError_t launch_weight(const Linear& p, const Plan& s, hipStream_t stream)
 
 const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k, int* splits)
 {
-    const Plan s = plan_of((Kind)kind, gated, rows, E, n, k);
+    const Plan s = plan_of((Kind)std::min(kind, 2), gated, rows, E, n, k, kind == 3);
     *splits = s.splits;
     static const char* const names[] = {"256 x 256", "128 x 256", "128 x 128", "64 x 128", "32 x 256", "32 x 128", "few rows"};
     return names[(int)s.form];
@@ -1680,7 +1685,8 @@ const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k,
 size_t linear_workspace(int64_t rows, int E, int n, int k)
 {
     const int64_t weights = (int64_t)E * n * (k + 1);
-    size_t most = parts(plan_of(Kind::WEIGHT, false, rows, E, n, k), weights);
+    size_t most = std::max(parts(plan_of(Kind::WEIGHT, false, rows, E, n, k), weights),
+                           parts(plan_of(Kind::WEIGHT, false, rows, E, n, k, true), weights));
     most = std::max(most, parts(plan_of(Kind::INPUT, false, rows, E, n, k), rows * k));
     most = std::max(most, parts(plan_of(Kind::FORWARD, false, rows, E, n, k), rows * n));
     if (n % 16 == 0)
@@ -1701,7 +1707,7 @@ hipError_t launch_linear_grad_input(const Linear& p, hipStream_t stream)
 
 hipError_t launch_linear_grad_weight(const Linear& p, hipStream_t stream)
 {
-    const Plan s = plan_of(Kind::WEIGHT, false, p.rows, p.E, p.n, p.k);
+    const Plan s = plan_of(Kind::WEIGHT, false, p.rows, p.E, p.n, p.k, p.out_f32);
     if (s.form == Form::FEW) {
         linear_weight_few_kernel<<<grid_of(s.groups), dim3(256), 0, stream>>>(p, s.m_tiles, s.n_tiles);
         return hipGetLastError();

@@ -109,7 +109,7 @@ struct Linear {
 };
 
 // The tile and splits that a call takes (kind 0 the product, 1 the gradient to
-// its input, 2 to its weights), for the tests.
+// its input, 2 to its weights, 3 in fp32), for the tests.
 const char* linear_form(int kind, bool gated, int64_t rows, int E, int n, int k, int* splits);
 size_t linear_workspace(int64_t rows, int E, int n, int k);
 hipError_t launch_linear(const Linear& p, hipStream_t stream);

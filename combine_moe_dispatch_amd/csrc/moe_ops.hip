@@ -201,7 +201,7 @@ const char* moe_ops_few_token_form(int32_t num_tokens, int32_t num_experts, int3
 const char* moe_ops_linear_form(int32_t kind, int32_t gated, int32_t rows, int32_t num_experts, int32_t n, int32_t k,
                                 int32_t* splits)
 {
-    if (kind < 0 || kind > 2 || !linear_sizes(rows, num_experts, n, k) || (gated && (kind != 0 || n % 16 != 0)))
+    if (kind < 0 || kind > 3 || !linear_sizes(rows, num_experts, n, k) || (gated && (kind != 0 || n % 16 != 0)))
         return "";
     return moe::ops::linear_form(kind, gated != 0, rows, num_experts, n, k, splits);
 }

@@ -428,30 +428,34 @@ def test_offsets_out_of_order():
 
 
 
-# (tile, splits, product / to the input / to the weights, gated, rows, E, n, k): every tile with
+# (tile, splits, product / to the input / to the weights / in fp32, gated, rows, E, n, k): every tile with
 # and without splits, long enough for its steady loop, most with a tail and ragged experts
 FORMS = [
-    ("128 x 128", 1, 0, 0, 3457, 16, 1600, 480), ("128 x 128", 8, 0, 0, 4055, 5, 16, 3832),
-    ("128 x 128", 1, 0, 1, 3393, 3, 1072, 472), ("128 x 128", 8, 0, 1, 4195, 3, 16, 3704),
-    ("128 x 128", 1, 1, 0, 4450, 2, 608, 816), ("128 x 128", 8, 1, 0, 3864, 3, 3920, 8),
-    ("128 x 128", 1, 2, 0, 3847, 8, 2128, 144), ("128 x 256", 1, 0, 0, 2437, 2, 1632, 480),
-    ("128 x 256", 8, 0, 0, 2067, 8, 144, 4464), ("128 x 256", 1, 0, 1, 3749, 8, 960, 480),
-    ("128 x 256", 8, 0, 1, 2055, 1, 144, 4680), ("128 x 256", 1, 1, 0, 3620, 3, 464, 1040),
-    ("128 x 256", 8, 1, 0, 2286, 5, 3888, 136), ("128 x 256", 1, 2, 0, 2583, 5, 3728, 136),
-    ("256 x 256", 1, 0, 0, 2159, 5, 3504, 480), ("256 x 256", 1, 0, 1, 3673, 8, 1968, 472),
-    ("256 x 256", 1, 1, 0, 3989, 16, 464, 1696), ("256 x 256", 1, 2, 0, 3749, 8, 2912, 272),
-    ("32 x 128", 1, 0, 0, 13, 2, 16, 472), ("32 x 128", 8, 0, 0, 11, 2, 16, 3632),
-    ("32 x 128", 1, 0, 1, 18, 2, 16, 456), ("32 x 128", 8, 0, 1, 19, 2, 16, 3704),
-    ("32 x 128", 1, 1, 0, 8, 2, 464, 8), ("32 x 128", 8, 1, 0, 9, 2, 3616, 8), ("32 x 128", 1, 2, 0, 907, 2, 16, 8),
-    ("32 x 128", 4, 2, 0, 3714, 2, 1072, 8), ("32 x 256", 1, 0, 0, 227, 64, 904, 472),
-    ("32 x 256", 1, 0, 1, 540, 16, 3984, 520),
-    ("32 x 256", 1, 1, 0, 30, 16, 480, 3904), ("32 x 256", 1, 2, 0, 4703, 8, 80, 4176),
-    ("64 x 128", 1, 0, 0, 4172, 8, 160, 776), ("64 x 128", 8, 0, 0, 2172, 3, 16, 3672),
-    ("64 x 128", 1, 0, 1, 4193, 5, 144, 848), ("64 x 128", 8, 0, 1, 1944, 2, 16, 4176),
-    ("64 x 128", 1, 1, 0, 4456, 3, 736, 144), ("64 x 128", 4, 1, 0, 3917, 3, 1904, 8),
-    ("64 x 128", 1, 2, 0, 2463, 5, 3616, 8), ("64 x 128", 8, 2, 0, 4020, 1, 2112, 8),
-    ("few rows", 1, 2, 0, 30, 8, 2048, 1032), ("few rows", 1, 2, 0, 19, 5, 4096, 1000),
-    ("few rows", 1, 2, 0, 3, 1, 4104, 4096)]
+    ("128 x 128", 1, 0, 0, 2746, 3, 1328, 456), ("128 x 128", 8, 0, 0, 4287, 5, 16, 3800),
+    ("128 x 128", 1, 0, 1, 4356, 3, 784, 592), ("128 x 128", 8, 0, 1, 3735, 5, 16, 3664),
+    ("128 x 128", 1, 1, 0, 1536, 16, 464, 2856), ("128 x 128", 8, 1, 0, 4621, 2, 3696, 8),
+    ("128 x 128", 1, 2, 0, 3752, 8, 2288, 136), ("128 x 128", 1, 3, 0, 2286, 5, 3888, 136),
+    ("128 x 256", 1, 0, 0, 4009, 3, 960, 480), ("128 x 256", 8, 0, 0, 1794, 16, 144, 4776),
+    ("128 x 256", 1, 0, 1, 4015, 2, 912, 464), ("128 x 256", 8, 0, 1, 2803, 1, 144, 4976),
+    ("128 x 256", 1, 1, 0, 3646, 8, 464, 912), ("128 x 256", 4, 1, 0, 4219, 5, 3808, 160),
+    ("128 x 256", 1, 2, 0, 2801, 5, 3760, 136), ("128 x 256", 1, 3, 0, 3056, 5, 3360, 152),
+    ("128 x 256", 4, 3, 0, 3717, 1, 3440, 272), ("256 x 256", 1, 0, 0, 3800, 8, 2000, 464),
+    ("256 x 256", 1, 0, 1, 4255, 3, 1680, 544), ("256 x 256", 1, 1, 0, 1607, 2, 480, 4880),
+    ("256 x 256", 1, 2, 0, 3794, 8, 2752, 312), ("256 x 256", 1, 3, 0, 3635, 8, 2976, 264),
+    ("32 x 128", 1, 0, 0, 8, 2, 16, 456), ("32 x 128", 8, 0, 0, 15, 2, 16, 3696),
+    ("32 x 128", 1, 0, 1, 10, 2, 16, 456), ("32 x 128", 8, 0, 1, 18, 2, 16, 3664),
+    ("32 x 128", 1, 1, 0, 12, 2, 464, 8), ("32 x 128", 8, 1, 0, 9, 2, 3888, 8), ("32 x 128", 1, 2, 0, 926, 2, 16, 8),
+    ("32 x 128", 4, 2, 0, 3903, 2, 1136, 8), ("32 x 128", 1, 3, 0, 907, 2, 16, 8),
+    ("32 x 128", 4, 3, 0, 3632, 2, 1056, 8), ("32 x 256", 1, 0, 0, 469, 16, 3904, 488),
+    ("32 x 256", 1, 0, 1, 96, 16, 4048, 496), ("32 x 256", 1, 1, 0, 34, 16, 464, 4168),
+    ("32 x 256", 1, 2, 0, 3941, 8, 80, 4512), ("32 x 256", 1, 3, 0, 3939, 8, 80, 4992),
+    ("64 x 128", 1, 0, 0, 4172, 8, 160, 776), ("64 x 128", 8, 0, 0, 2129, 2, 16, 3808),
+    ("64 x 128", 1, 0, 1, 4606, 2, 144, 728), ("64 x 128", 4, 0, 1, 3981, 2, 16, 1808),
+    ("64 x 128", 1, 1, 0, 4550, 2, 752, 144), ("64 x 128", 4, 1, 0, 3858, 5, 1840, 8),
+    ("64 x 128", 1, 2, 0, 3692, 8, 2128, 8), ("64 x 128", 8, 2, 0, 3896, 1, 2240, 8),
+    ("64 x 128", 1, 3, 0, 2481, 5, 3488, 8), ("64 x 128", 4, 3, 0, 4476, 2, 3200, 8),
+    ("few rows", 1, 2, 0, 30, 8, 2048, 1032), ("few rows", 1, 3, 0, 19, 5, 4096, 1000),
+    ("few rows", 1, 2, 0, 3, 1, 4104, 4096), ("few rows", 1, 3, 0, 3, 1, 4104, 4096)]
 
 
 @pytest.mark.parametrize("last", [1, 127, 128, 129, 255])
@@ -543,9 +547,10 @@ def test_forms(form, splits, kind, gated, rows, E, n, k):
         assert torch.equal(dx[:used].double(), grouped(dz, w, b, lambda a, v: a @ v)) and bool((dx[used:] == 9).all())
     else:
         for bias in (True, False):
-            dw, db = torch.full((E, n, k), 9.0, device=DEV), torch.full((E, n), 9.0, device=DEV)
-            mep.moe_expert_linear_grad_weight(rows, E, n, k, dz, x, off, dw, mep.MOE_FP32, db if bias else None, ws)
+            out = F32 if kind == 3 else BF16
+            dw, db = torch.full((E, n, k), 9.0, device=DEV, dtype=out), torch.full((E, n), 9.0, device=DEV)
+            mep.moe_expert_linear_grad_weight(rows, E, n, k, dz, x, off, dw, KIND[out], db if bias else None, ws)
             for e in range(E):
                 d, a = dz[b[e]:b[e + 1]].double(), x[b[e]:b[e + 1]].double()
-                assert torch.equal(dw[e].double(), d.T @ a), e
+                assert torch.equal(dw[e], (d.T @ a).to(out)), e
                 assert not bias or torch.equal(db[e].double(), d.sum(0)), e

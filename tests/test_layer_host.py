@@ -133,7 +133,7 @@ def _form(kind, gated, rows, E, n, k):
     (("256 x 256", 1), (0, 1, 32768, 16, 4096, 7168)), (("256 x 256", 1), (1, 0, 32768, 16, 7168, 2048)),
     (("256 x 256", 1), (2, 0, 32768, 16, 7168, 2048)), (("64 x 128", 1), (0, 0, 1000, 1, 4096, 4096)),
     (("32 x 128", 1), (0, 0, 37, 8, 1000, 392)), (("few rows", 1), (2, 0, 64, 64, 4096, 2048)),
-    (("", 0), (3, 0, 4, 1, 256, 256)), (("", 0), (1, 1, 4, 1, 256, 256)), (("", 0), (0, 1, 4, 1, 264, 256)),
+    (("", 0), (4, 0, 4, 1, 256, 256)), (("", 0), (1, 1, 4, 1, 256, 256)), (("", 0), (0, 1, 4, 1, 264, 256)),
     (("", 0), (0, 0, 4, 1, 260, 256)), (("", 0), (0, 0, 4, 0, 256, 256))])
 def test_linear_forms(want, args):
     assert _form(*args) == want
@@ -144,6 +144,7 @@ def test_workspace_serves_every_call():
     for rows, E, n, k in [(128, 1, 256, 7168), (64, 1, 4096, 4096), (2000, 8, 4096, 2048), (1, 1, 16, 65536),
                           (5000, 1, 256, 256), (3641, 1, 16, 8), (7, 3, 48, 4096)]:
         size = mep.moe_expert_linear_workspace(rows, E, n, k)
-        for kind, gated, outputs in [(0, 0, rows * n), (0, 1, rows * n), (1, 0, rows * k), (2, 0, E * n * (k + 1))]:
+        for kind, gated, outputs in [(0, 0, rows * n), (0, 1, rows * n), (1, 0, rows * k), (2, 0, E * n * (k + 1)),
+                                     (3, 0, E * n * (k + 1))]:
             _, splits = _form(kind, gated, rows, E, n, k)
             assert splits == 1 or size >= splits * outputs * 4, (rows, E, n, k, kind)
