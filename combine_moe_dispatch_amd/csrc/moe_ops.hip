@@ -1,6 +1,6 @@
-// Entry points of the operators around dispatch and combine (include/moe_ep.h,
-// "Operators around dispatch and combine"): argument validation and launches
-// on the caller's stream.
+// Entry points of the operators around dispatch and combine and of the expert
+// layer on one card (include/moe_ep.h, under these headings): argument validation
+// and launches on the caller's stream.
 #include "moe_ops.h"
 
 #include <rocprofiler-sdk-roctx/roctx.h>
