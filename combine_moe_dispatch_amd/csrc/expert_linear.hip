@@ -96,12 +96,16 @@ __device__ inline Buffer buffer_of(const void* base, uint32_t bytes)
 // LDS, 1 KB from `lds` on.  The compiler does not see this as a memory access:
 // told of it, it would wait for all such loads ahead of every transposing LDS
 // read.  They are waited for by meet() alone, and stay between the two that
-// enclose them (volatile statements keep their order).
+// enclose them (volatile statements keep their order).  The memory unit may read
+// a scalar register five wait states after a vector instruction wrote it, as
+// buffer_of's may just have done, and one after m0 was written; nothing holds it
+// back, and the compiler counts wait states only for instructions it knows.  So
+// they are here: one of the move, four of the s_nop.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"      // m0, a reserved register, is named as overwritten
 __device__ inline void load_to_lds(Buffer b, uint32_t offset, uint32_t more, const uint8_t* lds)
 {
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(b),
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(offset), "s"(b),
                  "s"(more), "s"((uint32_t)(uintptr_t)(lvoid*)lds)
                  : "m0");
 }
