@@ -1404,10 +1404,12 @@ __global__ __launch_bounds__(256) void join_weight_kernel(const Linear p, int sp
 // rounded the other way counts more than all of their own roundings (one in
 // 50000 values, 2^-8 of itself).  So the slopes are the formulas' elementary
 // operations in fp32 in the order written here, each rounded once and none fused:
-// whoever forms them so gets the same bf16 numbers.  Off by a few roundings of
-// 2^-24 of |dy|; GELU's lower tail, 1 + erf, is exact to 2^-24 absolutely.  The
-// vector unit bounds them: 32768 x 4096 GELU 190 us, SILU 158, SWIGLU 122, 4.2 to
-// 5.5 TB/s.
+// whoever forms them so gets the same bf16 numbers.  Not so GELU's below -2:
+// there 1 + erf has lost what it is off by, 2^-24 of 1, which is 13 of 2^-24 of the
+// slope at -2, 3% at -6, and the lower tail is formed as in the products'
+// epilogues.  So each slope is off by a few roundings of 2^-24 of its two parts.
+// The vector unit bounds them: 32768 x 4096 GELU 212 us (190 without the tail), SILU
+// 154, SWIGLU 118, 3.8 to 5.7 TB/s.
 __device__ inline float logistic_by_steps(float z)
 {
 #pragma clang fp contract(off)
@@ -1422,8 +1424,11 @@ __device__ inline float silu_grad_by_steps(float d, float z, float p)
 __device__ inline float gelu_grad_by_steps(float d, float z)
 {
 #pragma clang fp contract(off)
-    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
-    return d * (cdf + z * expf(-0.5f * z * z) * 0.39894228040143268f);
+    const float e = expf(-0.5f * z * z);             // (z is bf16: its square is exact)
+    float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+    if (z < -2.0f)
+        cdf = normal_cdf(z, e);
+    return d * (cdf + z * e * 0.39894228040143268f);
 }
 
 __global__ __launch_bounds__(256) void activation_grad_kernel(const Linear p, const uint16_t* dy)
