@@ -509,7 +509,7 @@ __device__ inline void expert_rows(const Linear& p, int e, int64_t& a, int64_t& 
 // One tile's product.
 struct Work {
     Side us, vs;              // of as many terms
-    __device__ inline int steps() const { return (us.terms + (STEP - 1)) / STEP; }
+    __device__ inline int steps() const { return parts_of(us.terms, STEP); }
 };
 
 // LDS rows of V's subtiles: the wave's first, and how far below it subtile j is; gated tiles
@@ -1179,7 +1179,7 @@ struct WeightTiles {
         int64_t t;
         if (!tile_of_id<TURNS<C>>(id, (int64_t)p.E * m_tiles * n_tiles, t))
             return false;
-        const int per = m_tiles * n_tiles;                   // 2^16 at most
+        const int per = m_tiles * n_tiles;                   // 2^20 at most (32 x 128 tiles of 65536 x 65536)
         at.e = (int)(t / per);
         tile_in_group(t - (int64_t)at.e * per, m_tiles, n_tiles, at.m, at.n);
         int64_t a, b;

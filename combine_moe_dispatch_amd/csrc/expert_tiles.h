@@ -37,6 +37,16 @@ __device__ inline void wait_loads_and_meet()
 // bytes, so that the 16 rows a fragment reads at once spread over the banks.
 __device__ inline int swizzle(int r) { return (r >> 1) & 7; }
 
+// How many parts of `size` (the last one smaller) n >= 0 indices have.  An expert
+// may have nearly 2^31 rows: what is added to them passes that.
+__host__ __device__ constexpr int parts_of(int n, int size)
+{
+    return (int)(((uint32_t)n + (uint32_t)(size - 1)) / (uint32_t)size);
+}
+static_assert(parts_of(0, 64) == 0 && parts_of(1, 64) == 1 && parts_of(64, 64) == 1 && parts_of(65, 64) == 2 &&
+                  parts_of(INT32_MAX, 64) == 1 << 25 && parts_of(INT32_MAX, 256) == 1 << 23,
+              "up to the most rows");
+
 struct Place {
     int e, m0, rows;          // expert, first row of the tile, rows of the tile (> 0)
     int n_tile;
@@ -87,7 +97,7 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     for (int i = 0; i <= PER; ++i) {
         o[i] = min(max(o[i], 0), rmax);
         if (i > 0)
-            mine += max(o[i] - o[i - 1] + BM - 1, 0) / BM;
+            mine += parts_of(max(o[i] - o[i - 1], 0), BM);
     }
     const int upto = wave_scan(mine);
     const int64_t tiles = (int64_t)__builtin_amdgcn_readlane(upto, WAVE - 1) * n_tiles;
@@ -97,7 +107,7 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
     // the lane whose experts hold the tile, and there the expert
     const int src = __popcll(__ballot((int64_t)upto * n_tiles <= t));
     int64_t u = t - (int64_t)(upto - mine) * n_tiles;
-    int e = lane * per, a = o[0], b = o[1], m_tiles = max(b - a + BM - 1, 0) / BM;
+    int e = lane * per, a = o[0], b = o[1], m_tiles = parts_of(max(b - a, 0), BM);
 #pragma unroll
     for (int i = 1; i < PER; ++i)
         if (u >= (int64_t)m_tiles * n_tiles) {
@@ -105,12 +115,12 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
             e = lane * per + i;
             a = o[i];
             b = o[i + 1];
-            m_tiles = max(b - a + BM - 1, 0) / BM;
+            m_tiles = parts_of(max(b - a, 0), BM);
         }
     out.e = __builtin_amdgcn_readlane(e, src);
     a = __builtin_amdgcn_readlane(a, src);
     b = __builtin_amdgcn_readlane(b, src);
-    m_tiles = (b - a + BM - 1) / BM;
+    m_tiles = parts_of(max(b - a, 0), BM);
     const int64_t v = (int64_t)__builtin_amdgcn_readlane((int)(u >> 32), src) << 32 |
                       (uint32_t)__builtin_amdgcn_readlane((int)u, src);
     // (ascending offsets always pass; others, whose tiles may be beyond counting,
