@@ -100,7 +100,8 @@ __device__ inline Buffer buffer_of(const void* base, uint32_t bytes)
 // a scalar register five wait states after a vector instruction wrote it, as
 // buffer_of's may just have done, and one after m0 was written; nothing holds it
 // back, and the compiler counts wait states only for instructions it knows.  So
-// they are here: one of the move, four of the s_nop.
+// they are here: one of the move, four of the s_nop (four more cost 1 to 1.5% of a
+// large product: 16 experts, 32768 rows, 4096 x 7168 through SWIGLU 1572 and 1596 us).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"      // m0, a reserved register, is named as overwritten
 __device__ inline void load_to_lds(Buffer b, uint32_t offset, uint32_t more, const uint8_t* lds)
@@ -881,9 +882,10 @@ __device__ __forceinline__ void sum_tile(const Work& w, uint8_t* lds, int wave, 
 // everything, one step).  A phase issues four loads, one beside every eight
 // products: two of the half of U that the phase before it was the last to read,
 // and half of V's, whose slot was free before.  What bounds it is the matrix unit under
-// the card's power limit (its clock falls to some 2 GHz): 8192 x 8192 x 8192 takes
-// 720 to 815 us forward (1350 to 1530 TFLOP/s; the library 750 to 770 us), 727 to 745 to
-// the input (852) and 743 to 757 to the weights (958).  A tile costs about 8 us beside
+// the card's power limit: by the counters it is busy in 70 to 75% of the cycles, at a
+// clock that falls to 1.6 to 1.8 GHz.  8192 x 8192 x 8192 takes 750 to 830 us forward
+// (1320 to 1465 TFLOP/s; the library 670 to 770 us, by card and what ran before), 737 to
+// 762 to the input (782 to 873) and 760 to 775 to the weights (902 to 985).  A tile costs about 8 us beside
 // its steps of 1.4: finding it, the first loads and the epilogue, which nothing hides
 // where one workgroup fills a CU.  Tried and slower or the same: 32 x 32 x 16 products
 // (4%), a persistent workgroup that loads its next tile during the epilogue (forward
@@ -1247,7 +1249,11 @@ __global__ __launch_bounds__(C::THREADS) void linear_weight_kernel(const Linear 
 // 237 with 4, 197 against 241 with 6, 227 against 241 with 8, where the vector
 // unit's multiply-adds are what bounds it (8 ragged rows each of 8 experts of 4096
 // x 4096 63 to 72 against 61 to 64); of small gradients the latencies (16 experts of
-// 6 rows, 1000 x 384 14 us against 8).
+// 6 rows, 1000 x 384 14 us against 8).  The choice is by the mean, since the host
+// does not know the rows: an expert that holds many of them goes through its rows in
+// the few workgroups of its own weights.  448 rows of 64 experts, 4096 x 2048, 202 us
+// with 7 rows each, 436 with 385 of them on one; 512 x 2048 34 and, all on one, 323;
+// 7168 rows of 1024 experts, 512 x 512, 116 and, all on one, 6900.
 constexpr int FEW_ROWS = 8, FEW_COLS = 512, FEW_N = 64;
 constexpr int FEW_MEAN = 7;                      // rows per expert
 constexpr int64_t FEW_LEAST = 1 << 24;           // weights
@@ -1567,6 +1573,8 @@ void set_tiles(Plan& s, Form form, Kind kind, bool gated, int64_t rows, int E, i
 //    2048 57 against 64;
 //  - splits: 128 rows, 256 x 7168 in 1, 4, 8, 16 splits 20, 13.6, 11.6, 11.7; 64
 //    rows, 4096 x 4096 in 1, 2, 4, 8 24, 14.5, 13.1, 14.9.
+// Eight splits at most leave CUs idle where a small gradient to the weights sums
+// many rows: 64 x 64 of 32768 rows 27 us, of 131072 89, for 8 and 34 MB.
 struct Cost {
     Form form;
     int bm, bn, per_cu;

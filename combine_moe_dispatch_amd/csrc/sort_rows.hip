@@ -297,7 +297,10 @@ __global__ __launch_bounds__(256) void unsort_rows_kernel(const Rows r)
 // while its K rows go by, GRAD_AHEAD of them in flight; a dot product is summed
 // per lane, over the lanes, then over the waves in their order.  Rows are read and written once:
 // 16384 tokens of 7168, 8 rows each, 793 us, 5.0 TB/s, where a copy reaches 6.6: as for the sort,
-// what is written jumps from row to row.
+// what is written jumps from row to row.  Rows of more than 32 wave-wide vectors (fp32 from 8200 on, bf16
+// from 16392) take U = 16, whose registers spill (184 bytes of scratch per lane, bf16 656): 8192
+// tokens of fp32, 4 rows each, 426 us of 8192 and 671 of 8200 (5.7, 3.6 TB/s); 4096 of bf16 213 us of
+// 16384 and 1082 of 16392 (5.7, 1.1 TB/s).
 constexpr int GRAD_AHEAD = 4;
 
 template <int LANES, int U, bool F32, bool STREAM>

@@ -493,13 +493,14 @@ int moe_few_token_layer(int32_t num_tokens, int32_t num_experts, int32_t top_k, 
  *
  * Where one card holds all experts of its tokens nothing has to be
  * dispatched: the tokens' rows are sorted by expert, go through bf16 products
- * and come back weighted.  These operators are that, with the gradients:
- * norm, moe_expert_linear (the router's logits), moe_topk_route,
- * moe_sort_plan, moe_sort_rows, moe_expert_linear twice, moe_unsort_rows; and
- * backwards moe_unsort_rows_grad, moe_expert_linear_grad_input and
- * _grad_weight, moe_unsort_rows (the gradient of the sorted rows),
- * moe_topk_route_grad.  moe_sort_rows also carries e4m3 rows, which
- * moe_expert_gate_up and moe_expert_matmul read.  Conventions as above.
+ * and come back weighted.  These operators are that, with the gradients
+ * (behind a norm, which has none here): moe_expert_linear (the router's
+ * logits), moe_topk_route, moe_sort_plan, moe_sort_rows, moe_expert_linear
+ * twice, moe_unsort_rows; and backwards moe_unsort_rows_grad,
+ * moe_expert_linear_grad_input and _grad_weight, moe_unsort_rows (the gradient
+ * of the sorted rows), moe_topk_route_grad.  moe_sort_rows also carries e4m3
+ * rows, which moe_expert_gate_up and moe_expert_matmul read.  Conventions as
+ * above.
  * ------------------------------------------------------------------------- */
 
 /* Where each (token, k) pair's row lies when pairs are sorted by expert.
