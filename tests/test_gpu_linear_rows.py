@@ -1,6 +1,8 @@
-"""The products on as many rows as the entry points take: an expert with nearly
-2^31 of them, 34 GB of operands, and one with a few.  Whole numbers, so that all
-values are exact."""
+"""Experts that hold nearly all rows: as many as the entry points take (2^31 - 1, 34
+GB of operands), and a few rows per expert of which one has most.  Whole numbers, so
+that all values are exact."""
+import ctypes
+
 import pytest
 
 from tests.gpu_util import say
@@ -81,3 +83,28 @@ def test_longest_sum_of_an_expert():
     assert torch.equal(dw[0].double(), first.T @ first) and torch.equal(db[0].double(), first.sum(0))
     assert torch.equal(dw[-1].double(), last.T @ last) and torch.equal(db[-1].double(), last.sum(0))
     assert not dw[1:-1].any() and not db[1:-1].any()
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts", [[0] * 15 + [112], [110] + [0] * 14 + [1], [1] * 8 + [97] + [1] * 7])
+def test_few_rows_mostly_of_one_expert(counts, kind):
+    """The gradient to the weights of a few rows per expert, by their mean."""
+    E, n, k, rows = len(counts), 2048, 1032, 112
+    say(f"[gpu] gradient to the weights, rows {counts}, {kind}")
+    mep._lib.moe_ops_linear_form.restype = ctypes.c_char_p
+    form = mep._lib.moe_ops_linear_form(3 if kind == torch.float32 else 2, 0, rows, E, n, k, ctypes.byref(ctypes.c_int32(0)))
+    assert form == b"few rows"
+    b = [0]
+    for c in counts:
+        b.append(b[-1] + c)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(11)
+    x, dz = (torch.randint(-3, 4, (rows, c), generator=g, device=DEV).to(BF16) for c in (k, n))
+    x[b[E]:] = dz[b[E]:] = float("nan")
+    dw, db = torch.full((E, n, k), 99.0, device=DEV, dtype=kind), torch.full((E, n), 99.0, device=DEV)
+    ws = torch.empty(max(1, mep.moe_expert_linear_workspace(rows, E, n, k)), dtype=torch.uint8, device=DEV)
+    mep.moe_expert_linear_grad_weight(rows, E, n, k, dz, x, torch.tensor(b, dtype=I32, device=DEV), dw,
+                                      mep.MOE_FP32 if kind == torch.float32 else mep.MOE_BF16, db, ws)
+    for e in range(E):
+        d, u = dz[b[e]:b[e + 1]].double(), x[b[e]:b[e + 1]].double()
+        assert torch.equal(dw[e], (d.T @ u).to(kind)) and torch.equal(db[e].double(), d.sum(0)), e
